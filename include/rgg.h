@@ -395,6 +395,65 @@ rgg_status rgg_grouped_gemm_swiglu_gather(rgg_handle* h, const void* X_tok, int6
                                           const void* W13, const int32_t* group_offsets, void* H, int E,
                                           int64_t M_tot, int K, int N, void* stream, const rgg_options* opt);
 
+/*
+ * rgg_grouped_gemm_dgrad -- the gradient by the activations of rgg_grouped_gemm:
+ *
+ *     dX[i, :] = dY[i, :] . W[e]^T      for every row i of expert e
+ *
+ * dY: bf16 [M_tot, N]; W: bf16 [E, K, N], as the forward call has it; dX: bf16
+ * [M_tot, K], written only on rows some expert owns.  The same kernels, plans,
+ * requirements, options, errors and stream contract as rgg_grouped_gemm, with N
+ * as the reduction and K as the output width (rgg_plan with K and N exchanged
+ * shows the configuration).
+ */
+rgg_status rgg_grouped_gemm_dgrad(rgg_handle* h, const void* dY, const void* W, const int32_t* group_offsets,
+                                  void* dX, int E, int64_t M_tot, int K, int N, void* stream,
+                                  const rgg_options* opt);
+
+/*
+ * rgg_grouped_gemm_swiglu_backward -- the backward pass of
+ * rgg_grouped_gemm_swiglu up to the gate-up product.  Gate g and up u are
+ * computed again from X and W13 (the forward call does not store them); with
+ * s = 1 / (1 + exp(-g)), for 0 <= j < N:
+ *
+ *     dGU[i, j]     = dH[i, j] * u * s * (1 + g * (1 - s))     (gradient by g)
+ *     dGU[i, N + j] = dH[i, j] * g * s                         (gradient by u)
+ *     H[i, j]       = g * s * u                                (if H is not NULL)
+ *
+ * from the fp32 accumulators, each output rounded once to bf16.  dH: bf16
+ * [M_tot, N]; dGU: bf16 [M_tot, 2N]; H: bf16 [M_tot, N] or NULL.  dX is then
+ * rgg_grouped_gemm_dgrad(dGU, W13), dW13 is rgg_grouped_gemm_wgrad(X, dGU), and
+ * the down projection's weight gradient reads H.  Other arguments, options
+ * and errors as for rgg_grouped_gemm_swiglu.
+ */
+rgg_status rgg_grouped_gemm_swiglu_backward(rgg_handle* h, const void* X, const void* W13,
+                                            const int32_t* group_offsets, const void* dH, void* dGU, void* H, int E,
+                                            int64_t M_tot, int K, int N, void* stream, const rgg_options* opt);
+
+/*
+ * rgg_grouped_gemm_wgrad -- the gradient by the weights of rgg_grouped_gemm:
+ *
+ *     dW[e] = X_e^T . dY_e      [K, m_e] x [m_e, N] for every expert e
+ *
+ * X: bf16 [M_tot, K]; dY: bf16 [M_tot, N]; dW: [E, K, N], bf16 (the fp32 sum
+ * rounded once) or fp32 (flag RGG_WGRAD_FP32: the sum itself).  Every element of
+ * dW is written, zeros for an expert without rows; with RGG_WGRAD_ACCUMULATE the
+ * sum is added to what dW holds (in fp32, before any rounding), and an expert
+ * without rows is left alone.  Rows of no expert do not reach any result,
+ * whatever they hold.  The sums' order depends on the sizes only: equal calls
+ * give equal bits.
+ *
+ * The kernel runs on CTA pairs.  Of `opt` it reads bm (0 or 256), bn (0, 128 or
+ * 256), stages (0 or 2..8), max_ctas (0 or at least 2), timeout_ns and
+ * debug_flags.  M_tot may be 0.  Sizes, alignment, errors and the stream
+ * contract as for rgg_grouped_gemm; invalid offsets write nothing.
+ */
+#define RGG_WGRAD_FP32 1
+#define RGG_WGRAD_ACCUMULATE 2
+rgg_status rgg_grouped_gemm_wgrad(rgg_handle* h, const void* X, const void* dY, const int32_t* group_offsets,
+                                  void* dW, int E, int64_t M_tot, int K, int N, int flags, void* stream,
+                                  const rgg_options* opt);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,7 +18,8 @@ import threading
 
 __all__ = [
     "RggError", "rgg_grouped_gemm", "rgg_grouped_gemm_swiglu", "rgg_grouped_gemm_fp8", "rgg_grouped_gemm_gather",
-    "rgg_grouped_gemm_swiglu_gather", "rgg_grouped_gemm_noalloc", "rgg_export_tiles", "rgg_export_walk",
+    "rgg_grouped_gemm_swiglu_gather", "rgg_grouped_gemm_dgrad", "rgg_grouped_gemm_wgrad",
+    "rgg_grouped_gemm_swiglu_backward", "rgg_grouped_gemm_noalloc", "rgg_export_tiles", "rgg_export_walk",
     "rgg_query_status",
     "rgg_plan", "rgg_status_string", "library_path", "load_library", "EXPORTED_SYMBOLS",
     "RGG_OK", "RGG_ERR_INVALID_ARG", "RGG_ERR_UNSUPPORTED", "RGG_ERR_CUDA", "RGG_ERR_BAD_OFFSETS",
@@ -46,6 +47,7 @@ EXPORTED_SYMBOLS = (
     "rgg_create", "rgg_destroy", "rgg_grouped_gemm", "rgg_export_tiles", "rgg_query_status",
     "rgg_plan", "rgg_status_string", "rgg_last_cuda_error", "rgg_grouped_gemm_noalloc", "rgg_grouped_gemm_swiglu",
     "rgg_grouped_gemm_fp8", "rgg_grouped_gemm_gather", "rgg_grouped_gemm_swiglu_gather", "rgg_export_walk",
+    "rgg_grouped_gemm_dgrad", "rgg_grouped_gemm_wgrad", "rgg_grouped_gemm_swiglu_backward",
 )
 
 
@@ -127,6 +129,12 @@ def open_library(path: str) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.argtypes = [P, P, I64, P, P, P, P, I, I64, I, I, P, ctypes.POINTER(_Options)]
         fn.restype = I
+    lib.rgg_grouped_gemm_dgrad.argtypes = [P, P, P, P, P, I, I64, I, I, P, ctypes.POINTER(_Options)]
+    lib.rgg_grouped_gemm_dgrad.restype = I
+    lib.rgg_grouped_gemm_wgrad.argtypes = [P, P, P, P, P, I, I64, I, I, I, P, ctypes.POINTER(_Options)]
+    lib.rgg_grouped_gemm_wgrad.restype = I
+    lib.rgg_grouped_gemm_swiglu_backward.argtypes = [P, P, P, P, P, P, P, I, I64, I, I, P, ctypes.POINTER(_Options)]
+    lib.rgg_grouped_gemm_swiglu_backward.restype = I
     lib.rgg_grouped_gemm_noalloc.argtypes = [P, P, P, P, I, I64, I, I, P, P]
     lib.rgg_grouped_gemm_noalloc.restype = I
     return lib
@@ -410,6 +418,132 @@ def rgg_grouped_gemm_swiglu_gather(X_tok, row_index, W13, group_offsets, H=None,
     return _gather_call("rgg_grouped_gemm_swiglu_gather", X_tok, row_index, W13, group_offsets, H, True, bm, bn,
                         stages, max_ctas, timeout_ns, host_counts, debug_flags, tail64, walk_order, gather_mode,
                         workspace, stream, check)
+
+
+def _check_operands(device, **tensors):
+    """Each tensor: (tensor, dtype, shape); a contiguous CUDA tensor of that type and shape on `device`."""
+    for name, (t, dtype, shape) in tensors.items():
+        if not t.is_cuda or t.device != device:
+            raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+        if t.dtype != dtype:
+            raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+
+
+def _finish(name, status, device, stream_ptr, check):
+    if status != RGG_OK:
+        _raise(status, name)
+    if check:
+        status = load_library().rgg_query_status(_handle(device), stream_ptr)
+        if status != RGG_OK:
+            _raise(status, name + " (device status)")
+
+
+def rgg_grouped_gemm_dgrad(dY, W, group_offsets, dX=None, *, bm=0, bn=0, stages=0, max_ctas=0, timeout_ns=0,
+                           host_counts=None, debug_flags=0, tail64=0, walk_order=0, mixed=0, mixed_pair_sms=0,
+                           pair_min_rows=0, stream=None, check=False):
+    """dX_e = dY_e . W_e^T for every expert: the gradient of ``rgg_grouped_gemm``
+    by its activations.
+
+    dY: bf16 CUDA [M_tot, N]; W: bf16 CUDA [E, K, N] as the forward call has
+    it; group_offsets: int32 CUDA [E+1]; dX: optional bf16 CUDA [M_tot, K]
+    (rows that belong to no expert are never written).  Options as for
+    ``rgg_grouped_gemm``."""
+    import torch
+    if dY.dim() != 2 or W.dim() != 3:
+        raise ValueError("dY must be [M_tot, N] and W [E, K, N]")
+    M_tot = dY.shape[0]
+    E, K, N = W.shape
+    if dX is None:
+        dX = torch.empty(M_tot, K, dtype=torch.bfloat16, device=dY.device)
+    _check_operands(dY.device, dY=(dY, torch.bfloat16, (M_tot, N)), W=(W, torch.bfloat16, (E, K, N)),
+                    group_offsets=(group_offsets, torch.int32, (E + 1,)), dX=(dX, torch.bfloat16, (M_tot, K)))
+    device = dY.device.index
+    opt, keep = _options(bm, bn, stages, max_ctas, timeout_ns, host_counts, debug_flags, tail64, 0, walk_order,
+                         mixed=mixed, mixed_pair_sms=mixed_pair_sms, pair_min_rows=pair_min_rows)
+    st = _stream_ptr(stream, device)
+    s = load_library().rgg_grouped_gemm_dgrad(_handle(device), dY.data_ptr(), W.data_ptr(), group_offsets.data_ptr(),
+                                              dX.data_ptr(), E, M_tot, K, N, st, ctypes.byref(opt))
+    del keep
+    _finish("rgg_grouped_gemm_dgrad", s, device, st, check)
+    return dX
+
+
+def rgg_grouped_gemm_wgrad(X, dY, group_offsets, dW=None, *, dtype=None, accumulate=False, bn=0, stages=0, max_ctas=0,
+                           timeout_ns=0, debug_flags=0, stream=None, check=False):
+    """dW[e] = X_e^T . dY_e for every expert: the gradient of ``rgg_grouped_gemm``
+    by its weights.
+
+    X: bf16 CUDA [M_tot, K]; dY: bf16 CUDA [M_tot, N]; group_offsets: int32
+    CUDA [E+1]; dW: optional CUDA [E, K, N], bf16 or fp32 (allocated in
+    ``dtype``, default bf16, when omitted).  An expert without rows gets
+    zeros.  ``accumulate=True`` adds to what dW holds, in fp32."""
+    import torch
+    if X.dim() != 2 or dY.dim() != 2 or group_offsets.dim() != 1 or group_offsets.numel() < 2:
+        raise ValueError("X must be [M_tot, K], dY [M_tot, N] and group_offsets [E+1]")
+    M_tot, K = X.shape
+    N, E = dY.shape[1], group_offsets.numel() - 1
+    if dtype is None:
+        dtype = torch.bfloat16 if dW is None else dW.dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("dW must be bf16 or fp32, not %s" % dtype)
+    if dW is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs dW")
+        dW = torch.empty(E, K, N, dtype=dtype, device=X.device)
+    _check_operands(X.device, X=(X, torch.bfloat16, (M_tot, K)), dY=(dY, torch.bfloat16, (M_tot, N)),
+                    group_offsets=(group_offsets, torch.int32, (E + 1,)), dW=(dW, dtype, (E, K, N)))
+    device = X.device.index
+    opt, _ = _options(0, bn, stages, max_ctas, timeout_ns, None, debug_flags)
+    st = _stream_ptr(stream, device)
+    flags = (1 if dtype == torch.float32 else 0) | (2 if accumulate else 0)
+    s = load_library().rgg_grouped_gemm_wgrad(_handle(device), X.data_ptr(), dY.data_ptr(), group_offsets.data_ptr(),
+                                              dW.data_ptr(), E, M_tot, K, N, flags, st, ctypes.byref(opt))
+    _finish("rgg_grouped_gemm_wgrad", s, device, st, check)
+    return dW
+
+
+def rgg_grouped_gemm_swiglu_backward(X, W13, group_offsets, dH, dGU=None, H=None, *, bm=0, bn=0, stages=0, max_ctas=0,
+                                     timeout_ns=0, host_counts=None, debug_flags=0, tail64=0, walk_order=0, mixed=0,
+                                     mixed_pair_sms=0, pair_min_rows=0, stream=None, check=False):
+    """The backward pass of ``rgg_grouped_gemm_swiglu`` up to the gate-up product,
+    which is computed again from X and W13.
+
+    X: bf16 CUDA [M_tot, K]; W13: bf16 CUDA [E, K, 2N] (gate columns first);
+    group_offsets: int32 CUDA [E+1]; dH: bf16 CUDA [M_tot, N].  Returns
+    ``(dGU, H)``: the gradient by [gate | up], bf16 [M_tot, 2N], and the
+    activation H, bf16 [M_tot, N], that the down projection's weight gradient
+    reads (both optional arguments; ``H=False`` leaves H out)."""
+    import torch
+    if X.dim() != 2 or W13.dim() != 3 or W13.shape[2] % 2 != 0:
+        raise ValueError("X must be [M_tot, K] and W13 [E, K, 2N]")
+    M_tot, K = X.shape
+    E, N = W13.shape[0], W13.shape[2] // 2
+    if dGU is None:
+        dGU = torch.empty(M_tot, 2 * N, dtype=torch.bfloat16, device=X.device)
+    if H is None:
+        H = torch.empty(M_tot, N, dtype=torch.bfloat16, device=X.device)
+    elif H is False:
+        H = None
+    operands = dict(X=(X, torch.bfloat16, (M_tot, K)), W13=(W13, torch.bfloat16, (E, K, 2 * N)),
+                    group_offsets=(group_offsets, torch.int32, (E + 1,)), dH=(dH, torch.bfloat16, (M_tot, N)),
+                    dGU=(dGU, torch.bfloat16, (M_tot, 2 * N)))
+    if H is not None:
+        operands["H"] = (H, torch.bfloat16, (M_tot, N))
+    _check_operands(X.device, **operands)
+    device = X.device.index
+    opt, keep = _options(bm, bn, stages, max_ctas, timeout_ns, host_counts, debug_flags, tail64, 0, walk_order,
+                         mixed=mixed, mixed_pair_sms=mixed_pair_sms, pair_min_rows=pair_min_rows)
+    st = _stream_ptr(stream, device)
+    s = load_library().rgg_grouped_gemm_swiglu_backward(
+        _handle(device), X.data_ptr(), W13.data_ptr(), group_offsets.data_ptr(), dH.data_ptr(), dGU.data_ptr(),
+        H.data_ptr() if H is not None else None, E, M_tot, K, N, st, ctypes.byref(opt))
+    del keep
+    _finish("rgg_grouped_gemm_swiglu_backward", s, device, st, check)
+    return dGU, H
 
 
 def rgg_export_tiles(group_offsets, M_tot: int, N: int, bm: int, bn: int, cap: int | None = None, stream=None):

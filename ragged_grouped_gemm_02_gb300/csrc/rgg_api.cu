@@ -17,6 +17,7 @@
 #include <string>
 
 #include "rgg.h"
+#include "rgg_host.h"
 #include "rgg_internal.h"
 
 struct rgg_handle {
@@ -32,30 +33,14 @@ thread_local std::string g_last_cuda_error;
 
 constexpr int kDefaultSms = 152;
 constexpr int kDefaultSmemOptin = 232448;
-constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+constexpr uint64_t kDefaultTimeoutNs = rgg::kHostDefaultTimeoutNs;
 
 rgg_status cuda_failure(cudaError_t err, const char* what) {
     g_last_cuda_error = std::string(what) + ": " + cudaGetErrorName(err) + " (" + cudaGetErrorString(err) + ")";
     return RGG_ERR_CUDA;
 }
 
-// Makes `device` current for the scope of a call and restores the caller's.
-class DeviceScope {
-public:
-    explicit DeviceScope(int device) {
-        if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = -1;
-        if (prev_ != device) err_ = cudaSetDevice(device);
-    }
-    ~DeviceScope() {
-        int cur = -1;
-        if (prev_ >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev_) cudaSetDevice(prev_);
-    }
-    cudaError_t error() const { return err_; }
-
-private:
-    int prev_ = -1;
-    cudaError_t err_ = cudaSuccess;
-};
+using DeviceScope = rgg::HostDeviceScope;
 
 using EncodeTiledFn = decltype(&cuTensorMapEncodeTiled);
 
@@ -73,7 +58,7 @@ EncodeTiledFn encode_tiled_fn() {
     return fn;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool aligned(const void* p, uintptr_t a) { return rgg::host_aligned(p, a); }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -456,8 +441,10 @@ rgg_status choose_gather_mode(int E, int64_t M_tot, const rgg_options* opt, int*
     return RGG_OK;
 }
 
+// `trans_w`: W is [E, N, K] (the transposed product, K contiguous); the box
+// is then 64 K elements by 64 rows.
 rgg_status encode_maps(const void* X, const void* W, int E, int64_t M_tot, int K, int N, int bm,
-                       CUtensorMap* tx, CUtensorMap* tx64, CUtensorMap* tw) {
+                       CUtensorMap* tx, CUtensorMap* tx64, CUtensorMap* tw, bool trans_w = false) {
     EncodeTiledFn encode = encode_tiled_fn();
     if (!encode) {
         g_last_cuda_error = "cuTensorMapEncodeTiled is not available from the driver";
@@ -489,9 +476,10 @@ rgg_status encode_maps(const void* X, const void* W, int E, int64_t M_tot, int K
     }
     // W: 3-D {N, K, E}, box {64, 64, 1}: one 64-column panel of 64 K rows.
     {
-        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(K),
+        const int inner = trans_w ? K : N, outer = trans_w ? N : K;
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
                                     static_cast<cuuint64_t>(E)};
-        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(N) * 2, static_cast<cuuint64_t>(N) * K * 2};
+        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner) * 2, static_cast<cuuint64_t>(N) * K * 2};
         const cuuint32_t box[3] = {64, 64, 1};
         const cuuint32_t estr[3] = {1, 1, 1};
         CUresult r = encode(tw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(W), dims, strides, box, estr,
@@ -571,6 +559,12 @@ rgg_status gather_call(rgg_handle* h, const void* X_tok, int64_t T, const int32_
                        const int32_t* group_offsets, void* Y, int E, int64_t M_tot, int K, int N, void* stream,
                        const rgg_options* opt, bool swiglu);
 
+// The fused gate-up projection (out = H) or its backward pass (out = dGU, `act`
+// = H or null).
+rgg_status swiglu_call(rgg_handle* h, const void* X, const void* W13, const int32_t* group_offsets, const void* dH,
+                       void* out, void* act, int E, int64_t M_tot, int K, int N, void* stream, const rgg_options* opt,
+                       bool backward);
+
 }  // namespace
 
 namespace rgg {
@@ -579,6 +573,28 @@ namespace rgg {
 rgg_status host_cuda_failure(cudaError_t err, const char* what) { return cuda_failure(err, what); }
 
 void host_set_last_error(const char* what) { g_last_cuda_error = what; }
+
+HostDevice host_device(const rgg_handle* h) { return HostDevice{h->device, h->num_sms, h->smem_optin, h->d_status}; }
+
+rgg_status host_check_sizes(int E, int64_t M_tot, int K, int N) { return check_sizes(E, M_tot, K, N); }
+
+rgg_status host_encode_rows(const void* p, int64_t rows, int cols, int box_rows, CUtensorMap* map) {
+    EncodeTiledFn encode = encode_tiled_fn();
+    if (!encode) {
+        g_last_cuda_error = "cuTensorMapEncodeTiled is not available from the driver";
+        return RGG_ERR_CUDA;
+    }
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return RGG_OK;
+    g_last_cuda_error = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(static_cast<int>(r));
+    return RGG_ERR_CUDA;
+}
 
 rgg_status host_check_gemm_args(const void* X, const void* W, const int32_t* group_offsets, const void* Y, int E,
                                 int64_t M_tot, int K, int N) {
@@ -593,7 +609,7 @@ rgg_status host_check_gemm_args(const void* X, const void* W, const int32_t* gro
 
 rgg_status host_grouped_gemm(int num_sms, int smem_optin, int32_t* status, const void* X, const void* W,
                              const int32_t* group_offsets, void* Y, int E, int64_t M_tot, int K, int N,
-                             cudaStream_t st, const rgg_options* opt) {
+                             cudaStream_t st, const rgg_options* opt, bool trans_w) {
     if (M_tot == 0) {
         cudaError_t err = launch_validate_offsets(group_offsets, E, M_tot, status, st);
         return err == cudaSuccess ? RGG_OK : cuda_failure(err, "validate_offsets launch");
@@ -602,7 +618,7 @@ rgg_status host_grouped_gemm(int num_sms, int smem_optin, int32_t* status, const
     rgg_status s = make_plan(num_sms, smem_optin, E, M_tot, K, N, opt, &p, 0);
     if (s != RGG_OK) return s;
     CUtensorMap tx, tx64, tw;
-    s = encode_maps(X, W, E, M_tot, K, N, p.bm, &tx, &tx64, &tw);
+    s = encode_maps(X, W, E, M_tot, K, N, p.bm, &tx, &tx64, &tw, trans_w);
     if (s != RGG_OK) return s;
     GemmArgs a;
     a.offsets = group_offsets;
@@ -633,8 +649,8 @@ rgg_status host_grouped_gemm(int num_sms, int smem_optin, int32_t* status, const
         a.split_sms = p.split_sms;
         GemmArgs as = a;
         as.stages = p.single_stages;
-        cudaError_t err = launch_gemm_mixed(p.grid, p.smem_bytes, a, p.single_grid, p.single_smem, as, st, tx, tx64,
-                                            tw);
+        auto launch = trans_w ? launch_gemm_mixed_dgrad : launch_gemm_mixed;
+        cudaError_t err = launch(p.grid, p.smem_bytes, a, p.single_grid, p.single_smem, as, st, tx, tx64, tw);
         if (err != cudaSuccess) {
             // a kernel that did launch still counts its CTAs: zero the counters behind it
             cudaMemsetAsync(a.sched, 0, 3 * sizeof(int32_t), st);
@@ -642,7 +658,8 @@ rgg_status host_grouped_gemm(int num_sms, int smem_optin, int32_t* status, const
         }
         return RGG_OK;
     }
-    cudaError_t err = (p.bm == 256)   ? launch_gemm_pair(p.bn, p.grid, p.smem_bytes, st, tx, tx64, tw, a)
+    cudaError_t err = trans_w         ? launch_gemm_dgrad(p.bm, p.bn, p.grid, p.smem_bytes, st, tx, tx64, tw, a)
+                      : (p.bm == 256) ? launch_gemm_pair(p.bn, p.grid, p.smem_bytes, st, tx, tx64, tw, a)
                       : (p.bm == 128) ? launch_gemm_bm128(p.bn, p.grid, p.smem_bytes, st, tx, tx64, tw, a)
                                       : launch_gemm_bm64(p.bn, p.grid, p.smem_bytes, st, tx, tx64, tw, a);
     return err == cudaSuccess ? RGG_OK : cuda_failure(err, "grouped_gemm launch");
@@ -776,69 +793,28 @@ rgg_status rgg_grouped_gemm(rgg_handle* h, const void* X, const void* W, const i
                                   static_cast<cudaStream_t>(stream), opt);
 }
 
+rgg_status rgg_grouped_gemm_dgrad(rgg_handle* h, const void* dY, const void* W, const int32_t* group_offsets, void* dX,
+                                  int E, int64_t M_tot, int K, int N, void* stream, const rgg_options* opt) {
+    if (!h) return RGG_ERR_INVALID_ARG;
+    // the product dY . W^T: N is its reduction and K its output width
+    rgg_status s = rgg::host_check_gemm_args(dY, W, group_offsets, dX, E, M_tot, N, K);
+    if (s != RGG_OK) return s;
+    DeviceScope scope(h->device);
+    if (scope.error() != cudaSuccess) return cuda_failure(scope.error(), "cudaSetDevice");
+    return rgg::host_grouped_gemm(h->num_sms, h->smem_optin, h->d_status, dY, W, group_offsets, dX, E, M_tot, N, K,
+                                  static_cast<cudaStream_t>(stream), opt, true);
+}
+
 rgg_status rgg_grouped_gemm_swiglu(rgg_handle* h, const void* X, const void* W13, const int32_t* group_offsets,
                                    void* H, int E, int64_t M_tot, int K, int N, void* stream,
                                    const rgg_options* opt) {
-    if (!h || !group_offsets || !W13) return RGG_ERR_INVALID_ARG;
-    rgg_status s = check_sizes(E, M_tot, K, N);
-    if (s != RGG_OK) return s;
-    if (N > (1 << 30)) return RGG_ERR_INVALID_ARG;
-    if (M_tot > 0 && (!X || !H)) return RGG_ERR_INVALID_ARG;
-    if (!aligned(W13, 16) || !aligned(group_offsets, 4) || (M_tot > 0 && (!aligned(X, 16) || !aligned(H, 16))))
-        return RGG_ERR_INVALID_ARG;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    DeviceScope scope(h->device);
-    if (scope.error() != cudaSuccess) return cuda_failure(scope.error(), "cudaSetDevice");
-    if (M_tot == 0) {
-        cudaError_t err = rgg::launch_validate_offsets(group_offsets, E, M_tot, h->d_status, st);
-        return err == cudaSuccess ? RGG_OK : cuda_failure(err, "validate_offsets launch");
-    }
-    Plan p;
-    s = make_plan(h->num_sms, h->smem_optin, E, M_tot, K, 2 * N, opt, &p, kPlanNoBn192);
-    if (s != RGG_OK) return s;
-    CUtensorMap tx, tx64, tw;
-    s = encode_maps(X, W13, E, M_tot, K, 2 * N, p.bm, &tx, &tx64, &tw);
-    if (s != RGG_OK) return s;
-    rgg::GemmArgs a;
-    a.offsets = group_offsets;
-    a.Y = static_cast<__nv_bfloat16*>(H);
-    a.status = h->d_status;
-    a.M_tot = M_tot;
-    a.E = E;
-    a.K = K;
-    a.N = N;  // output columns; the gate / up split of W13 is at column N
-    a.num_k_blocks = static_cast<int32_t>(ceil_div(K, rgg::kBK));
-    a.n_tiles_n = static_cast<int32_t>(ceil_div(N, p.bn / 2));
-    a.stages = p.stages;
-    a.y_vec32 = ((N % 16) == 0 && aligned(H, 32)) ? 1 : 0;
-    a.timeout_ns = (opt && opt->timeout_ns) ? opt->timeout_ns : kDefaultTimeoutNs;
-    a.debug_flags = opt ? (opt->debug_flags & RGG_DEBUG_PRODUCER_STALL) : 0;
-    a.tail64 = p.tail64;
-    a.walk_order = p.walk_order;
-    if (p.mixed) {
-        // as for rgg_grouped_gemm's mixed launch
-        a.sched = h->d_status + 16;
-        a.sched_total = p.grid + p.single_grid;
-        a.sched_pairs = p.grid / 2;
-        a.sched_singles = p.single_grid;
-        a.sched_claims = (p.mixed == 1) ? 1 : 0;
-        a.pair_min_rows = p.pair_min_rows;
-        a.sched_split = p.device_split;
-        a.split_sms = p.split_sms;
-        rgg::GemmArgs as = a;
-        as.stages = p.single_stages;
-        cudaError_t err = rgg::launch_gemm_mixed_swiglu(p.grid, p.smem_bytes, a, p.single_grid, p.single_smem, as, st,
-                                                        tx, tx64, tw);
-        if (err != cudaSuccess) {
-            cudaMemsetAsync(a.sched, 0, 3 * sizeof(int32_t), st);
-            return cuda_failure(err, "grouped_gemm_swiglu (mixed) launch");
-        }
-        return RGG_OK;
-    }
-    if (p.bm == 256 && p.bn != 256) a.tail64 = 0;  // 128-column pairs: a 64-column panel cannot hold gate and up
-    cudaError_t err = (p.bm == 256) ? rgg::launch_gemm_pair_swiglu(p.bn, p.grid, p.smem_bytes, st, tx, tx64, tw, a)
-                                    : rgg::launch_gemm_swiglu(p.bm, p.bn, p.grid, p.smem_bytes, st, tx, tx64, tw, a);
-    return err == cudaSuccess ? RGG_OK : cuda_failure(err, "grouped_gemm_swiglu launch");
+    return swiglu_call(h, X, W13, group_offsets, nullptr, H, nullptr, E, M_tot, K, N, stream, opt, false);
+}
+
+rgg_status rgg_grouped_gemm_swiglu_backward(rgg_handle* h, const void* X, const void* W13,
+                                            const int32_t* group_offsets, const void* dH, void* dGU, void* H, int E,
+                                            int64_t M_tot, int K, int N, void* stream, const rgg_options* opt) {
+    return swiglu_call(h, X, W13, group_offsets, dH, dGU, H, E, M_tot, K, N, stream, opt, true);
 }
 
 rgg_status rgg_grouped_gemm_fp8(rgg_handle* h, const void* X8, const void* W8, const float* sx, const float* sw,
@@ -1011,6 +987,75 @@ rgg_status gather_call(rgg_handle* h, const void* X_tok, int64_t T, const int32_
     a.t_rows = static_cast<int32_t>(T);
     cudaError_t err = rgg::launch_gemm_gather(swiglu, p.bm, p.bn, p.grid, p.smem_bytes, st, tx, tw, a);
     return err == cudaSuccess ? RGG_OK : cuda_failure(err, "grouped_gemm_gather launch");
+}
+
+rgg_status swiglu_call(rgg_handle* h, const void* X, const void* W13, const int32_t* group_offsets, const void* dH,
+                       void* out, void* act, int E, int64_t M_tot, int K, int N, void* stream, const rgg_options* opt,
+                       bool backward) {
+    if (!h || !group_offsets || !W13) return RGG_ERR_INVALID_ARG;
+    rgg_status s = check_sizes(E, M_tot, K, N);
+    if (s != RGG_OK) return s;
+    if (N > (1 << 30)) return RGG_ERR_INVALID_ARG;
+    if (M_tot > 0 && (!X || !out || (backward && !dH))) return RGG_ERR_INVALID_ARG;
+    if (!aligned(W13, 16) || !aligned(group_offsets, 4) ||
+        (M_tot > 0 && (!aligned(X, 16) || !aligned(out, 16) || !aligned(dH, 16) || !aligned(act, 16))))
+        return RGG_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    DeviceScope scope(h->device);
+    if (scope.error() != cudaSuccess) return cuda_failure(scope.error(), "cudaSetDevice");
+    if (M_tot == 0) {
+        cudaError_t err = rgg::launch_validate_offsets(group_offsets, E, M_tot, h->d_status, st);
+        return err == cudaSuccess ? RGG_OK : cuda_failure(err, "validate_offsets launch");
+    }
+    Plan p;
+    s = make_plan(h->num_sms, h->smem_optin, E, M_tot, K, 2 * N, opt, &p, kPlanNoBn192);
+    if (s != RGG_OK) return s;
+    CUtensorMap tx, tx64, tw;
+    s = encode_maps(X, W13, E, M_tot, K, 2 * N, p.bm, &tx, &tx64, &tw);
+    if (s != RGG_OK) return s;
+    rgg::GemmArgs a;
+    a.offsets = group_offsets;
+    a.Y = static_cast<__nv_bfloat16*>(out);
+    a.dH = static_cast<const __nv_bfloat16*>(dH);
+    a.act = static_cast<__nv_bfloat16*>(act);
+    a.status = h->d_status;
+    a.M_tot = M_tot;
+    a.E = E;
+    a.K = K;
+    a.N = N;  // output columns; the gate / up split of W13 is at column N
+    a.num_k_blocks = static_cast<int32_t>(ceil_div(K, rgg::kBK));
+    a.n_tiles_n = static_cast<int32_t>(ceil_div(N, p.bn / 2));
+    a.stages = p.stages;
+    a.y_vec32 = ((N % 16) == 0 && aligned(out, 32)) ? 1 : 0;
+    a.timeout_ns = (opt && opt->timeout_ns) ? opt->timeout_ns : kDefaultTimeoutNs;
+    a.debug_flags = opt ? (opt->debug_flags & RGG_DEBUG_PRODUCER_STALL) : 0;
+    a.tail64 = p.tail64;
+    a.walk_order = p.walk_order;
+    if (p.mixed) {
+        // as for rgg_grouped_gemm's mixed launch
+        a.sched = h->d_status + 16;
+        a.sched_total = p.grid + p.single_grid;
+        a.sched_pairs = p.grid / 2;
+        a.sched_singles = p.single_grid;
+        a.sched_claims = (p.mixed == 1) ? 1 : 0;
+        a.pair_min_rows = p.pair_min_rows;
+        a.sched_split = p.device_split;
+        a.split_sms = p.split_sms;
+        rgg::GemmArgs as = a;
+        as.stages = p.single_stages;
+        auto launch = backward ? rgg::launch_gemm_mixed_swiglu_bwd : rgg::launch_gemm_mixed_swiglu;
+        cudaError_t err = launch(p.grid, p.smem_bytes, a, p.single_grid, p.single_smem, as, st, tx, tx64, tw);
+        if (err != cudaSuccess) {
+            cudaMemsetAsync(a.sched, 0, 3 * sizeof(int32_t), st);
+            return cuda_failure(err, "grouped_gemm_swiglu (mixed) launch");
+        }
+        return RGG_OK;
+    }
+    if (p.bm == 256 && p.bn != 256) a.tail64 = 0;  // 128-column pairs: a 64-column panel cannot hold gate and up
+    cudaError_t err = backward        ? rgg::launch_gemm_swiglu_bwd(p.bm, p.bn, p.grid, p.smem_bytes, st, tx, tx64, tw, a)
+                      : (p.bm == 256) ? rgg::launch_gemm_pair_swiglu(p.bn, p.grid, p.smem_bytes, st, tx, tx64, tw, a)
+                                      : rgg::launch_gemm_swiglu(p.bm, p.bn, p.grid, p.smem_bytes, st, tx, tx64, tw, a);
+    return err == cudaSuccess ? RGG_OK : cuda_failure(err, "grouped_gemm_swiglu launch");
 }
 
 }  // namespace

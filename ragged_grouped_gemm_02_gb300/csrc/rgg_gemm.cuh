@@ -84,6 +84,8 @@ struct GemmArgs {
     const float* sw = nullptr;  // FP8 kernels: fp32 scale of each (expert, column) of W [E, N]
     const int32_t* row_index = nullptr;  // gather kernels: token row of each routed row [M_tot]
     int32_t t_rows = 0;                  // gather kernels: rows of the token matrix
+    const __nv_bfloat16* dH = nullptr;   // gate-up backward: gradient by H [M_tot, N] (Y is then dGU [M_tot, 2N])
+    __nv_bfloat16* act = nullptr;        // gate-up backward: H [M_tot, N], or null
     // Mixed launch (rgg_sched.cuh): tiles claimed from two device counters
     // sched[0] (class P) and sched[1] (class S); sched[2] counts finished CTAs
     // of the sched_total CTAs of both kernels (the last one resets all three).
@@ -208,8 +210,8 @@ struct TileConfig {
     static constexpr uint32_t kBStep = kFp8 ? 4096u : 2048u;  // B start advance per MMA (32 or 16 K rows)
     static constexpr uint32_t kTmemCols = (2 * BN <= 256) ? 256u : 512u;  // two accumulator buffers
     // Instruction descriptor for an M x n MMA (n = the panels a tile loads x kPanelN).
-    __host__ __device__ static constexpr uint32_t idesc(int m, int n) {
-        return kFp8 ? idesc_e4m3_f32(m, n, true) : idesc_bf16_f32(m, n, true);
+    __host__ __device__ static constexpr uint32_t idesc(int m, int n, bool b_mn_major = true) {
+        return kFp8 ? idesc_e4m3_f32(m, n, b_mn_major) : idesc_bf16_f32(m, n, b_mn_major);
     }
 };
 
@@ -228,9 +230,15 @@ __device__ __forceinline__ bool runs_as_64_rows(const GemmArgs& args, const Tile
 // gate-up projection: W holds 2N columns (gate [0, N), up [N, 2N)); a tile of
 // BN/2 output columns loads the matching BN/2 gate and BN/2 up columns into one
 // B stage, one MMA of width BN puts gate | up side by side in TMEM, and the
-// epilogue writes silu(gate) * up.
+// epilogue writes silu(gate) * up.  kEpiSwiGLUBwd is the backward pass of that
+// op on the same tiles: gate and up are computed again and the epilogue turns
+// them and dH into the gradient [dGate | dUp] and the activation H.
 constexpr int kEpiPlain = 0;
 constexpr int kEpiSwiGLU = 1;
+constexpr int kEpiSwiGLUBwd = 2;
+
+// Tiles that load matching gate and up columns.
+__host__ __device__ constexpr bool epi_gate_up(int epi) { return epi != kEpiPlain; }
 
 // Weight panels a tile loads and multiplies.  A plain tile whose columns run
 // past N (the last N tile of an expert) loads only the panels that hold
@@ -256,7 +264,7 @@ __device__ __forceinline__ int tile_panels(int32_t col0, int32_t N) {
 // same split lost 3-5 %.
 template <int kEpi, bool kFp8>
 __host__ __device__ constexpr int epilogue_warps() {
-    return (kFp8 || kEpi == kEpiSwiGLU) ? 8 : 4;
+    return (kFp8 || epi_gate_up(kEpi)) ? 8 : 4;
 }
 template <int kEpi, bool kFp8>
 __host__ __device__ constexpr int cta_threads() {
@@ -264,6 +272,52 @@ __host__ __device__ constexpr int cta_threads() {
 }
 
 __device__ __forceinline__ float silu_f32(float z) { return z / (1.0f + __expf(-z)); }
+
+// The gate-up backward for 32 columns of one row (gate and up accumulators in
+// v and u, first output column `col`): with s = 1 / (1 + exp(-g)),
+//     dG = dH * u * s * (1 + g * (1 - s)),  dU = dH * g * s,  H = g * s * u,
+// in fp32 from the unrounded accumulators, each rounded once to bf16.  dH is
+// read 8 columns (16 bytes) at a time, the granule N is a multiple of.
+__device__ __forceinline__ void store_swiglu_backward(const GemmArgs& args, int64_t row, int col,
+                                                      const uint32_t (&v)[32], const uint32_t (&u)[32], int32_t row_lo,
+                                                      int32_t row_hi) {
+    const int N = args.N;
+    const __nv_bfloat16* dh = args.dH + row * N + col;
+    __nv_bfloat16* dg_out = args.Y + row * (2 * static_cast<int64_t>(N)) + col;
+    __nv_bfloat16* act_out = args.act ? args.act + row * N + col : nullptr;
+    uint4 d4[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        d4[q] = (col + 8 * q < N) ? __ldg(reinterpret_cast<const uint4*>(dh + 8 * q)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (col + 8 * q >= N) break;
+        if (!RGG_BOUNDS_OK(store_ok(row, col + 8 * q, 8, row_lo, row_hi, N), args.status)) break;
+        const uint32_t dw[4] = {d4[q].x, d4[q].y, d4[q].z, d4[q].w};
+        uint32_t wg[4], wu[4], wh[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float dg[2], du[2], h[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float g = __uint_as_float(v[8 * q + 2 * i + j]);
+                const float up = __uint_as_float(u[8 * q + 2 * i + j]);
+                const float d = __uint_as_float(j ? (dw[i] & 0xffff0000u) : (dw[i] << 16));
+                const float s = __fdividef(1.0f, 1.0f + __expf(-g));
+                const float gs = g * s;
+                h[j] = gs * up;
+                du[j] = d * gs;
+                dg[j] = d * up * s * (1.0f + (g - gs));
+            }
+            wg[i] = pack_bf16x2(__float_as_uint(dg[0]), __float_as_uint(dg[1]));
+            wu[i] = pack_bf16x2(__float_as_uint(du[0]), __float_as_uint(du[1]));
+            wh[i] = pack_bf16x2(__float_as_uint(h[0]), __float_as_uint(h[1]));
+        }
+        st_global_v4(dg_out + 8 * q, wg[0], wg[1], wg[2], wg[3]);
+        st_global_v4(dg_out + N + 8 * q, wu[0], wu[1], wu[2], wu[3]);
+        if (act_out) st_global_v4(act_out + 8 * q, wh[0], wh[1], wh[2], wh[3]);
+    }
+}
 
 // Epilogue of one finished accumulator buffer of a 1-CTA tile, for one
 // epilogue warp: lane `lane` of the warp holds tile row r_local (TMEM row
@@ -279,7 +333,7 @@ template <int BN, int kEpi, bool kFp8>
 __device__ __forceinline__ void epilogue_store_tile(const GemmArgs& args, const TileCoord& c, bool half, int r_local,
                                                     uint32_t t_row, int lane, int cc0, bool store, int32_t row_lo,
                                                     int32_t row_hi, uint32_t tcol) {
-    constexpr int kOutN = (kEpi == kEpiSwiGLU) ? BN / 2 : BN;
+    constexpr int kOutN = epi_gate_up(kEpi) ? BN / 2 : BN;
     constexpr int kPartCols = kOutN / (epilogue_warps<kEpi, kFp8>() / 4);
     constexpr uint32_t kTmemCols = TileConfig<64, BN, kFp8>::kTmemCols;
     const int N = args.N;
@@ -292,7 +346,7 @@ __device__ __forceinline__ void epilogue_store_tile(const GemmArgs& args, const 
         uint32_t v[32];
         const bool ld_ok = RGG_BOUNDS_OK(tmem_cols_ok(tcol + cc, 32, kTmemCols), args.status);
         if (ld_ok) tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(cc), v);
-        if (kEpi == kEpiSwiGLU) {
+        if constexpr (epi_gate_up(kEpi)) {
             // gate in columns [cc, cc+32), up in [kOutN + cc, kOutN + cc + 32)
             uint32_t u[32];
             const bool ldu_ok = RGG_BOUNDS_OK(tmem_cols_ok(tcol + kOutN + cc, 32, kTmemCols), args.status);
@@ -302,9 +356,13 @@ __device__ __forceinline__ void epilogue_store_tile(const GemmArgs& args, const 
                 for (int i = 0; i < 32; ++i) u[i] = 0u;
             if (!ld_ok)
                 for (int i = 0; i < 32; ++i) v[i] = 0u;
+            if constexpr (kEpi == kEpiSwiGLUBwd) {
+                if (row_ok) store_swiglu_backward(args, row, c.col0 + cc, v, u, row_lo, row_hi);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                v[i] = __float_as_uint(silu_f32(__uint_as_float(v[i])) * __uint_as_float(u[i]));
+                for (int i = 0; i < 32; ++i)
+                    v[i] = __float_as_uint(silu_f32(__uint_as_float(v[i])) * __uint_as_float(u[i]));
+            }
         } else {
             tmem_ld_wait();
             if (!ld_ok)
@@ -332,7 +390,7 @@ __device__ __forceinline__ void epilogue_store_tile(const GemmArgs& args, const 
                 }
             }
         }
-        if (row_ok) {
+        if (kEpi != kEpiSwiGLUBwd && row_ok) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int col = c.col0 + cc + 16 * h;
@@ -375,7 +433,14 @@ constexpr int kGatherTma = 1;
 // the MMA thread and the epilogue warps through a small shared-memory queue
 // (q_full / q_empty barriers per slot); a descriptor with expert -1 ends the
 // walk.  Otherwise each role decodes the static walk t = cta, cta + grid, ...
-template <int BM, int BN, int kEpi = kEpiPlain, bool kFp8 = false, int kGather = kGatherNone, bool kDyn = false>
+//
+// kTransW: Y_e = X_e . W_e^T, the gradient by the activations (dX = dY . W^T).
+// W stays as it lies, [E, N, K] in the kernel's terms (K, the reduction, is
+// contiguous): a panel is then 64 rows of W by 64 K elements, the K-major
+// form of B, whose K step of 16 is +32 B as for A.  Panels, bytes and stages
+// are the same.
+template <int BM, int BN, int kEpi = kEpiPlain, bool kFp8 = false, int kGather = kGatherNone, bool kDyn = false,
+          bool kTransW = false>
 __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_x64,
                         const __grid_constant__ CUtensorMap tmap_w, const GemmArgs args) {
@@ -383,21 +448,23 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
     static_assert(!kDyn || (BM == 128 && BN == kMixedBN && !kFp8 && kGather == kGatherNone),
                   "the mixed launch's 1-CTA kernel runs bf16 128 x 256 tiles (plain or fused gate-up)");
     static_assert(kEpi == kEpiPlain || (BN % 128) == 0, "fused gate-up tiles hold whole gate and up panels");
-    static_assert(!(kFp8 && kEpi == kEpiSwiGLU), "the fused gate-up epilogue is bf16 only");
+    static_assert(!(kFp8 && epi_gate_up(kEpi)), "the fused gate-up epilogue is bf16 only");
+    static_assert(!kTransW || (kEpi == kEpiPlain && !kFp8 && kGather == kGatherNone),
+                  "the transposed product is the plain bf16 one");
     static_assert(!(kFp8 && kGather != kGatherNone), "the token gather is bf16 only");
     static_assert(BM / 4 <= 32, "one producer lane per group of four tile rows");
-    constexpr int kOutN = (kEpi == kEpiSwiGLU) ? BN / 2 : BN;  // output columns per tile
+    constexpr int kOutN = epi_gate_up(kEpi) ? BN / 2 : BN;  // output columns per tile
     constexpr int kPanels = BN / Cfg::kPanelN;
     constexpr int kElemBytes = kFp8 ? 1 : 2;
-    const int64_t kNw = (kEpi == kEpiSwiGLU) ? 2 * static_cast<int64_t>(args.N) : args.N;  // columns of W
+    const int64_t kNw = epi_gate_up(kEpi) ? 2 * static_cast<int64_t>(args.N) : args.N;  // columns of W
     (void)kNw;
     // A plain tile loads only panels below N (tile_panels); the fused gate-up
     // tile's last up panel of an expert's last N tile can start past column
     // 2N, a box the copy zero-fills.
-    constexpr int64_t kWOverhang = (kEpi == kEpiSwiGLU) ? Cfg::kPanelN : 0;
+    constexpr int64_t kWOverhang = epi_gate_up(kEpi) ? Cfg::kPanelN : 0;
     // Column of W read by B panel p of a tile whose first output column is col0.
     auto w_col = [&](int32_t col0, int p) -> int32_t {
-        if (kEpi == kEpiSwiGLU)
+        if (epi_gate_up(kEpi))
             return (p < kPanels / 2) ? col0 + Cfg::kPanelN * p : args.N + col0 + Cfg::kPanelN * (p - kPanels / 2);
         return col0 + Cfg::kPanelN * p;
     };
@@ -456,7 +523,7 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
         if (warp == 0) build_class_prefix_warp(s_off, s_pre, E, 256, args.n_tiles_n, args.pair_min_rows, 0x7fffffff);
         if (warp == 1) build_class_prefix_warp(s_off, s_order, E, 128, args.n_tiles_n, 0, args.pair_min_rows);
         if (warp == 2 && args.sched_split) {
-            const int ps = mixed_pair_sms_from_offsets(s_off, E, kEpi == kEpiSwiGLU ? 2 * args.N : args.N,
+            const int ps = mixed_pair_sms_from_offsets(s_off, E, epi_gate_up(kEpi) ? 2 * args.N : args.N,
                                                        args.pair_min_rows, args.split_sms);
             if (lane == 0) misc[2] = static_cast<uint32_t>(ps);
         }
@@ -654,12 +721,21 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
                                       args.status))
                         tma_load_2d(a0 + st * sp.a_stage, xmap, full_bar(st), kb * Cfg::kKStage, c.row0);
 #pragma unroll
-                    for (int p = 0; p < kPanels; ++p)
-                        if (p < np && RGG_BOUNDS_OK(w_box_ok(w_col(c.col0, p), kb * Cfg::kKStage, c.expert, kNw,
-                                                             args.K, E, kElemBytes, kWOverhang),
-                                                    args.status))
-                            tma_load_3d(b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w, full_bar(st),
-                                        w_col(c.col0, p), kb * Cfg::kKStage, c.expert);
+                    for (int p = 0; p < kPanels; ++p) {
+                        const int32_t wc = w_col(c.col0, p), wk = kb * Cfg::kKStage;
+                        if constexpr (kTransW) {
+                            if (p < np && RGG_BOUNDS_OK(w_box_ok(wk, wc, c.expert, args.K, args.N, E, kElemBytes),
+                                                        args.status))
+                                tma_load_3d(b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w, full_bar(st), wk, wc,
+                                            c.expert);
+                        } else {
+                            if (p < np && RGG_BOUNDS_OK(w_box_ok(wc, wk, c.expert, kNw, args.K, E, kElemBytes,
+                                                                 kWOverhang),
+                                                        args.status))
+                                tma_load_3d(b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w, full_bar(st), wc, wk,
+                                            c.expert);
+                        }
+                    }
                     ++issued;
                     if (++st == S) {
                         st = 0;
@@ -722,7 +798,7 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
             bool ok = true;
             auto mma_tile = [&](const TileCoord& c) {
                 const int np = tile_panels<kPanels, Cfg::kPanelN, kEpi>(c.col0, args.N);
-                const uint32_t idesc = Cfg::idesc(runs_as_64_rows<BM>(args, c) ? 64 : BM, np * Cfg::kPanelN);
+                const uint32_t idesc = Cfg::idesc(runs_as_64_rows<BM>(args, c) ? 64 : BM, np * Cfg::kPanelN, !kTransW);
                 if (!wait_or_abort(acce_bar(acc), acc_ph ^ 1u, abort_flag, args.status, args.timeout_ns)) {
                     ok = false;
                     return;
@@ -740,7 +816,8 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
 #pragma unroll
                     for (int j = 0; j < kMmasPerStage; ++j) {
                         const uint64_t ad = sw128_desc(a_st + 32u * j, 16u, 1024u);
-                        const uint64_t bd = sw128_desc(b_st + Cfg::kBStep * j, Cfg::kPanelB, 1024u);
+                        const uint64_t bd = kTransW ? sw128_desc(b_st + 32u * j, 16u, 1024u)
+                                                    : sw128_desc(b_st + Cfg::kBStep * j, Cfg::kPanelB, 1024u);
                         if constexpr (kFp8)
                             mma_f8_ss(d_tmem, ad, bd, idesc, (kb | j) != 0 ? 1u : 0u);
                         else

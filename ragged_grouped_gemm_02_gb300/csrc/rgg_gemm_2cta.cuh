@@ -78,7 +78,7 @@ __device__ __forceinline__ bool pair_runs_as_128_rows(const GemmArgs& args, cons
 // 1 018 TFLOP/s, prefill 1 417 -> 1 526).
 template <int kEpi>
 __host__ __device__ constexpr int pair_epilogue_warps() {
-    return kEpi == kEpiSwiGLU ? 8 : 4;
+    return epi_gate_up(kEpi) ? 8 : 4;
 }
 
 // kDyn: the pair kernel of the mixed launch (rgg_sched.cuh).  The leader's
@@ -87,14 +87,18 @@ __host__ __device__ constexpr int pair_epilogue_warps() {
 // CTAs' tile queues; the leader's MMA thread, the peer's producer and both
 // CTAs' epilogue warps take it from their own CTA's queue and release the slot
 // on the leader's q_empty.  A descriptor with expert -1 ends the walk.
-template <int BN, int kEpi = kEpiPlain, bool kDyn = false>
+//
+// kTransW: Y_e = X_e . W_e^T with W in [E, N, K] order (K contiguous): B panels
+// of 64 W rows by 64 K elements, as in the 1-CTA kernel.
+template <int BN, int kEpi = kEpiPlain, bool kDyn = false, bool kTransW = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilogue_warps<kEpi>(), 1)
     grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_x64,
                              const __grid_constant__ CUtensorMap tmap_w, const GemmArgs args) {
     using Cfg = PairConfig<BN>;
     static_assert(!kDyn || BN == kMixedBN, "the mixed launch's pairs run 256-column MMAs");
+    static_assert(!kTransW || kEpi == kEpiPlain, "the transposed product is the plain one");
     constexpr int BM = 256;  // rows per pair tile
-    constexpr int kOutN = (kEpi == kEpiSwiGLU) ? BN / 2 : BN;  // output columns per tile
+    constexpr int kOutN = epi_gate_up(kEpi) ? BN / 2 : BN;  // output columns per tile
     auto half_tile = [&](const TileCoord& c) {
         return (kEpi == kEpiPlain || BN == 256) && pair_runs_as_128_rows(args, c);
     };
@@ -154,7 +158,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
         if (warp == 0) build_class_prefix_warp(s_off, s_pre, E, 256, args.n_tiles_n, args.pair_min_rows, 0x7fffffff);
         if (warp == 1) build_class_prefix_warp(s_off, s_order, E, 128, args.n_tiles_n, 0, args.pair_min_rows);
         if (warp == 2 && args.sched_split) {
-            const int ps = mixed_pair_sms_from_offsets(s_off, E, kEpi == kEpiSwiGLU ? 2 * args.N : args.N,
+            const int ps = mixed_pair_sms_from_offsets(s_off, E, epi_gate_up(kEpi) ? 2 * args.N : args.N,
                                                        args.pair_min_rows, args.split_sms);
             if (lane == 0) misc[2] = static_cast<uint32_t>(ps);
         }
@@ -259,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                 const int ncols = pair_tile_cols<BN, kEpi>(c.col0, args.N);
                 const int np = ncols / (2 * Cfg::kPanelN);  // panels this CTA loads
                 // plain: this CTA's half of the tile's columns; SwiGLU: the gate (CTA 0) or up (CTA 1) columns
-                const int32_t b_col = (kEpi == kEpiSwiGLU) ? c.col0 + (rank ? args.N : 0)
+                const int32_t b_col = epi_gate_up(kEpi) ? c.col0 + (rank ? args.N : 0)
                                                            : c.col0 + (ncols / 2) * static_cast<int32_t>(rank);
                 const CUtensorMap* xmap = half ? &tmap_x64 : &tmap_x;
                 const uint32_t tx_bytes = 2u * ((half ? 64u : 128u) * 128u + np * Cfg::kPanelB);
@@ -275,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                         // arrive releases it)
                         if (!kDyn && kb == 0)
                             info_ring[n_produced++ % kInfoSlots] =
-                                idesc_bf16_f32(half ? 128 : 256, pair_tile_cols<BN, kEpi>(c.col0, args.N), true);
+                                idesc_bf16_f32(half ? 128 : 256, pair_tile_cols<BN, kEpi>(c.col0, args.N), !kTransW);
                         mbar_arrive_expect_tx(full_bar(st), tx_bytes);
                     }
                     // the second CTA's rows may start past M_tot (a short tile at the end of X): the copy
@@ -285,16 +289,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
 #pragma unroll
                     for (int p = 0; p < Cfg::kPanels; ++p) {
                         // a gate-up tail tile: panel 0 this CTA's 64 gate columns, panel 1 their up columns
-                        const int32_t wc = (kEpi == kEpiSwiGLU && half)
+                        const int32_t wc = (epi_gate_up(kEpi) && half)
                                                ? (p == 0 ? c.col0 : args.N + c.col0) +
                                                      Cfg::kPanelN * static_cast<int32_t>(rank)
                                                : b_col + Cfg::kPanelN * p;
-                        if (p < np && RGG_BOUNDS_OK(w_box_ok(wc, kb * Cfg::kKStage, c.expert,
-                                                             kEpi == kEpiSwiGLU ? 2 * int64_t(args.N) : args.N,
-                                                             args.K, E, 2, Cfg::kPanelN),
-                                                    args.status))
-                            tma_load_3d_pair(b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w, full_leader, wc,
-                                             kb * Cfg::kKStage, c.expert);
+                        const int32_t wk = kb * Cfg::kKStage;
+                        if constexpr (kTransW) {
+                            // rows past the last (the second CTA's half of a narrow tile) are zero-filled
+                            if (p < np && RGG_BOUNDS_OK(w_box_ok(wk, wc, c.expert, args.K,
+                                                                 int64_t(args.N) + Cfg::kPanelN, E, 2),
+                                                        args.status))
+                                tma_load_3d_pair(b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w, full_leader, wk,
+                                                 wc, c.expert);
+                        } else {
+                            if (p < np && RGG_BOUNDS_OK(w_box_ok(wc, wk, c.expert,
+                                                                 epi_gate_up(kEpi) ? 2 * int64_t(args.N) : args.N,
+                                                                 args.K, E, 2, Cfg::kPanelN),
+                                                        args.status))
+                                tma_load_3d_pair(b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w, full_leader, wc,
+                                                 wk, c.expert);
+                        }
                     }
                     ++issued;
                     if (++st == S) {
@@ -398,7 +412,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
 #pragma unroll
                     for (int j = 0; j < kMmasPerStage; ++j) {
                         const uint64_t ad = sw128_desc(a_st + 32u * j, 16u, 1024u);
-                        const uint64_t bd = sw128_desc(b_st + Cfg::kBStep * j, Cfg::kPanelB, 1024u);
+                        const uint64_t bd = kTransW ? sw128_desc(b_st + 32u * j, 16u, 1024u)
+                                                    : sw128_desc(b_st + Cfg::kBStep * j, Cfg::kPanelB, 1024u);
                         mma_bf16_ss_pair(d_tmem, ad, bd, idesc, (kb | j) != 0 ? 1u : 0u);
                     }
                     mma_commit_pair(empty_bar(st), 0x3);
@@ -419,7 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                 cw.init(L, true, single_units > 0);
                 for (int32_t p = pair; ok && p < cw.n_positions; p += pair_units) {
                     const TileCoord c = cw.at(L, p);
-                    mma_tile(idesc_bf16_f32(half_tile(c) ? 128 : 256, pair_tile_cols<BN, kEpi>(c.col0, args.N), true),
+                    mma_tile(idesc_bf16_f32(half_tile(c) ? 128 : 256, pair_tile_cols<BN, kEpi>(c.col0, args.N), !kTransW),
                              false);
                 }
             } else if constexpr (kDyn) {
@@ -432,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                         break;
                     }
                     if (c.expert < 0) break;
-                    mma_tile(idesc_bf16_f32(half_tile(c) ? 128 : 256, pair_tile_cols<BN, kEpi>(c.col0, args.N), true),
+                    mma_tile(idesc_bf16_f32(half_tile(c) ? 128 : 256, pair_tile_cols<BN, kEpi>(c.col0, args.N), !kTransW),
                              false);
                 }
             } else {
@@ -468,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
             const bool half = half_tile(c);
             const int r_local = half ? 64 * static_cast<int>(rank) + 32 * (q & 1) + lane
                                      : 128 * static_cast<int>(rank) + q * 32 + lane;
-            const int tcols = (kEpi == kEpiSwiGLU) ? kOutN : pair_tile_cols<BN, kEpi>(c.col0, N);
+            const int tcols = epi_gate_up(kEpi) ? kOutN : pair_tile_cols<BN, kEpi>(c.col0, N);
             const int ncols = half ? tcols / 2 : tcols;
             const int cbase = half ? (q >> 1) * (tcols / 2) : 0;  // first tile column this warp holds
             const bool row_ok = r_local < c.rows;
@@ -487,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                 const uint32_t tcol = static_cast<uint32_t>(acc * BN + cc);
                 const bool ld_ok = RGG_BOUNDS_OK(tmem_cols_ok(tcol, 32, Cfg::kTmemCols), args.status);
                 if (ld_ok) tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(cc), v);
-                if constexpr (kEpi == kEpiSwiGLU) {
+                if constexpr (epi_gate_up(kEpi)) {
                     // gate in columns [cc, cc+32), up in [up_off + cc, up_off + cc + 32): kOutN
                     // columns on (M = 256), half that on an M = 128 tail tile
                     const int up_off = half ? kOutN / 2 : kOutN;
@@ -499,15 +514,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                         for (int i = 0; i < 32; ++i) u[i] = 0u;
                     if (!ld_ok)
                         for (int i = 0; i < 32; ++i) v[i] = 0u;
+                    if constexpr (kEpi == kEpiSwiGLUBwd) {
+                        if (row_ok) store_swiglu_backward(args, row, c.col0 + cbase + cc, v, u, row_lo, row_hi);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = __float_as_uint(silu_f32(__uint_as_float(v[i])) * __uint_as_float(u[i]));
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = __float_as_uint(silu_f32(__uint_as_float(v[i])) * __uint_as_float(u[i]));
+                    }
                 } else {
                     tmem_ld_wait();
                     if (!ld_ok)
                         for (int i = 0; i < 32; ++i) v[i] = 0u;
                 }
-                if (row_ok) {
+                if (kEpi != kEpiSwiGLUBwd && row_ok) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int col = c.col0 + cbase + cc + 16 * h;

@@ -1,0 +1,50 @@
+// rgg_host.h -- host helpers of the C ABI shared by its translation units
+// (defined in rgg_api.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "rgg.h"
+
+namespace rgg {
+
+constexpr uint64_t kHostDefaultTimeoutNs = 2000000000ull;
+
+// What a handle holds.
+struct HostDevice {
+    int device, num_sms, smem_optin;
+    int32_t* status;
+};
+HostDevice host_device(const rgg_handle* h);
+
+// Makes `device` current for the scope of a call and restores the caller's.
+class HostDeviceScope {
+public:
+    explicit HostDeviceScope(int device) {
+        if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = -1;
+        if (prev_ != device) err_ = cudaSetDevice(device);
+    }
+    ~HostDeviceScope() {
+        int cur = -1;
+        if (prev_ >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev_) cudaSetDevice(prev_);
+    }
+    cudaError_t error() const { return err_; }
+
+private:
+    int prev_ = -1;
+    cudaError_t err_ = cudaSuccess;
+};
+
+inline bool host_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// 1 <= E <= 4096, 0 <= M_tot < 2^31, K and N at least 8 and multiples of 8.
+rgg_status host_check_sizes(int E, int64_t M_tot, int K, int N);
+
+// The tensor map of a row-major bf16 matrix [rows, cols] with boxes of 64
+// columns (one 128-byte swizzle row) by `box_rows` rows.
+rgg_status host_encode_rows(const void* p, int64_t rows, int cols, int box_rows, CUtensorMap* map);
+
+}  // namespace rgg

@@ -93,6 +93,26 @@ cudaError_t launch_gemm_mixed_swiglu(int pair_grid, size_t pair_smem, const Gemm
                                      const CUtensorMap& tmap_x, const CUtensorMap& tmap_x64,
                                      const CUtensorMap& tmap_w);
 
+// The gradient by the activations (W read transposed: tmap_w spans {K, N, E} in
+// the kernel's terms, K the reduction): `bm` 64, 128 (bn 128, 192, 256) or 256
+// (bn 128, 256); and its mixed launch.
+cudaError_t launch_gemm_dgrad(int bm, int bn, int grid, size_t smem, cudaStream_t stream, const CUtensorMap& tmap_x,
+                              const CUtensorMap& tmap_x64, const CUtensorMap& tmap_w, const GemmArgs& args);
+cudaError_t launch_gemm_mixed_dgrad(int pair_grid, size_t pair_smem, const GemmArgs& pair_args, int single_grid,
+                                    size_t single_smem, const GemmArgs& single_args, cudaStream_t stream,
+                                    const CUtensorMap& tmap_x, const CUtensorMap& tmap_x64,
+                                    const CUtensorMap& tmap_w);
+
+// The backward pass of the fused gate-up op (args.dH, args.act; args.Y is
+// [M_tot, 2N]): `bm` 64, 128 or 256, `bn` 128 or 256; and its mixed launch.
+cudaError_t launch_gemm_swiglu_bwd(int bm, int bn, int grid, size_t smem, cudaStream_t stream,
+                                   const CUtensorMap& tmap_x, const CUtensorMap& tmap_x64, const CUtensorMap& tmap_w,
+                                   const GemmArgs& args);
+cudaError_t launch_gemm_mixed_swiglu_bwd(int pair_grid, size_t pair_smem, const GemmArgs& pair_args, int single_grid,
+                                         size_t single_smem, const GemmArgs& single_args, cudaStream_t stream,
+                                         const CUtensorMap& tmap_x, const CUtensorMap& tmap_x64,
+                                         const CUtensorMap& tmap_w);
+
 // The flat tile list written out by the same device code the GEMM uses, in
 // list order (walk_order 0) or in the order walk_order visits it.
 cudaError_t launch_export_tiles(const int32_t* offsets, int E, int64_t M_tot, int N, int bm, int bn,
@@ -110,10 +130,11 @@ rgg_status host_check_gemm_args(const void* X, const void* W, const int32_t* gro
 // Plan, encode and launch rgg_grouped_gemm on the current device for a GPU of
 // `num_sms` SMs and `smem_optin` bytes of shared memory per block, recording
 // device-detected errors in the device word `status`.  Arguments already
-// checked by host_check_gemm_args.
+// checked by host_check_gemm_args.  `trans_w`: Y_e = X_e . W_e^T with W
+// [E, N, K] (rgg_grouped_gemm_dgrad).
 rgg_status host_grouped_gemm(int num_sms, int smem_optin, int32_t* status, const void* X, const void* W,
                              const int32_t* group_offsets, void* Y, int E, int64_t M_tot, int K, int N,
-                             cudaStream_t stream, const rgg_options* opt);
+                             cudaStream_t stream, const rgg_options* opt, bool trans_w = false);
 
 // Offsets check alone (used when there are no rows to multiply).
 cudaError_t launch_validate_offsets(const int32_t* offsets, int E, int64_t M_tot, int32_t* status,

@@ -70,6 +70,14 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
     return ok != 0;
 }
 
+// Makes this thread's shared-memory writes visible to the async proxy (TMA,
+// tcgen05) before what it signals next.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
+}
+
 // ------------------------------------------- programmatic dependent launch
 
 // Lets the kernel launched after this one on the stream with programmatic

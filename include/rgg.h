@@ -454,6 +454,103 @@ rgg_status rgg_grouped_gemm_wgrad(rgg_handle* h, const void* X, const void* dY, 
                                   void* dW, int E, int64_t M_tot, int K, int N, int flags, void* stream,
                                   const rgg_options* opt);
 
+/* One tensor of a list: `numel` contiguous values of type `dtype` at `in`, results to `out` (may be `in`). */
+#define RGG_BF16 0
+#define RGG_FP32 1
+#define RGG_FP16 2
+typedef struct rgg_tensor {
+    const void* in;
+    void* out;
+    int64_t numel;
+    int64_t dtype;
+} rgg_tensor;
+
+/*
+ * rgg_clip_grad_norm -- the global 2-norm of a list of gradients, and the
+ * gradients clipped by it:
+ *
+ *     norm = sqrt(sum over all tensors of sum g^2)
+ *     out  = g * min(1, max_norm / (norm + 1e-6))
+ *
+ * tensors: HOST array of `count` descriptors with device pointers, read before
+ * the call returns; types may differ between tensors, any alignment of the
+ * element size will do, numel may be 0.  norm_out: device fp32 [1], the norm
+ * before clipping.  The norm is summed in fp64 from fp32 sums of at most 128
+ * squares (in fp64 throughout where those would overflow or lose bits), in an
+ * order that depends on the list only: equal calls give equal bits.  Results
+ * are rounded once to their type.  Where the factor is 1, tensors clipped in
+ * place are not written.
+ *
+ * A norm that is not finite (a gradient holds Inf or NaN) leaves the values
+ * unscaled: `out` is then a copy of `in`, and norm_out says so to the caller,
+ * who skips the step or handles it.  max_norm may be 0 (all results 0) or Inf
+ * (the norm alone); a negative one or NaN is RGG_ERR_INVALID_ARG.
+ *
+ * workspace: device memory of at least rgg_clip_grad_norm_workspace(count)
+ * bytes, 8-byte aligned, not shared by calls that may overlap.  Nothing is
+ * allocated; asynchronous on `stream`; can be captured in a graph.
+ */
+int64_t rgg_clip_grad_norm_workspace(int count);
+rgg_status rgg_clip_grad_norm(rgg_handle* h, const rgg_tensor* tensors, int count, float max_norm, float* norm_out,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * MXFP4 (OCP microscaling, 4-bit E2M1 values with an E8M0 scale per 32 of K).
+ *
+ * Codes: two values a byte, the even K index in the low half, K contiguous:
+ * [rows, K/2].  Scales: one byte (2^(byte - 127), 255 = NaN) per 32 values
+ * along K, in blocks of 128 rows by 4 scales, 512 bytes each; row r and scale s
+ * of a block are at (r % 32) * 16 + (r / 32) * 4 + s, and the blocks of 128 rows
+ * are [row block, ceil(K / 128), 512].
+ *   activations [M_tot, K], rows grouped by expert: row i of expert e is row
+ *     (i - off[e]) % 128 of row block off[e] / 128 + e + (i - off[e]) / 128;
+ *     M_tot / 128 + E row blocks (rgg_mxfp4_scale_bytes bytes).
+ *   weights [E, K, N]: codes [E, N, K/2]; column n of expert e is row n % 128 of
+ *     row block e * ceil(N / 128) + n / 128; E * ceil(N/128) * ceil(K/128) * 512
+ *     bytes.
+ * Bytes of a block that belong to no row are never read; those of no value of K
+ * are written 0.
+ *
+ * The quantisers (bf16 in): per 32 values, a = max |x|, the scale is
+ * 2^(floor(log2 a) - 2) (byte 0 at least) and a code is x / scale rounded to
+ * nearest even, at most 6 in magnitude.  32 values that hold Inf or NaN get the
+ * scale NaN and codes 0.  The dequantisers give the values back as bf16, without
+ * rounding; weights come back as [E, N, K].
+ *
+ * K % 32 == 0 and K >= 32, N % 8 == 0; all pointers 16-byte aligned (offsets 4).
+ * rgg_mxfp4_quantize and rgg_mxfp4_dequantize leave rows of no expert alone and
+ * report invalid offsets through the status word, writing nothing.
+ * Asynchronous on `stream`; nothing is allocated.
+ */
+int64_t rgg_mxfp4_scale_bytes(int64_t M_tot, int E, int K);
+rgg_status rgg_mxfp4_quantize(rgg_handle* h, const void* X, const int32_t* group_offsets, void* codes, void* scales,
+                              int E, int64_t M_tot, int K, void* stream);
+rgg_status rgg_mxfp4_dequantize(rgg_handle* h, const void* codes, const void* scales, const int32_t* group_offsets,
+                                void* X, int E, int64_t M_tot, int K, void* stream);
+rgg_status rgg_mxfp4_quantize_weights(rgg_handle* h, const void* W, void* codes, void* scales, int E, int K, int N,
+                                      void* stream);
+rgg_status rgg_mxfp4_dequantize_weights(rgg_handle* h, const void* codes, const void* scales, void* W, int E, int K,
+                                        int N, void* stream);
+
+/*
+ * rgg_grouped_gemm_mxfp4 -- the grouped product of MXFP4 operands:
+ *     Y[i, n] = sum_k x[i, k] * w[e, n, k]      for every row i of expert e
+ * in fp32 on the tensor core (tcgen05.mma kind::mxf4 with block scaling),
+ * rounded once to bf16.  rgg_grouped_gemm_swiglu_mxfp4 is the gate-up projection:
+ * the weight has 2N columns, gate first, and H = silu(g) * u is bf16 [M_tot, N];
+ * N must then be a multiple of 128.  Operands as the quantisers leave them.  Of
+ * `opt` they read bm (0 or 128), bn (0, 128 for the plain product, or 256),
+ * stages, max_ctas, timeout_ns and debug_flags.  Other arguments, errors and
+ * the stream contract as for rgg_grouped_gemm.
+ */
+rgg_status rgg_grouped_gemm_mxfp4(rgg_handle* h, const void* x_codes, const void* x_scales, const void* w_codes,
+                                  const void* w_scales, const int32_t* group_offsets, void* Y, int E, int64_t M_tot,
+                                  int K, int N, void* stream, const rgg_options* opt);
+rgg_status rgg_grouped_gemm_swiglu_mxfp4(rgg_handle* h, const void* x_codes, const void* x_scales,
+                                         const void* w13_codes, const void* w13_scales, const int32_t* group_offsets,
+                                         void* H, int E, int64_t M_tot, int K, int N, void* stream,
+                                         const rgg_options* opt);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,7 +19,9 @@ import threading
 __all__ = [
     "RggError", "rgg_grouped_gemm", "rgg_grouped_gemm_swiglu", "rgg_grouped_gemm_fp8", "rgg_grouped_gemm_gather",
     "rgg_grouped_gemm_swiglu_gather", "rgg_grouped_gemm_dgrad", "rgg_grouped_gemm_wgrad",
-    "rgg_grouped_gemm_swiglu_backward", "rgg_grouped_gemm_noalloc", "rgg_export_tiles", "rgg_export_walk",
+    "rgg_grouped_gemm_swiglu_backward", "rgg_clip_grad_norm",
+    "rgg_mxfp4_quantize", "rgg_mxfp4_dequantize", "rgg_mxfp4_quantize_weights", "rgg_mxfp4_dequantize_weights",
+    "rgg_grouped_gemm_mxfp4", "rgg_grouped_gemm_swiglu_mxfp4", "rgg_grouped_gemm_noalloc", "rgg_export_tiles", "rgg_export_walk",
     "rgg_query_status",
     "rgg_plan", "rgg_status_string", "library_path", "load_library", "EXPORTED_SYMBOLS",
     "RGG_OK", "RGG_ERR_INVALID_ARG", "RGG_ERR_UNSUPPORTED", "RGG_ERR_CUDA", "RGG_ERR_BAD_OFFSETS",
@@ -48,6 +50,9 @@ EXPORTED_SYMBOLS = (
     "rgg_plan", "rgg_status_string", "rgg_last_cuda_error", "rgg_grouped_gemm_noalloc", "rgg_grouped_gemm_swiglu",
     "rgg_grouped_gemm_fp8", "rgg_grouped_gemm_gather", "rgg_grouped_gemm_swiglu_gather", "rgg_export_walk",
     "rgg_grouped_gemm_dgrad", "rgg_grouped_gemm_wgrad", "rgg_grouped_gemm_swiglu_backward",
+    "rgg_clip_grad_norm", "rgg_clip_grad_norm_workspace", "rgg_mxfp4_scale_bytes", "rgg_mxfp4_quantize",
+    "rgg_mxfp4_dequantize", "rgg_mxfp4_quantize_weights", "rgg_mxfp4_dequantize_weights", "rgg_grouped_gemm_mxfp4",
+    "rgg_grouped_gemm_swiglu_mxfp4",
 )
 
 
@@ -133,6 +138,21 @@ def open_library(path: str) -> ctypes.CDLL:
     lib.rgg_grouped_gemm_dgrad.restype = I
     lib.rgg_grouped_gemm_wgrad.argtypes = [P, P, P, P, P, I, I64, I, I, I, P, ctypes.POINTER(_Options)]
     lib.rgg_grouped_gemm_wgrad.restype = I
+    lib.rgg_clip_grad_norm.argtypes = [P, P, I, ctypes.c_float, P, P, I64, P]
+    lib.rgg_clip_grad_norm.restype = I
+    lib.rgg_clip_grad_norm_workspace.argtypes = [I]
+    lib.rgg_clip_grad_norm_workspace.restype = I64
+    lib.rgg_mxfp4_scale_bytes.argtypes = [I64, I, I]
+    lib.rgg_mxfp4_scale_bytes.restype = I64
+    lib.rgg_mxfp4_quantize.argtypes = [P, P, P, P, P, I, I64, I, P]
+    lib.rgg_mxfp4_dequantize.argtypes = [P, P, P, P, P, I, I64, I, P]
+    for name in ("rgg_mxfp4_quantize_weights", "rgg_mxfp4_dequantize_weights"):
+        getattr(lib, name).argtypes = [P, P, P, P, I, I, I, P]
+    for name in ("rgg_grouped_gemm_mxfp4", "rgg_grouped_gemm_swiglu_mxfp4"):
+        getattr(lib, name).argtypes = [P, P, P, P, P, P, P, I, I64, I, I, P, ctypes.POINTER(_Options)]
+    for name in ("rgg_mxfp4_quantize", "rgg_mxfp4_dequantize", "rgg_mxfp4_quantize_weights",
+                 "rgg_mxfp4_dequantize_weights", "rgg_grouped_gemm_mxfp4", "rgg_grouped_gemm_swiglu_mxfp4"):
+        getattr(lib, name).restype = I
     lib.rgg_grouped_gemm_swiglu_backward.argtypes = [P, P, P, P, P, P, P, I, I64, I, I, P, ctypes.POINTER(_Options)]
     lib.rgg_grouped_gemm_swiglu_backward.restype = I
     lib.rgg_grouped_gemm_noalloc.argtypes = [P, P, P, P, I, I64, I, I, P, P]
@@ -544,6 +564,195 @@ def rgg_grouped_gemm_swiglu_backward(X, W13, group_offsets, dH, dGU=None, H=None
     del keep
     _finish("rgg_grouped_gemm_swiglu_backward", s, device, st, check)
     return dGU, H
+
+
+def rgg_clip_grad_norm(grads, max_norm, out=None, *, stream=None):
+    """The global 2-norm of a list of gradients, and the gradients scaled by
+    ``min(1, max_norm / (norm + 1e-6))``: in place, or into the tensors ``out``.
+
+    grads: contiguous CUDA tensors on one device, bf16, fp16 or fp32 (types
+    may differ); out: as many, each of its gradient's type and size.  Returns
+    the norm before clipping, an fp32 CUDA scalar (nothing is synchronised).
+    If it is not finite the gradients are left (or copied) unscaled."""
+    import torch
+    from array import array
+    grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
+    if out is None:
+        out = grads
+    else:
+        out = [out] if isinstance(out, torch.Tensor) else list(out)
+        if len(out) != len(grads):
+            raise ValueError("out must have as many tensors as grads (%d, not %d)" % (len(grads), len(out)))
+    if not grads:
+        raise ValueError("grads is empty")
+    if not max_norm >= 0:
+        raise ValueError("max_norm must not be negative or NaN")
+    codes = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+    dev = grads[0].device
+    packed = array("q")
+    for g, o in zip(grads, out):
+        code = codes.get(g.dtype)
+        if code is None or o.dtype != g.dtype:
+            raise TypeError("gradients must be bf16, fp16 or fp32, and each output of its gradient's type")
+        if not g.is_cuda or g.device != dev or o.device != dev:
+            raise ValueError("all tensors must be CUDA tensors on one device")
+        n = g.numel()
+        if o.numel() != n or not (g.is_contiguous() and o.is_contiguous()):
+            raise ValueError("gradients and outputs must be contiguous, each output of its gradient's size")
+        packed.extend((g.data_ptr(), o.data_ptr(), n, code))
+    lib = load_library()
+    bytes_ = lib.rgg_clip_grad_norm_workspace(len(grads))
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    workspace = torch.empty(bytes_ // 8, dtype=torch.float64, device=dev)
+    st = _stream_ptr(stream, dev.index)
+    if stream is not None:
+        # allocated on the current stream, used on another one
+        workspace.record_stream(stream)
+    s = lib.rgg_clip_grad_norm(_handle(dev.index), packed.buffer_info()[0], len(grads), float(max_norm),
+                               norm.data_ptr(), workspace.data_ptr(), bytes_, st)
+    if s != RGG_OK:
+        _raise(s, "rgg_clip_grad_norm")
+    return norm
+
+
+def _mx_scale_shape(M_tot, E, K):
+    return (M_tot // 128 + E, -(-K // 128), 512)
+
+
+def _mx_weight_scale_shape(E, N, K):
+    return (E, -(-N // 128), -(-K // 128), 512)
+
+
+def rgg_mxfp4_quantize(X, group_offsets, codes=None, scales=None, *, stream=None, check=False):
+    """MXFP4 form of activations whose rows are grouped by expert: 4-bit E2M1
+    codes with one power-of-two scale per 32 values along K.
+
+    X: bf16 CUDA [M_tot, K], K a multiple of 32; group_offsets: int32 CUDA
+    [E+1].  Returns ``(codes, scales)``: uint8 [M_tot, K/2], two codes a byte,
+    and uint8 [M_tot // 128 + E, ceil(K / 128), 512] in the order the products
+    read (include/rgg.h).  Rows of no expert are left alone."""
+    import torch
+    if X.dim() != 2 or group_offsets.dim() != 1 or group_offsets.numel() < 2:
+        raise ValueError("X must be [M_tot, K] and group_offsets [E+1]")
+    M_tot, K = X.shape
+    E = group_offsets.numel() - 1
+    if codes is None:
+        codes = torch.empty(M_tot, K // 2, dtype=torch.uint8, device=X.device)
+    if scales is None:
+        scales = torch.empty(_mx_scale_shape(M_tot, E, K), dtype=torch.uint8, device=X.device)
+    _check_operands(X.device, X=(X, torch.bfloat16, (M_tot, K)), group_offsets=(group_offsets, torch.int32, (E + 1,)),
+                    codes=(codes, torch.uint8, (M_tot, K // 2)),
+                    scales=(scales, torch.uint8, _mx_scale_shape(M_tot, E, K)))
+    device = X.device.index
+    st = _stream_ptr(stream, device)
+    s = load_library().rgg_mxfp4_quantize(_handle(device), X.data_ptr(), group_offsets.data_ptr(), codes.data_ptr(),
+                                          scales.data_ptr(), E, M_tot, K, st)
+    _finish("rgg_mxfp4_quantize", s, device, st, check)
+    return codes, scales
+
+
+def rgg_mxfp4_dequantize(codes, scales, group_offsets, X=None, *, stream=None, check=False):
+    """The values of ``rgg_mxfp4_quantize``'s result, bf16 [M_tot, K] (exact)."""
+    import torch
+    if codes.dim() != 2 or group_offsets.dim() != 1 or group_offsets.numel() < 2:
+        raise ValueError("codes must be [M_tot, K/2] and group_offsets [E+1]")
+    M_tot, K = codes.shape[0], 2 * codes.shape[1]
+    E = group_offsets.numel() - 1
+    if X is None:
+        X = torch.empty(M_tot, K, dtype=torch.bfloat16, device=codes.device)
+    _check_operands(codes.device, codes=(codes, torch.uint8, (M_tot, K // 2)),
+                    scales=(scales, torch.uint8, _mx_scale_shape(M_tot, E, K)),
+                    group_offsets=(group_offsets, torch.int32, (E + 1,)), X=(X, torch.bfloat16, (M_tot, K)))
+    device = codes.device.index
+    st = _stream_ptr(stream, device)
+    s = load_library().rgg_mxfp4_dequantize(_handle(device), codes.data_ptr(), scales.data_ptr(),
+                                            group_offsets.data_ptr(), X.data_ptr(), E, M_tot, K, st)
+    _finish("rgg_mxfp4_dequantize", s, device, st, check)
+    return X
+
+
+def rgg_mxfp4_quantize_weights(W, codes=None, scales=None, *, stream=None):
+    """MXFP4 form of expert weights, laid out once: W bf16 CUDA [E, K, N], blocks
+    of 32 along K.  Returns ``(codes, scales)``: uint8 [E, N, K/2] and uint8
+    [E, ceil(N / 128), ceil(K / 128), 512]."""
+    import torch
+    if W.dim() != 3:
+        raise ValueError("W must be [E, K, N]")
+    E, K, N = W.shape
+    if codes is None:
+        codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=W.device)
+    if scales is None:
+        scales = torch.empty(_mx_weight_scale_shape(E, N, K), dtype=torch.uint8, device=W.device)
+    _check_operands(W.device, W=(W, torch.bfloat16, (E, K, N)), codes=(codes, torch.uint8, (E, N, K // 2)),
+                    scales=(scales, torch.uint8, _mx_weight_scale_shape(E, N, K)))
+    device = W.device.index
+    st = _stream_ptr(stream, device)
+    s = load_library().rgg_mxfp4_quantize_weights(_handle(device), W.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                                  E, K, N, st)
+    _finish("rgg_mxfp4_quantize_weights", s, device, st, False)
+    return codes, scales
+
+
+def rgg_mxfp4_dequantize_weights(codes, scales, W=None, *, stream=None):
+    """The values of ``rgg_mxfp4_quantize_weights``'s result, bf16 [E, N, K] (exact)."""
+    import torch
+    if codes.dim() != 3:
+        raise ValueError("codes must be [E, N, K/2]")
+    E, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+    if W is None:
+        W = torch.empty(E, N, K, dtype=torch.bfloat16, device=codes.device)
+    _check_operands(codes.device, codes=(codes, torch.uint8, (E, N, K // 2)),
+                    scales=(scales, torch.uint8, _mx_weight_scale_shape(E, N, K)),
+                    W=(W, torch.bfloat16, (E, N, K)))
+    device = codes.device.index
+    st = _stream_ptr(stream, device)
+    s = load_library().rgg_mxfp4_dequantize_weights(_handle(device), codes.data_ptr(), scales.data_ptr(),
+                                                    W.data_ptr(), E, K, N, st)
+    _finish("rgg_mxfp4_dequantize_weights", s, device, st, False)
+    return W
+
+
+def _mxfp4_call(name, x_codes, x_scales, w_codes, w_scales, group_offsets, out, gate_up, bn, stages, max_ctas,
+                timeout_ns, debug_flags, stream, check):
+    import torch
+    if x_codes.dim() != 2 or w_codes.dim() != 3 or (gate_up and w_codes.shape[1] % 2 != 0):
+        raise ValueError("codes must be [M_tot, K/2] for the activations and [E, N, K/2] for the weights")
+    M_tot, half = x_codes.shape
+    E, cols = w_codes.shape[:2]
+    N = cols // 2 if gate_up else cols
+    if out is None:
+        out = torch.empty(M_tot, N, dtype=torch.bfloat16, device=x_codes.device)
+    _check_operands(x_codes.device, x_codes=(x_codes, torch.uint8, (M_tot, half)),
+                    x_scales=(x_scales, torch.uint8, _mx_scale_shape(M_tot, E, 2 * half)),
+                    w_codes=(w_codes, torch.uint8, (E, cols, half)),
+                    w_scales=(w_scales, torch.uint8, _mx_weight_scale_shape(E, cols, 2 * half)),
+                    group_offsets=(group_offsets, torch.int32, (E + 1,)), out=(out, torch.bfloat16, (M_tot, N)))
+    device = x_codes.device.index
+    opt, _ = _options(0, bn, stages, max_ctas, timeout_ns, None, debug_flags)
+    st = _stream_ptr(stream, device)
+    s = getattr(load_library(), name)(_handle(device), x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(),
+                                      w_scales.data_ptr(), group_offsets.data_ptr(), out.data_ptr(), E, M_tot,
+                                      2 * half, N, st, ctypes.byref(opt))
+    _finish(name, s, device, st, check)
+    return out
+
+
+def rgg_grouped_gemm_mxfp4(x_codes, x_scales, w_codes, w_scales, group_offsets, Y=None, *, bn=0, stages=0, max_ctas=0,
+                           timeout_ns=0, debug_flags=0, stream=None, check=False):
+    """Y_e = X_e . W_e for every expert with MXFP4 operands, as
+    ``rgg_mxfp4_quantize`` and ``rgg_mxfp4_quantize_weights`` leave them; Y:
+    optional bf16 CUDA [M_tot, N]."""
+    return _mxfp4_call("rgg_grouped_gemm_mxfp4", x_codes, x_scales, w_codes, w_scales, group_offsets, Y, False, bn,
+                       stages, max_ctas, timeout_ns, debug_flags, stream, check)
+
+
+def rgg_grouped_gemm_swiglu_mxfp4(x_codes, x_scales, w13_codes, w13_scales, group_offsets, H=None, *, stages=0,
+                                  max_ctas=0, timeout_ns=0, debug_flags=0, stream=None, check=False):
+    """H = silu(gate) * up for every expert with MXFP4 operands: w13_codes hold
+    the 2N columns of W13 (gate first), N a multiple of 128; H: optional bf16
+    CUDA [M_tot, N]."""
+    return _mxfp4_call("rgg_grouped_gemm_swiglu_mxfp4", x_codes, x_scales, w13_codes, w13_scales, group_offsets, H,
+                       True, 0, stages, max_ctas, timeout_ns, debug_flags, stream, check)
 
 
 def rgg_export_tiles(group_offsets, M_tot: int, N: int, bm: int, bn: int, cap: int | None = None, stream=None):

@@ -28,7 +28,8 @@ LIB_DEBUG = os.path.join(PKG, "librgg_debug.so")
 
 SOURCES = ["rgg_api.cu", "rgg_aux.cu", "rgg_gemm_bm128.cu", "rgg_gemm_bm64.cu", "rgg_gemm_pair.cu",
            "rgg_noalloc.cu", "rgg_gemm_swiglu.cu", "rgg_gemm_fp8.cu", "rgg_gemm_gather.cu",
-           "rgg_gemm_mixed.cu", "rgg_gemm_dgrad.cu", "rgg_gemm_swiglu_bwd.cu", "rgg_wgrad.cu"]
+           "rgg_gemm_mixed.cu", "rgg_gemm_dgrad.cu", "rgg_gemm_swiglu_bwd.cu", "rgg_wgrad.cu", "rgg_clip.cu",
+           "rgg_mxfp4_quant.cu", "rgg_mxfp4_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

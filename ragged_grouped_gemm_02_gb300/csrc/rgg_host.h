@@ -47,4 +47,7 @@ rgg_status host_check_sizes(int E, int64_t M_tot, int K, int N);
 // columns (one 128-byte swizzle row) by `box_rows` rows.
 rgg_status host_encode_rows(const void* p, int64_t rows, int cols, int box_rows, CUtensorMap* map);
 
+// The 3-D tensor map of `batch` byte matrices [rows, bytes], with boxes of 128 bytes (one swizzle row) by `box_rows` rows.
+rgg_status host_encode_codes(const void* p, int64_t rows, int batch, int64_t bytes, int box_rows, CUtensorMap* map);
+
 }  // namespace rgg

@@ -539,8 +539,9 @@ rgg_status rgg_mxfp4_dequantize_weights(rgg_handle* h, const void* codes, const 
  * rounded once to bf16.  rgg_grouped_gemm_swiglu_mxfp4 is the gate-up projection:
  * the weight has 2N columns, gate first, and H = silu(g) * u is bf16 [M_tot, N];
  * N must then be a multiple of 128.  Operands as the quantisers leave them.  Of
- * `opt` they read bm (0 or 128), bn (0, 128 for the plain product, or 256),
- * stages, max_ctas, timeout_ns and debug_flags.  Other arguments, errors and
+ * `opt` they read bn (256: 256 x 256 tiles on CTA pairs, 128: 128 x 128 tiles on
+ * single CTAs, 0: by the rows per expert), bm (0 or the same), stages, max_ctas
+ * (at least 2 for pairs), timeout_ns and debug_flags.  Other arguments, errors and
  * the stream contract as for rgg_grouped_gemm.
  */
 rgg_status rgg_grouped_gemm_mxfp4(rgg_handle* h, const void* x_codes, const void* x_scales, const void* w_codes,

@@ -741,18 +741,19 @@ def rgg_grouped_gemm_mxfp4(x_codes, x_scales, w_codes, w_scales, group_offsets, 
                            timeout_ns=0, debug_flags=0, stream=None, check=False):
     """Y_e = X_e . W_e for every expert with MXFP4 operands, as
     ``rgg_mxfp4_quantize`` and ``rgg_mxfp4_quantize_weights`` leave them; Y:
-    optional bf16 CUDA [M_tot, N]."""
+    optional bf16 CUDA [M_tot, N].  bn: 256 (256 x 256 tiles on CTA pairs), 128
+    (128 x 128 on single CTAs) or 0, by the rows per expert."""
     return _mxfp4_call("rgg_grouped_gemm_mxfp4", x_codes, x_scales, w_codes, w_scales, group_offsets, Y, False, bn,
                        stages, max_ctas, timeout_ns, debug_flags, stream, check)
 
 
-def rgg_grouped_gemm_swiglu_mxfp4(x_codes, x_scales, w13_codes, w13_scales, group_offsets, H=None, *, stages=0,
+def rgg_grouped_gemm_swiglu_mxfp4(x_codes, x_scales, w13_codes, w13_scales, group_offsets, H=None, *, bn=0, stages=0,
                                   max_ctas=0, timeout_ns=0, debug_flags=0, stream=None, check=False):
     """H = silu(gate) * up for every expert with MXFP4 operands: w13_codes hold
     the 2N columns of W13 (gate first), N a multiple of 128; H: optional bf16
     CUDA [M_tot, N]."""
     return _mxfp4_call("rgg_grouped_gemm_swiglu_mxfp4", x_codes, x_scales, w13_codes, w13_scales, group_offsets, H,
-                       True, 0, stages, max_ctas, timeout_ns, debug_flags, stream, check)
+                       True, bn, stages, max_ctas, timeout_ns, debug_flags, stream, check)
 
 
 def rgg_export_tiles(group_offsets, M_tot: int, N: int, bm: int, bn: int, cap: int | None = None, stream=None):

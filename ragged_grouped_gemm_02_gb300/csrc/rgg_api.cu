@@ -596,6 +596,45 @@ rgg_status host_encode_rows(const void* p, int64_t rows, int cols, int box_rows,
     return RGG_ERR_CUDA;
 }
 
+rgg_status host_encode_out(const void* p, int batch, int64_t rows, int cols, bool f32, int box_rows, CUtensorMap* map) {
+    EncodeTiledFn encode = encode_tiled_fn();
+    if (!encode) {
+        g_last_cuda_error = "cuTensorMapEncodeTiled is not available from the driver";
+        return RGG_ERR_CUDA;
+    }
+    const cuuint64_t row_bytes = static_cast<cuuint64_t>(cols) * (f32 ? 4 : 2);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(batch)};
+    const cuuint64_t strides[2] = {row_bytes, row_bytes * static_cast<cuuint64_t>(rows)};
+    const cuuint32_t box[3] = {f32 ? 32u : 64u, static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                              const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return RGG_OK;
+    g_last_cuda_error = "cuTensorMapEncodeTiled (output) failed with CUresult " + std::to_string(static_cast<int>(r));
+    return RGG_ERR_CUDA;
+}
+
+rgg_status host_encode_words(const void* p, int64_t rows, int64_t words, int box_words, CUtensorMap* map) {
+    EncodeTiledFn encode = encode_tiled_fn();
+    if (!encode) {
+        g_last_cuda_error = "cuTensorMapEncodeTiled is not available from the driver";
+        return RGG_ERR_CUDA;
+    }
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(words), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(words) * 4};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_words), 1};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(p), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return RGG_OK;
+    g_last_cuda_error = "cuTensorMapEncodeTiled (scales) failed with CUresult " + std::to_string(static_cast<int>(r));
+    return RGG_ERR_CUDA;
+}
+
 rgg_status host_encode_codes(const void* p, int64_t rows, int batch, int64_t bytes, int box_rows, CUtensorMap* map) {
     EncodeTiledFn encode = encode_tiled_fn();
     if (!encode) {

@@ -47,7 +47,15 @@ rgg_status host_check_sizes(int E, int64_t M_tot, int K, int N);
 // columns (one 128-byte swizzle row) by `box_rows` rows.
 rgg_status host_encode_rows(const void* p, int64_t rows, int cols, int box_rows, CUtensorMap* map);
 
+// The tensor map of bf16 or fp32 matrices [batch, rows, cols] with boxes of 128
+// bytes by `box_rows` rows, for stores.
+rgg_status host_encode_out(const void* p, int batch, int64_t rows, int cols, bool f32, int box_rows, CUtensorMap* map);
+
 // The 3-D tensor map of `batch` byte matrices [rows, bytes], with boxes of 128 bytes (one swizzle row) by `box_rows` rows.
 rgg_status host_encode_codes(const void* p, int64_t rows, int batch, int64_t bytes, int box_rows, CUtensorMap* map);
+
+// The tensor map of a matrix of 32-bit words [rows, words] with boxes of one
+// row by `box_words` words, unswizzled.
+rgg_status host_encode_words(const void* p, int64_t rows, int64_t words, int box_words, CUtensorMap* map);
 
 }  // namespace rgg

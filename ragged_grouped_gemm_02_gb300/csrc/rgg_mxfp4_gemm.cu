@@ -9,14 +9,13 @@
 
 namespace rgg {
 
-template <int BN, bool kGateUp>
-static cudaError_t launch_mxfp4(int grid, size_t smem, cudaStream_t stream, const CUtensorMap& tx,
-                                const CUtensorMap& tw, const MxArgs& args) {
-    auto kernel = grouped_mxfp4_kernel<BN, kGateUp>;
+template <typename Kernel>
+static cudaError_t launch_mxfp4(Kernel kernel, int grid, size_t smem, cudaStream_t stream, const MxMaps& maps,
+                                const MxArgs& args) {
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(smem));
     if (err != cudaSuccess) return err;
-    return launch_chained(kernel, grid, kMxThreads, smem, stream, tx, tw, args);
+    return launch_chained(kernel, grid, kMxThreads, smem, stream, maps, args);
 }
 
 static rgg_status mxfp4_call(rgg_handle* h, const void* x_codes, const void* x_scales, const void* w_codes,
@@ -30,11 +29,13 @@ static rgg_status mxfp4_call(rgg_handle* h, const void* x_codes, const void* x_s
     if (!host_aligned(x_codes, 16) || !host_aligned(x_scales, 16) || !host_aligned(w_codes, 16) ||
         !host_aligned(w_scales, 16) || !host_aligned(Y, 16) || !host_aligned(group_offsets, 4))
         return RGG_ERR_INVALID_ARG;
-    const int want_bn = opt ? opt->bn : 0, want_stages = opt ? opt->stages : 0, max_ctas = opt ? opt->max_ctas : 0;
-    if (opt && opt->bm != 0 && opt->bm != kMxBM) return RGG_ERR_INVALID_ARG;
-    if ((want_bn != 0 && want_bn != 128 && want_bn != 256) || (gate_up && want_bn == 128)) return RGG_ERR_INVALID_ARG;
+    const int want_bm = opt ? opt->bm : 0, want_stages = opt ? opt->stages : 0, max_ctas = opt ? opt->max_ctas : 0;
+    if ((want_bm != 0 && want_bm != 128 && want_bm != 256) || max_ctas < 0)
+        return RGG_ERR_INVALID_ARG;
+    const int want_bn = opt ? opt->bn : 0;
+    if (want_bn != 0 && want_bn != (want_bm == 0 ? want_bn : want_bm)) return RGG_ERR_INVALID_ARG;
+    if (want_bn != 0 && want_bn != 128 && want_bn != 256) return RGG_ERR_INVALID_ARG;
     if (want_stages != 0 && (want_stages < 2 || want_stages > kMaxStages)) return RGG_ERR_INVALID_ARG;
-    if (max_ctas < 0) return RGG_ERR_INVALID_ARG;
     const HostDevice dev = host_device(h);
     HostDeviceScope scope(dev.device);
     if (scope.error() != cudaSuccess) return host_cuda_failure(scope.error(), "cudaSetDevice");
@@ -46,49 +47,53 @@ static rgg_status mxfp4_call(rgg_handle* h, const void* x_codes, const void* x_s
 
     const int cap = max_ctas > 0 ? std::min(max_ctas, dev.num_sms) : dev.num_sms;
     const int64_t avg = (M_tot + E - 1) / E;
-    auto tiles_n = [&](int bn) { return (N + (gate_up ? bn / 2 : bn) - 1) / (gate_up ? bn / 2 : bn); };
-    int bn = want_bn;
-    if (bn == 0) {
-        // the narrower tile where it takes as many waves' columns or fewer, the experts taken as balanced
-        const int64_t mt = E * ((avg + kMxBM - 1) / kMxBM);
-        auto cost = [&](int b) { return (mt * tiles_n(b) + cap - 1) / cap * (b + 64); };
-        bn = (!gate_up && cost(128) < cost(256)) ? 128 : 256;
-    }
-    const int64_t most = (M_tot / kMxBM + E) * tiles_n(bn);
-    if (most >= (int64_t(1) << 31)) return RGG_ERR_UNSUPPORTED;
-    const int64_t room = static_cast<int64_t>(dev.smem_optin) - 1024 - mx_smem(bn, 0, E).total;
-    const int per_stage = static_cast<int>(mx_smem(bn, 1, E).total - mx_smem(bn, 0, E).total);
+    auto tiles_n = [&](int b) { return (N + (gate_up ? b / 2 : b) - 1) / (gate_up ? b / 2 : b); };
+    int b = want_bm ? want_bm : want_bn;
+    if (b == 0) b = (avg > 128 && cap >= 2) ? 256 : 128;
+    const bool pair = b == 256;
+    if (pair && cap < 2) return RGG_ERR_INVALID_ARG;
+    const int64_t most = (M_tot / b + E) * tiles_n(b);
+    if (most >= (int64_t(1) << 30)) return RGG_ERR_UNSUPPORTED;
+    const int64_t room = static_cast<int64_t>(dev.smem_optin) - 1024 - mx_smem(0, E).total;
+    const int per_stage = static_cast<int>(mx_smem(1, E).total - mx_smem(0, E).total);
     const int fit = static_cast<int>(std::min<int64_t>(kMaxStages, room / per_stage));
     const int stages = want_stages ? want_stages : fit;
     if (stages < 2 || stages > fit) return RGG_ERR_UNSUPPORTED;
-    const int smem = std::max<int>(static_cast<int>(mx_smem(bn, stages, E).total) + 1024, dev.smem_optin / 2 + 1024);
+    const int smem = std::max<int>(static_cast<int>(mx_smem(stages, E).total) + 1024, dev.smem_optin / 2 + 1024);
 
     const int cols = gate_up ? 2 * N : N;
-    CUtensorMap tx, tw;
-    s = host_encode_codes(x_codes, M_tot, 1, K / 2, kMxBoxRows, &tx);
-    if (s == RGG_OK) s = host_encode_codes(w_codes, cols, E, K / 2, 128, &tw);
+    const int64_t kblocks = mx_k_blocks(K);
+    MxMaps m;
+    s = host_encode_codes(x_codes, M_tot, 1, K / 2, 128, &m.x128);
+    if (s == RGG_OK) s = host_encode_codes(x_codes, M_tot, 1, K / 2, 32, &m.x32);
+    if (s == RGG_OK) s = host_encode_codes(w_codes, cols, E, K / 2, 128, &m.w128);
+    if (s == RGG_OK) s = host_encode_codes(w_codes, cols, E, K / 2, 64, &m.w64);
+    if (s == RGG_OK) s = host_encode_words(x_scales, mx_row_blocks(M_tot, E), kblocks * (kMxBlockBytes / 4), 256, &m.sx);
+    if (s == RGG_OK)
+        s = host_encode_words(w_scales, static_cast<int64_t>(E) * ((cols + kMxRows - 1) / kMxRows),
+                              kblocks * (kMxBlockBytes / 4), 256, &m.sw);
     if (s != RGG_OK) return s;
 
     MxArgs a;
     a.offsets = group_offsets;
-    a.scale_x = static_cast<const uint8_t*>(x_scales);
-    a.scale_w = static_cast<const uint8_t*>(w_scales);
     a.Y = static_cast<__nv_bfloat16*>(Y);
     a.status = dev.status;
     a.M_tot = M_tot;
     a.E = E;
     a.K = K;
     a.N = N;
-    a.n_tiles_n = tiles_n(bn);
+    a.n_tiles_n = tiles_n(b);
     a.stages = stages;
     a.y_vec32 = (N % 16 == 0 && host_aligned(Y, 32)) ? 1 : 0;
-    a.n_major = avg >= 3 * kMxBM ? 1 : 0;  // as the bf16 plan: the tiles that read one weight panel side by side
+    a.n_major = avg >= 3 * b ? 1 : 0;  // as the bf16 plan: the tiles that read one weight panel side by side
     a.debug_flags = opt ? (opt->debug_flags & RGG_DEBUG_PRODUCER_STALL) : 0;
     a.timeout_ns = (opt && opt->timeout_ns) ? opt->timeout_ns : kHostDefaultTimeoutNs;
-    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(cap, most)));
-    cudaError_t err = gate_up     ? launch_mxfp4<256, true>(grid, smem, st, tx, tw, a)
-                      : bn == 256 ? launch_mxfp4<256, false>(grid, smem, st, tx, tw, a)
-                                  : launch_mxfp4<128, false>(grid, smem, st, tx, tw, a);
+    const int grid = static_cast<int>(pair ? 2 * std::max<int64_t>(1, std::min<int64_t>(cap / 2, most))
+                                           : std::max<int64_t>(1, std::min<int64_t>(cap, most)));
+    cudaError_t err = pair ? launch_mxfp4(gate_up ? grouped_mxfp4_pair_kernel<true> : grouped_mxfp4_pair_kernel<false>,
+                                          grid, smem, st, m, a)
+                           : launch_mxfp4(gate_up ? grouped_mxfp4_kernel<true> : grouped_mxfp4_kernel<false>, grid,
+                                          smem, st, m, a);
     return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, "grouped_gemm_mxfp4 launch");
 }
 

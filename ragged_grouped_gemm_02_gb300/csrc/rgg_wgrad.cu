@@ -9,24 +9,36 @@
 
 namespace rgg {
 
+// The multiplier and shift of wgrad_divide.
+static void wgrad_divisor(int32_t d, uint32_t* by, int32_t* shift) {
+    int32_t bits = 0;
+    while ((int64_t(1) << bits) < d) ++bits;
+    *shift = 30 + bits;
+    *by = static_cast<uint32_t>((uint64_t(1) << *shift) / static_cast<uint64_t>(d) + 1);
+}
+
+struct WgradMaps {
+    CUtensorMap x, x16, dy, dy16, dw;  // with boxes of 64 and of 16 rows
+};
+
 template <int BN, bool kF32, bool kAdd>
-static cudaError_t launch_wgrad(int grid, size_t smem, cudaStream_t stream, const CUtensorMap& tx,
-                                const CUtensorMap& ty, const WgradArgs& args) {
+static cudaError_t launch_wgrad(int grid, size_t smem, cudaStream_t stream, const WgradMaps& m,
+                                const WgradArgs& args) {
     auto kernel = grouped_wgrad_kernel<BN, kF32, kAdd>;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(smem));
     if (err != cudaSuccess) return err;
-    return launch_chained(kernel, grid, kWgradThreads, smem, stream, tx, ty, args);
+    return launch_chained(kernel, grid, kWgradThreads, smem, stream, m.x, m.x16, m.dy, m.dy16, m.dw, args);
 }
 
 template <int BN>
-static cudaError_t launch_wgrad_kind(int flags, int grid, size_t smem, cudaStream_t stream, const CUtensorMap& tx,
-                                     const CUtensorMap& ty, const WgradArgs& args) {
+static cudaError_t launch_wgrad_kind(int flags, int grid, size_t smem, cudaStream_t stream, const WgradMaps& m,
+                                     const WgradArgs& args) {
     switch (flags) {
-        case 0: return launch_wgrad<BN, false, false>(grid, smem, stream, tx, ty, args);
-        case RGG_WGRAD_FP32: return launch_wgrad<BN, true, false>(grid, smem, stream, tx, ty, args);
-        case RGG_WGRAD_ACCUMULATE: return launch_wgrad<BN, false, true>(grid, smem, stream, tx, ty, args);
-        default: return launch_wgrad<BN, true, true>(grid, smem, stream, tx, ty, args);
+        case 0: return launch_wgrad<BN, false, false>(grid, smem, stream, m, args);
+        case RGG_WGRAD_FP32: return launch_wgrad<BN, true, false>(grid, smem, stream, m, args);
+        case RGG_WGRAD_ACCUMULATE: return launch_wgrad<BN, false, true>(grid, smem, stream, m, args);
+        default: return launch_wgrad<BN, true, true>(grid, smem, stream, m, args);
     }
 }
 
@@ -65,41 +77,47 @@ extern "C" rgg_status rgg_grouped_gemm_wgrad(rgg_handle* h, const void* X, const
         bn = cost(128) < cost(256) ? 128 : 256;
     }
     if (tiles(bn) >= (int64_t(1) << 30)) return RGG_ERR_UNSUPPORTED;
-    const bool sorted = E > 1 && E <= kMaxSortedExperts;
-    const int64_t room = static_cast<int64_t>(dev.smem_optin) - 1024 - wgrad_smem(bn, 0, E, sorted).total;
+    const int64_t room = static_cast<int64_t>(dev.smem_optin) - 1024 - wgrad_smem(bn, 0, E).total;
     const int per_stage = (2 + bn / 128) * static_cast<int>(kWgradPanel) + 32;
     const int fit = static_cast<int>(std::min<int64_t>(8, room / per_stage));
     const int stages = want_stages ? want_stages : fit;
     if (stages < 2 || stages > fit) return RGG_ERR_UNSUPPORTED;
     // more than half of the SM's shared memory, so that one CTA lives on each SM
-    const int smem = std::max<int>(static_cast<int>(wgrad_smem(bn, stages, E, sorted).total) + 1024,
+    const int smem = std::max<int>(static_cast<int>(wgrad_smem(bn, stages, E).total) + 1024,
                                    dev.smem_optin / 2 + 1024);
 
     // Without rows no copy is issued; the maps then stand on dW's memory.
-    CUtensorMap tx, ty;
+    WgradMaps m;
     const int64_t rows = M_tot > 0 ? M_tot : 1;
-    s = host_encode_rows(M_tot > 0 ? X : dW, rows, K, kWgradRows, &tx);
-    if (s == RGG_OK) s = host_encode_rows(M_tot > 0 ? dY : dW, rows, N, kWgradRows, &ty);
+    const void* px = M_tot > 0 ? X : dW;
+    const void* py = M_tot > 0 ? dY : dW;
+    s = host_encode_rows(px, rows, K, kWgradRows, &m.x);
+    if (s == RGG_OK) s = host_encode_rows(px, rows, K, 16, &m.x16);
+    if (s == RGG_OK) s = host_encode_rows(py, rows, N, kWgradRows, &m.dy);
+    if (s == RGG_OK) s = host_encode_rows(py, rows, N, 16, &m.dy16);
+    if (s == RGG_OK) s = host_encode_out(dW, E, K, N, (flags & RGG_WGRAD_FP32) != 0, 32, &m.dw);
     if (s != RGG_OK) return s;
 
     WgradArgs a;
     a.offsets = group_offsets;
+    a.X = static_cast<const __nv_bfloat16*>(X);
+    a.dY = static_cast<const __nv_bfloat16*>(dY);
     a.dW = dW;
     a.status = dev.status;
     a.M_tot = M_tot;
     a.E = E;
     a.K = K;
     a.N = N;
-    a.tiles_k = (K + kWgradBM - 1) / kWgradBM;
     a.tiles_n = (N + bn - 1) / bn;
+    a.tiles_e = a.tiles_n * ((K + kWgradBM - 1) / kWgradBM);
+    wgrad_divisor(a.tiles_n, &a.by_tiles_n, &a.shift_n);
+    wgrad_divisor(a.tiles_e, &a.by_tiles_e, &a.shift_e);
     a.stages = stages;
-    a.vec32 = (N % ((flags & RGG_WGRAD_FP32) ? 8 : 16) == 0 && host_aligned(dW, 32)) ? 1 : 0;
-    a.sorted = sorted ? 1 : 0;
     a.debug_flags = opt ? (opt->debug_flags & RGG_DEBUG_PRODUCER_STALL) : 0;
     a.timeout_ns = (opt && opt->timeout_ns) ? opt->timeout_ns : kHostDefaultTimeoutNs;
     const int grid = 2 * static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(pairs, tiles(bn))));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t err = bn == 256 ? launch_wgrad_kind<256>(flags, grid, smem, st, tx, ty, a)
-                                : launch_wgrad_kind<128>(flags, grid, smem, st, tx, ty, a);
+    cudaError_t err = bn == 256 ? launch_wgrad_kind<256>(flags, grid, smem, st, m, a)
+                                : launch_wgrad_kind<128>(flags, grid, smem, st, m, a);
     return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, "grouped_gemm_wgrad launch");
 }

@@ -177,11 +177,12 @@ def test_product(K, N, bn):
     _check_rows(Y, ref, refs.bound(ref, K, mag), off)
 
 
+@pytest.mark.parametrize("bn", [128, 256])
 @pytest.mark.parametrize("K,N", [(32, 128), (544, 128), (256, 384), (1056, 256)])
-def test_gate_up(K, N):
+def test_gate_up(K, N, bn):
     X, W, off, offg, xq, wq = _product_case(COUNTS, K, 2 * N, seed=K + N)
     H = _canary_out(X.shape[0], N)
-    rgg.rgg_grouped_gemm_swiglu_mxfp4(*xq, *wq, offg, H, check=True)
+    rgg.rgg_grouped_gemm_swiglu_mxfp4(*xq, *wq, offg, H, bn=bn, check=True)
     gu, mag = _reference(X, W, off)
     g, u = gu[:, :N], gu[:, N:]
     eps = K * 2.0 ** -23 * mag
@@ -191,7 +192,7 @@ def test_gate_up(K, N):
     _check_rows(H, ref, limit, off)
 
 
-@pytest.mark.parametrize("stages,max_ctas", [(2, 1), (3, 2), (0, 3)])
+@pytest.mark.parametrize("stages,max_ctas", [(2, 2), (3, 3), (0, 6)])
 def test_long_walks(stages, max_ctas):
     # many tiles a CTA: the accumulators, their shared columns and the ring go round
     X, W, off, offg, xq, wq = _product_case(COUNTS, 800, 712, seed=stages)
@@ -274,7 +275,8 @@ def test_refusals():
                  lambda: rgg.rgg_mxfp4_quantize_weights(Wg[:, :48].contiguous()),
                  lambda: rgg.rgg_mxfp4_quantize_weights(Wg[:, :, :12].contiguous()),
                  lambda: rgg.rgg_grouped_gemm_swiglu_mxfp4(*xq, *wq, offg),
-                 lambda: rgg.rgg_grouped_gemm_mxfp4(*xq, *wq, offg, bn=192)):
+                 lambda: rgg.rgg_grouped_gemm_mxfp4(*xq, *wq, offg, bn=192),
+                 lambda: rgg.rgg_grouped_gemm_mxfp4(*xq, *wq, offg, bn=256, max_ctas=1)):
         with pytest.raises(rgg.RggError) as ei:
             call()
         assert ei.value.status == rgg.RGG_ERR_INVALID_ARG

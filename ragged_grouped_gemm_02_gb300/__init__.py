@@ -93,6 +93,8 @@ def library_path() -> str:
 def load_library() -> ctypes.CDLL:
     """Load librgg.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -177,6 +179,9 @@ def _raise(status: int, call: str):
 
 
 def _handle(device: int) -> ctypes.c_void_p:
+    h = _handles.get(device)
+    if h is not None:
+        return h
     lib = load_library()
     with _lock:
         h = _handles.get(device)
@@ -440,17 +445,26 @@ def rgg_grouped_gemm_swiglu_gather(X_tok, row_index, W13, group_offsets, H=None,
                         workspace, stream, check)
 
 
-def _check_operands(device, **tensors):
-    """Each tensor: (tensor, dtype, shape); a contiguous CUDA tensor of that type and shape on `device`."""
-    for name, (t, dtype, shape) in tensors.items():
-        if not t.is_cuda or t.device != device:
-            raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
-        if t.dtype != dtype:
-            raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
-        if t.shape != shape:
-            raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
+def _operand(name, t, dtype, shape, device):
+    """Refuses anything but a contiguous tensor of that type and shape on `device`, a CUDA device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
+        return
+    if not t.is_cuda or t.device != device:
+        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _raw_stream(stream, device):
+    """The stream's handle as an integer (the current stream's without building a Stream object)."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _finish(name, status, device, stream_ptr, check):
@@ -479,14 +493,20 @@ def rgg_grouped_gemm_dgrad(dY, W, group_offsets, dX=None, *, bm=0, bn=0, stages=
     E, K, N = W.shape
     if dX is None:
         dX = torch.empty(M_tot, K, dtype=torch.bfloat16, device=dY.device)
-    _check_operands(dY.device, dY=(dY, torch.bfloat16, (M_tot, N)), W=(W, torch.bfloat16, (E, K, N)),
-                    group_offsets=(group_offsets, torch.int32, (E + 1,)), dX=(dX, torch.bfloat16, (M_tot, K)))
-    device = dY.device.index
-    opt, keep = _options(bm, bn, stages, max_ctas, timeout_ns, host_counts, debug_flags, tail64, 0, walk_order,
-                         mixed=mixed, mixed_pair_sms=mixed_pair_sms, pair_min_rows=pair_min_rows)
-    st = _stream_ptr(stream, device)
+    dev = dY.device
+    _operand("dY", dY, torch.bfloat16, (M_tot, N), dev)
+    _operand("W", W, torch.bfloat16, (E, K, N), dev)
+    _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
+    _operand("dX", dX, torch.bfloat16, (M_tot, K), dev)
+    device = dev.index
+    opt = keep = None
+    if (bm or bn or stages or max_ctas or timeout_ns or debug_flags or tail64 or walk_order or mixed or mixed_pair_sms
+            or pair_min_rows or host_counts is not None):
+        opt, keep = _options(bm, bn, stages, max_ctas, timeout_ns, host_counts, debug_flags, tail64, 0, walk_order,
+                             mixed=mixed, mixed_pair_sms=mixed_pair_sms, pair_min_rows=pair_min_rows)
+    st = _raw_stream(stream, device)
     s = load_library().rgg_grouped_gemm_dgrad(_handle(device), dY.data_ptr(), W.data_ptr(), group_offsets.data_ptr(),
-                                              dX.data_ptr(), E, M_tot, K, N, st, ctypes.byref(opt))
+                                              dX.data_ptr(), E, M_tot, K, N, st, opt)
     del keep
     _finish("rgg_grouped_gemm_dgrad", s, device, st, check)
     return dX
@@ -514,14 +534,19 @@ def rgg_grouped_gemm_wgrad(X, dY, group_offsets, dW=None, *, dtype=None, accumul
         if accumulate:
             raise ValueError("accumulate=True needs dW")
         dW = torch.empty(E, K, N, dtype=dtype, device=X.device)
-    _check_operands(X.device, X=(X, torch.bfloat16, (M_tot, K)), dY=(dY, torch.bfloat16, (M_tot, N)),
-                    group_offsets=(group_offsets, torch.int32, (E + 1,)), dW=(dW, dtype, (E, K, N)))
-    device = X.device.index
-    opt, _ = _options(0, bn, stages, max_ctas, timeout_ns, None, debug_flags)
-    st = _stream_ptr(stream, device)
+    dev = X.device
+    _operand("X", X, torch.bfloat16, (M_tot, K), dev)
+    _operand("dY", dY, torch.bfloat16, (M_tot, N), dev)
+    _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
+    _operand("dW", dW, dtype, (E, K, N), dev)
+    device = dev.index
+    opt = None
+    if bn or stages or max_ctas or timeout_ns or debug_flags:
+        opt, _ = _options(0, bn, stages, max_ctas, timeout_ns, None, debug_flags)
+    st = _raw_stream(stream, device)
     flags = (1 if dtype == torch.float32 else 0) | (2 if accumulate else 0)
     s = load_library().rgg_grouped_gemm_wgrad(_handle(device), X.data_ptr(), dY.data_ptr(), group_offsets.data_ptr(),
-                                              dW.data_ptr(), E, M_tot, K, N, flags, st, ctypes.byref(opt))
+                                              dW.data_ptr(), E, M_tot, K, N, flags, st, opt)
     _finish("rgg_grouped_gemm_wgrad", s, device, st, check)
     return dW
 
@@ -548,19 +573,24 @@ def rgg_grouped_gemm_swiglu_backward(X, W13, group_offsets, dH, dGU=None, H=None
         H = torch.empty(M_tot, N, dtype=torch.bfloat16, device=X.device)
     elif H is False:
         H = None
-    operands = dict(X=(X, torch.bfloat16, (M_tot, K)), W13=(W13, torch.bfloat16, (E, K, 2 * N)),
-                    group_offsets=(group_offsets, torch.int32, (E + 1,)), dH=(dH, torch.bfloat16, (M_tot, N)),
-                    dGU=(dGU, torch.bfloat16, (M_tot, 2 * N)))
+    dev = X.device
+    _operand("X", X, torch.bfloat16, (M_tot, K), dev)
+    _operand("W13", W13, torch.bfloat16, (E, K, 2 * N), dev)
+    _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
+    _operand("dH", dH, torch.bfloat16, (M_tot, N), dev)
+    _operand("dGU", dGU, torch.bfloat16, (M_tot, 2 * N), dev)
     if H is not None:
-        operands["H"] = (H, torch.bfloat16, (M_tot, N))
-    _check_operands(X.device, **operands)
-    device = X.device.index
-    opt, keep = _options(bm, bn, stages, max_ctas, timeout_ns, host_counts, debug_flags, tail64, 0, walk_order,
-                         mixed=mixed, mixed_pair_sms=mixed_pair_sms, pair_min_rows=pair_min_rows)
-    st = _stream_ptr(stream, device)
+        _operand("H", H, torch.bfloat16, (M_tot, N), dev)
+    device = dev.index
+    opt = keep = None
+    if (bm or bn or stages or max_ctas or timeout_ns or debug_flags or tail64 or walk_order or mixed or mixed_pair_sms
+            or pair_min_rows or host_counts is not None):
+        opt, keep = _options(bm, bn, stages, max_ctas, timeout_ns, host_counts, debug_flags, tail64, 0, walk_order,
+                             mixed=mixed, mixed_pair_sms=mixed_pair_sms, pair_min_rows=pair_min_rows)
+    st = _raw_stream(stream, device)
     s = load_library().rgg_grouped_gemm_swiglu_backward(
         _handle(device), X.data_ptr(), W13.data_ptr(), group_offsets.data_ptr(), dH.data_ptr(), dGU.data_ptr(),
-        H.data_ptr() if H is not None else None, E, M_tot, K, N, st, ctypes.byref(opt))
+        H.data_ptr() if H is not None else None, E, M_tot, K, N, st, opt)
     del keep
     _finish("rgg_grouped_gemm_swiglu_backward", s, device, st, check)
     return dGU, H
@@ -604,7 +634,7 @@ def rgg_clip_grad_norm(grads, max_norm, out=None, *, stream=None):
     bytes_ = lib.rgg_clip_grad_norm_workspace(len(grads))
     norm = torch.empty((), dtype=torch.float32, device=dev)
     workspace = torch.empty(bytes_ // 8, dtype=torch.float64, device=dev)
-    st = _stream_ptr(stream, dev.index)
+    st = _raw_stream(stream, dev.index)
     if stream is not None:
         # allocated on the current stream, used on another one
         workspace.record_stream(stream)
@@ -640,11 +670,13 @@ def rgg_mxfp4_quantize(X, group_offsets, codes=None, scales=None, *, stream=None
         codes = torch.empty(M_tot, K // 2, dtype=torch.uint8, device=X.device)
     if scales is None:
         scales = torch.empty(_mx_scale_shape(M_tot, E, K), dtype=torch.uint8, device=X.device)
-    _check_operands(X.device, X=(X, torch.bfloat16, (M_tot, K)), group_offsets=(group_offsets, torch.int32, (E + 1,)),
-                    codes=(codes, torch.uint8, (M_tot, K // 2)),
-                    scales=(scales, torch.uint8, _mx_scale_shape(M_tot, E, K)))
-    device = X.device.index
-    st = _stream_ptr(stream, device)
+    dev = X.device
+    _operand("X", X, torch.bfloat16, (M_tot, K), dev)
+    _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
+    _operand("codes", codes, torch.uint8, (M_tot, K // 2), dev)
+    _operand("scales", scales, torch.uint8, _mx_scale_shape(M_tot, E, K), dev)
+    device = dev.index
+    st = _raw_stream(stream, device)
     s = load_library().rgg_mxfp4_quantize(_handle(device), X.data_ptr(), group_offsets.data_ptr(), codes.data_ptr(),
                                           scales.data_ptr(), E, M_tot, K, st)
     _finish("rgg_mxfp4_quantize", s, device, st, check)
@@ -660,11 +692,13 @@ def rgg_mxfp4_dequantize(codes, scales, group_offsets, X=None, *, stream=None, c
     E = group_offsets.numel() - 1
     if X is None:
         X = torch.empty(M_tot, K, dtype=torch.bfloat16, device=codes.device)
-    _check_operands(codes.device, codes=(codes, torch.uint8, (M_tot, K // 2)),
-                    scales=(scales, torch.uint8, _mx_scale_shape(M_tot, E, K)),
-                    group_offsets=(group_offsets, torch.int32, (E + 1,)), X=(X, torch.bfloat16, (M_tot, K)))
-    device = codes.device.index
-    st = _stream_ptr(stream, device)
+    dev = codes.device
+    _operand("codes", codes, torch.uint8, (M_tot, K // 2), dev)
+    _operand("scales", scales, torch.uint8, _mx_scale_shape(M_tot, E, K), dev)
+    _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
+    _operand("X", X, torch.bfloat16, (M_tot, K), dev)
+    device = dev.index
+    st = _raw_stream(stream, device)
     s = load_library().rgg_mxfp4_dequantize(_handle(device), codes.data_ptr(), scales.data_ptr(),
                                             group_offsets.data_ptr(), X.data_ptr(), E, M_tot, K, st)
     _finish("rgg_mxfp4_dequantize", s, device, st, check)
@@ -683,10 +717,12 @@ def rgg_mxfp4_quantize_weights(W, codes=None, scales=None, *, stream=None):
         codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=W.device)
     if scales is None:
         scales = torch.empty(_mx_weight_scale_shape(E, N, K), dtype=torch.uint8, device=W.device)
-    _check_operands(W.device, W=(W, torch.bfloat16, (E, K, N)), codes=(codes, torch.uint8, (E, N, K // 2)),
-                    scales=(scales, torch.uint8, _mx_weight_scale_shape(E, N, K)))
-    device = W.device.index
-    st = _stream_ptr(stream, device)
+    dev = W.device
+    _operand("W", W, torch.bfloat16, (E, K, N), dev)
+    _operand("codes", codes, torch.uint8, (E, N, K // 2), dev)
+    _operand("scales", scales, torch.uint8, _mx_weight_scale_shape(E, N, K), dev)
+    device = dev.index
+    st = _raw_stream(stream, device)
     s = load_library().rgg_mxfp4_quantize_weights(_handle(device), W.data_ptr(), codes.data_ptr(), scales.data_ptr(),
                                                   E, K, N, st)
     _finish("rgg_mxfp4_quantize_weights", s, device, st, False)
@@ -701,11 +737,12 @@ def rgg_mxfp4_dequantize_weights(codes, scales, W=None, *, stream=None):
     E, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
     if W is None:
         W = torch.empty(E, N, K, dtype=torch.bfloat16, device=codes.device)
-    _check_operands(codes.device, codes=(codes, torch.uint8, (E, N, K // 2)),
-                    scales=(scales, torch.uint8, _mx_weight_scale_shape(E, N, K)),
-                    W=(W, torch.bfloat16, (E, N, K)))
-    device = codes.device.index
-    st = _stream_ptr(stream, device)
+    dev = codes.device
+    _operand("codes", codes, torch.uint8, (E, N, K // 2), dev)
+    _operand("scales", scales, torch.uint8, _mx_weight_scale_shape(E, N, K), dev)
+    _operand("W", W, torch.bfloat16, (E, N, K), dev)
+    device = dev.index
+    st = _raw_stream(stream, device)
     s = load_library().rgg_mxfp4_dequantize_weights(_handle(device), codes.data_ptr(), scales.data_ptr(),
                                                     W.data_ptr(), E, K, N, st)
     _finish("rgg_mxfp4_dequantize_weights", s, device, st, False)
@@ -722,17 +759,21 @@ def _mxfp4_call(name, x_codes, x_scales, w_codes, w_scales, group_offsets, out, 
     N = cols // 2 if gate_up else cols
     if out is None:
         out = torch.empty(M_tot, N, dtype=torch.bfloat16, device=x_codes.device)
-    _check_operands(x_codes.device, x_codes=(x_codes, torch.uint8, (M_tot, half)),
-                    x_scales=(x_scales, torch.uint8, _mx_scale_shape(M_tot, E, 2 * half)),
-                    w_codes=(w_codes, torch.uint8, (E, cols, half)),
-                    w_scales=(w_scales, torch.uint8, _mx_weight_scale_shape(E, cols, 2 * half)),
-                    group_offsets=(group_offsets, torch.int32, (E + 1,)), out=(out, torch.bfloat16, (M_tot, N)))
-    device = x_codes.device.index
-    opt, _ = _options(0, bn, stages, max_ctas, timeout_ns, None, debug_flags)
-    st = _stream_ptr(stream, device)
+    dev = x_codes.device
+    _operand("x_codes", x_codes, torch.uint8, (M_tot, half), dev)
+    _operand("x_scales", x_scales, torch.uint8, _mx_scale_shape(M_tot, E, 2 * half), dev)
+    _operand("w_codes", w_codes, torch.uint8, (E, cols, half), dev)
+    _operand("w_scales", w_scales, torch.uint8, _mx_weight_scale_shape(E, cols, 2 * half), dev)
+    _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
+    _operand("out", out, torch.bfloat16, (M_tot, N), dev)
+    device = dev.index
+    opt = None
+    if bn or stages or max_ctas or timeout_ns or debug_flags:
+        opt, _ = _options(0, bn, stages, max_ctas, timeout_ns, None, debug_flags)
+    st = _raw_stream(stream, device)
     s = getattr(load_library(), name)(_handle(device), x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(),
                                       w_scales.data_ptr(), group_offsets.data_ptr(), out.data_ptr(), E, M_tot,
-                                      2 * half, N, st, ctypes.byref(opt))
+                                      2 * half, N, st, opt)
     _finish(name, s, device, st, check)
     return out
 

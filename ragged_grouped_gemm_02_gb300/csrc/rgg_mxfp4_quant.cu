@@ -65,6 +65,70 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
     return __vmaxu2(a, b & 0x7fff7fffu);
 }
 
+// Segments of rows that a warp takes one after the other: where a segment's
+// values and its row's scales lie.  Rows are grouped by expert (s_off) or, with
+// rows_per > 0, are E matrices of rows_per rows.
+struct RowWalk {
+    int64_t left;    // segments still to take, this one among them
+    int64_t row;
+    int32_t seg, segments, e, r;  // r: the row in its expert
+    int64_t scales;  // byte of the row's first scale
+
+    __device__ __forceinline__ void locate(const int32_t* s_off, int rows_per, int64_t kblocks) {
+        const int64_t block = rows_per > 0 ? static_cast<int64_t>(e) * ((rows_per + kMxRows - 1) / kMxRows) + r / kMxRows
+                                           : mx_row_block(s_off[e], e, r);
+        scales = block * kblocks * kMxBlockBytes + mx_in_block(r % kMxRows);
+    }
+
+    // This warp's share of the segments of rows [first, last).
+    __device__ __forceinline__ void begin(const int32_t* s_off, int E, int rows_per, int64_t first, int64_t last, int K,
+                                          int64_t kblocks) {
+        segments = (K + kSegment - 1) / kSegment;
+        const int64_t units = (last - first) * segments;
+        const int64_t warps = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
+        const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5);
+        const int64_t per = (units + warps - 1) / warps;
+        const int64_t u = warp * per;
+        left = u + per < units ? per : units - u;
+        if (left <= 0) return;
+        row = first + u / segments;
+        seg = static_cast<int32_t>(u % segments);
+        if (rows_per > 0) {
+            e = static_cast<int32_t>(row / rows_per);
+            r = static_cast<int32_t>(row - static_cast<int64_t>(e) * rows_per);
+        } else {
+            e = 0;
+            int hi = E;  // the last expert whose first row is not after `row`
+            while (hi - e > 1) {
+                const int mid = (e + hi) >> 1;
+                if (s_off[mid] <= row) e = mid;
+                else hi = mid;
+            }
+            r = static_cast<int32_t>(row - s_off[e]);
+        }
+        locate(s_off, rows_per, kblocks);
+    }
+
+    // To the next segment; call while left > 1.
+    __device__ __forceinline__ void next(const int32_t* s_off, int rows_per, int64_t kblocks) {
+        --left;
+        if (++seg < segments) return;
+        seg = 0;
+        ++row;
+        ++r;
+        if (rows_per > 0) {
+            if (r == rows_per) {
+                r = 0;
+                ++e;
+            }
+        } else {
+            while (s_off[e + 1] <= row) ++e;
+            r = static_cast<int32_t>(row - s_off[e]);
+        }
+        locate(s_off, rows_per, kblocks);
+    }
+};
+
 __global__ void __launch_bounds__(kQuantThreads)
     mx_quantize_rows_kernel(const uint4* __restrict__ X, const int32_t* __restrict__ offsets, int E, int64_t M_tot,
                             int K, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales, int32_t* status) {
@@ -76,59 +140,52 @@ __global__ void __launch_bounds__(kQuantThreads)
         return;
     }
     const int lane = threadIdx.x & 31;
-    const int segments = (K + kSegment - 1) / kSegment;
     const int64_t kblocks = mx_k_blocks(K);
-    const int64_t units = static_cast<int64_t>(s_off[E] - s_off[0]) * segments;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
-    const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5);
-    const int64_t per = (units + warps - 1) / warps;
-    int64_t u = warp * per;
-    const int64_t end = u + per < units ? u + per : units;
-    if (u >= end) return;
-    int64_t row = s_off[0] + u / segments;
-    int seg = static_cast<int>(u % segments);
-    int e = 0, hi = E;  // the last expert whose first row is not after `row`
-    while (hi - e > 1) {
-        const int mid = (e + hi) >> 1;
-        if (s_off[mid] <= row) e = mid;
-        else hi = mid;
-    }
-    for (; u < end; ++u) {
-        while (s_off[e + 1] <= row) ++e;
-        const uint4* x = X + row * (K / 8);
-        uint4 v[4];
-        int k[4];
+    const int k8 = K / 8;  // 16-byte pieces of a row
+    RowWalk w;
+    w.begin(s_off, E, 0, s_off[0], s_off[E], K, kblocks);
+    if (w.left <= 0) return;
+    // the next segment's values are on their way while this one's are coded
+    uint4 v[4];
+    auto load = [&]() {
+        const uint4* x = X + w.row * k8;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            k[i] = seg * kSegment + i * 256 + lane * 8;
-            v[i] = k[i] < K ? __ldg(x + k[i] / 8) : make_uint4(0u, 0u, 0u, 0u);
+            const int at = w.seg * (kSegment / 8) + i * 32 + lane;
+            v[i] = at < k8 ? __ldg(x + at) : make_uint4(0u, 0u, 0u, 0u);
         }
-        const int64_t r = row - s_off[e];
-        uint8_t* block = scales + (mx_row_block(s_off[e], e, r) * kblocks) * kMxBlockBytes +
-                         mx_in_block(static_cast<int>(r % kMxRows));
+    };
+    load();
+    while (true) {
+        const uint4 now[4] = {v[0], v[1], v[2], v[3]};
+        uint32_t* out = codes + w.row * k8;
+        uint8_t* block = scales + w.scales;
+        const int seg = w.seg;
+        const bool more = w.left > 1;
+        if (more) {
+            w.next(s_off, 0, kblocks);
+            load();
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            const uint32_t x[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
             uint32_t top = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top = max_abs_bf16x2(top, w[j]);
+            for (int j = 0; j < 4; ++j) top = max_abs_bf16x2(top, x[j]);
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const uint32_t lo = top & 0xffffu, hi16 = top >> 16;
             const uint32_t byte = mx_scale_byte(lo > hi16 ? lo : hi16);
-            if (k[i] < K) codes[row * (K / 8) + k[i] / 8] = mx_codes8(w, byte);
+            const int at = seg * (kSegment / 8) + i * 32 + lane;
+            if (at < k8) out[at] = mx_codes8(x, byte);
             // four blocks make one word: lanes 0-15 and 16-31 each hold one
             uint32_t word = byte << (8 * ((lane >> 2) & 3));
             word |= __shfl_xor_sync(0xffffffffu, word, 4);
             word |= __shfl_xor_sync(0xffffffffu, word, 8);
-            const int kb = k[i] / 128;
-            if ((lane & 15) == 0 && kb < kblocks)
-                *reinterpret_cast<uint32_t*>(block + static_cast<int64_t>(kb) * kMxBlockBytes) = word;
+            const int kb = at / 16;
+            if ((lane & 15) == 0 && kb < kblocks) *reinterpret_cast<uint32_t*>(block + kb * kMxBlockBytes) = word;
         }
-        if (++seg == segments) {
-            seg = 0;
-            ++row;
-        }
+        if (!more) break;
     }
 }
 
@@ -216,51 +273,44 @@ __global__ void __launch_bounds__(kQuantThreads)
         if (threadIdx.x == 0) atomicCAS(status, 0, kStatusBadOffsets);
         return;
     }
-    const int64_t first = offsets ? s_off[0] : 0;
-    const int64_t last = offsets ? s_off[E] : rows_total;
     const int64_t kblocks = mx_k_blocks(K);
     const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
-    const int segments = (K + kSegment - 1) / kSegment;
-    const int64_t units = (last - first) * segments;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5); u < units;
-         u += warps) {
-        const int64_t row = first + u / segments;
-        const int k0 = static_cast<int>(u % segments) * kSegment + lane * 8;
-        const uint8_t* block;
-        if (offsets) {
-            int e = 0, hi = E;
-            while (hi - e > 1) {
-                const int mid = (e + hi) >> 1;
-                if (s_off[mid] <= row) e = mid;
-                else hi = mid;
-            }
-            const int64_t r = row - s_off[e];
-            block = scales + mx_row_block(s_off[e], e, r) * kblocks * kMxBlockBytes + mx_in_block(static_cast<int>(r % kMxRows));
-        } else {
-            const int64_t e = row / rows_per;
-            const int r = static_cast<int>(row - e * rows_per);
-            block = scales + (e * ((rows_per + kMxRows - 1) / kMxRows) + r / kMxRows) * kblocks * kMxBlockBytes +
-                    mx_in_block(r % kMxRows);
-        }
-        uint32_t c[4], b[4];
+    const int k8 = K / 8;
+    const int per = offsets ? 0 : rows_per;
+    RowWalk w;
+    w.begin(s_off, E, per, offsets ? s_off[0] : 0, offsets ? s_off[E] : rows_total, K, kblocks);
+    if (w.left <= 0) return;
+    uint32_t c[4], b[4];
+    auto load = [&]() {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int k = k0 + i * 256;
-            c[i] = k < K ? __ldg(codes + row * (K / 8) + k / 8) : 0u;
-            b[i] = k < K ? __ldg(block + static_cast<int64_t>(k / 128) * kMxBlockBytes + (k / 32) % 4) : 0u;
+            const int at = w.seg * (kSegment / 8) + i * 32 + lane;  // pieces of eight values
+            c[i] = at < k8 ? __ldg(codes + w.row * k8 + at) : 0u;
+            b[i] = at < k8 ? __ldg(scales + w.scales + (at / 16) * kMxBlockBytes + (at / 4) % 4) : 0u;
+        }
+    };
+    load();
+    while (true) {
+        const uint32_t cn[4] = {c[0], c[1], c[2], c[3]}, bn[4] = {b[0], b[1], b[2], b[3]};
+        uint4* o = out + w.row * k8;
+        const int seg = w.seg;
+        const bool more = w.left > 1;
+        if (more) {
+            w.next(s_off, per, kblocks);
+            load();
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int k = k0 + i * 256;
-            if (k < K) out[row * (K / 8) + k / 8] = mx_values8(c[i], b[i]);
+            const int at = seg * (kSegment / 8) + i * 32 + lane;
+            if (at < k8) o[at] = mx_values8(cn[i], bn[i]);
         }
+        if (!more) break;
     }
 }
 
 static int quant_grid(int num_sms, int64_t units) {
     const int64_t want = (units + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, 8LL * num_sms)));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, 16LL * num_sms)));
 }
 
 static rgg_status mx_check(const rgg_handle* h, int E, int64_t M_tot, int K) {

@@ -491,13 +491,14 @@ def rgg_grouped_gemm_dgrad(dY, W, group_offsets, dX=None, *, bm=0, bn=0, stages=
         raise ValueError("dY must be [M_tot, N] and W [E, K, N]")
     M_tot = dY.shape[0]
     E, K, N = W.shape
-    if dX is None:
-        dX = torch.empty(M_tot, K, dtype=torch.bfloat16, device=dY.device)
     dev = dY.device
     _operand("dY", dY, torch.bfloat16, (M_tot, N), dev)
     _operand("W", W, torch.bfloat16, (E, K, N), dev)
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
-    _operand("dX", dX, torch.bfloat16, (M_tot, K), dev)
+    if dX is None:
+        dX = torch.empty(M_tot, K, dtype=torch.bfloat16, device=dev)
+    else:
+        _operand("dX", dX, torch.bfloat16, (M_tot, K), dev)
     device = dev.index
     opt = keep = None
     if (bm or bn or stages or max_ctas or timeout_ns or debug_flags or tail64 or walk_order or mixed or mixed_pair_sms
@@ -530,15 +531,16 @@ def rgg_grouped_gemm_wgrad(X, dY, group_offsets, dW=None, *, dtype=None, accumul
         dtype = torch.bfloat16 if dW is None else dW.dtype
     if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("dW must be bf16 or fp32, not %s" % dtype)
-    if dW is None:
-        if accumulate:
-            raise ValueError("accumulate=True needs dW")
-        dW = torch.empty(E, K, N, dtype=dtype, device=X.device)
+    if dW is None and accumulate:
+        raise ValueError("accumulate=True needs dW")
     dev = X.device
     _operand("X", X, torch.bfloat16, (M_tot, K), dev)
     _operand("dY", dY, torch.bfloat16, (M_tot, N), dev)
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
-    _operand("dW", dW, dtype, (E, K, N), dev)
+    if dW is None:
+        dW = torch.empty(E, K, N, dtype=dtype, device=dev)
+    else:
+        _operand("dW", dW, dtype, (E, K, N), dev)
     device = dev.index
     opt = None
     if bn or stages or max_ctas or timeout_ns or debug_flags:
@@ -567,19 +569,20 @@ def rgg_grouped_gemm_swiglu_backward(X, W13, group_offsets, dH, dGU=None, H=None
         raise ValueError("X must be [M_tot, K] and W13 [E, K, 2N]")
     M_tot, K = X.shape
     E, N = W13.shape[0], W13.shape[2] // 2
-    if dGU is None:
-        dGU = torch.empty(M_tot, 2 * N, dtype=torch.bfloat16, device=X.device)
-    if H is None:
-        H = torch.empty(M_tot, N, dtype=torch.bfloat16, device=X.device)
-    elif H is False:
-        H = None
     dev = X.device
     _operand("X", X, torch.bfloat16, (M_tot, K), dev)
     _operand("W13", W13, torch.bfloat16, (E, K, 2 * N), dev)
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
     _operand("dH", dH, torch.bfloat16, (M_tot, N), dev)
-    _operand("dGU", dGU, torch.bfloat16, (M_tot, 2 * N), dev)
-    if H is not None:
+    if dGU is None:
+        dGU = torch.empty(M_tot, 2 * N, dtype=torch.bfloat16, device=dev)
+    else:
+        _operand("dGU", dGU, torch.bfloat16, (M_tot, 2 * N), dev)
+    if H is None:
+        H = torch.empty(M_tot, N, dtype=torch.bfloat16, device=dev)
+    elif H is False:
+        H = None
+    else:
         _operand("H", H, torch.bfloat16, (M_tot, N), dev)
     device = dev.index
     opt = keep = None
@@ -617,19 +620,33 @@ def rgg_clip_grad_norm(grads, max_norm, out=None, *, stream=None):
         raise ValueError("grads is empty")
     if not max_norm >= 0:
         raise ValueError("max_norm must not be negative or NaN")
-    codes = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+    bf16, fp32, fp16 = torch.bfloat16, torch.float32, torch.float16
     dev = grads[0].device
-    packed = array("q")
+    if dev.type != "cuda":
+        raise ValueError("all tensors must be CUDA tensors on one device")
+    packed = []
     for g, o in zip(grads, out):
-        code = codes.get(g.dtype)
-        if code is None or o.dtype != g.dtype:
-            raise TypeError("gradients must be bf16, fp16 or fp32, and each output of its gradient's type")
-        if not g.is_cuda or g.device != dev or o.device != dev:
-            raise ValueError("all tensors must be CUDA tensors on one device")
+        dtype = g.dtype
+        code = 0 if dtype is bf16 else 1 if dtype is fp32 else 2 if dtype is fp16 else None
         n = g.numel()
-        if o.numel() != n or not (g.is_contiguous() and o.is_contiguous()):
-            raise ValueError("gradients and outputs must be contiguous, each output of its gradient's size")
-        packed.extend((g.data_ptr(), o.data_ptr(), n, code))
+        at = g.data_ptr()
+        if code is None:
+            raise TypeError("gradients must be bf16, fp16 or fp32, not %s" % dtype)
+        if g.device != dev:
+            raise ValueError("all tensors must be CUDA tensors on one device")
+        if not g.is_contiguous():
+            raise ValueError("gradients must be contiguous")
+        if o is g:
+            packed += (at, at, n, code)
+            continue
+        if o.dtype is not dtype:
+            raise TypeError("an output must have its gradient's type")
+        if o.device != dev:
+            raise ValueError("all tensors must be CUDA tensors on one device")
+        if o.numel() != n or not o.is_contiguous():
+            raise ValueError("an output must be contiguous and have its gradient's size")
+        packed += (at, o.data_ptr(), n, code)
+    packed = array("q", packed)
     lib = load_library()
     bytes_ = lib.rgg_clip_grad_norm_workspace(len(grads))
     norm = torch.empty((), dtype=torch.float32, device=dev)
@@ -666,15 +683,17 @@ def rgg_mxfp4_quantize(X, group_offsets, codes=None, scales=None, *, stream=None
         raise ValueError("X must be [M_tot, K] and group_offsets [E+1]")
     M_tot, K = X.shape
     E = group_offsets.numel() - 1
-    if codes is None:
-        codes = torch.empty(M_tot, K // 2, dtype=torch.uint8, device=X.device)
-    if scales is None:
-        scales = torch.empty(_mx_scale_shape(M_tot, E, K), dtype=torch.uint8, device=X.device)
     dev = X.device
     _operand("X", X, torch.bfloat16, (M_tot, K), dev)
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
-    _operand("codes", codes, torch.uint8, (M_tot, K // 2), dev)
-    _operand("scales", scales, torch.uint8, _mx_scale_shape(M_tot, E, K), dev)
+    if codes is None:
+        codes = torch.empty(M_tot, K // 2, dtype=torch.uint8, device=dev)
+    else:
+        _operand("codes", codes, torch.uint8, (M_tot, K // 2), dev)
+    if scales is None:
+        scales = torch.empty(_mx_scale_shape(M_tot, E, K), dtype=torch.uint8, device=dev)
+    else:
+        _operand("scales", scales, torch.uint8, _mx_scale_shape(M_tot, E, K), dev)
     device = dev.index
     st = _raw_stream(stream, device)
     s = load_library().rgg_mxfp4_quantize(_handle(device), X.data_ptr(), group_offsets.data_ptr(), codes.data_ptr(),
@@ -690,13 +709,14 @@ def rgg_mxfp4_dequantize(codes, scales, group_offsets, X=None, *, stream=None, c
         raise ValueError("codes must be [M_tot, K/2] and group_offsets [E+1]")
     M_tot, K = codes.shape[0], 2 * codes.shape[1]
     E = group_offsets.numel() - 1
-    if X is None:
-        X = torch.empty(M_tot, K, dtype=torch.bfloat16, device=codes.device)
     dev = codes.device
     _operand("codes", codes, torch.uint8, (M_tot, K // 2), dev)
     _operand("scales", scales, torch.uint8, _mx_scale_shape(M_tot, E, K), dev)
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
-    _operand("X", X, torch.bfloat16, (M_tot, K), dev)
+    if X is None:
+        X = torch.empty(M_tot, K, dtype=torch.bfloat16, device=dev)
+    else:
+        _operand("X", X, torch.bfloat16, (M_tot, K), dev)
     device = dev.index
     st = _raw_stream(stream, device)
     s = load_library().rgg_mxfp4_dequantize(_handle(device), codes.data_ptr(), scales.data_ptr(),
@@ -757,15 +777,16 @@ def _mxfp4_call(name, x_codes, x_scales, w_codes, w_scales, group_offsets, out, 
     M_tot, half = x_codes.shape
     E, cols = w_codes.shape[:2]
     N = cols // 2 if gate_up else cols
-    if out is None:
-        out = torch.empty(M_tot, N, dtype=torch.bfloat16, device=x_codes.device)
     dev = x_codes.device
     _operand("x_codes", x_codes, torch.uint8, (M_tot, half), dev)
     _operand("x_scales", x_scales, torch.uint8, _mx_scale_shape(M_tot, E, 2 * half), dev)
     _operand("w_codes", w_codes, torch.uint8, (E, cols, half), dev)
     _operand("w_scales", w_scales, torch.uint8, _mx_weight_scale_shape(E, cols, 2 * half), dev)
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
-    _operand("out", out, torch.bfloat16, (M_tot, N), dev)
+    if out is None:
+        out = torch.empty(M_tot, N, dtype=torch.bfloat16, device=dev)
+    else:
+        _operand("out", out, torch.bfloat16, (M_tot, N), dev)
     device = dev.index
     opt = None
     if bn or stages or max_ctas or timeout_ns or debug_flags:

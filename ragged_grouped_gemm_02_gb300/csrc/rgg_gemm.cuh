@@ -17,10 +17,11 @@
 //
 // CTA = 192 threads (320 for the fused gate-up and FP8 epilogues), one CTA per
 // SM, persistent over tiles t = cta, cta+grid.. (or another walk order)
-//   warp 0   : TMA producer (one lane)          smem ring  <- X tile, W tile
-//   warp 1   : TMEM owner + MMA issuer (one lane) TMEM acc <- tcgen05.mma
+//   warp 0   : TMA producer                     smem ring  <- X tile, W tile
+//   warp 1   : TMEM owner + MMA issuer          TMEM acc   <- tcgen05.mma
 //   warps 2-5: epilogue (2-9: two warps per      Y        <- TMEM via registers
 //              TMEM lane quadrant, see epilogue_warps)
+// (warps 0 and 1 run in step, one lane issuing: rgg_warp_issue.cuh)
 // The TMEM accumulator holds two BN-column buffers; acc_full/acc_empty
 // barriers per buffer let the epilogue of tile i run under the MMAs of i+1.
 //
@@ -45,10 +46,10 @@
 #include "rgg_ptx.cuh"
 #include "rgg_sched.cuh"
 #include "rgg_tiles.cuh"
+#include "rgg_warp_issue.cuh"
 
 namespace rgg {
 
-constexpr int kStatusTimeout = 5;
 constexpr int kStatusBadOffsets = 4;
 constexpr int kStatusBadRowIndex = 7;
 constexpr int kStatusCapacity = 6;
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
     };
     extern __shared__ __align__(1024) uint8_t smem_raw[];
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = uniform_warp();
     const int lane = threadIdx.x & 31;
     const int E = args.E;
     const int S = args.stages;
@@ -591,26 +592,24 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
     const int32_t WS = walk_stride_for(T);
     // The tile visited at walk position p.
     auto tile_at = [&](int32_t p) -> TileCoord {
-        return walk_decode(s_off, s_pre, s_order, s_spre, E, BM, kOutN, nN, T, WO, WS, p);
+        return uniform_tile(walk_decode(s_off, s_pre, s_order, s_spre, E, BM, kOutN, nN, T, WO, WS, p));
     };
-    // Mixed launch: a consumer takes the next descriptor from the queue
-    // (`warp_wide`: all lanes of an epilogue warp wait, lane 0 releases the
-    // slot for the warp).  False on an abort; expert -1 ends the walk.
-    auto q_pop = [&](int& qs, uint32_t& qp, TileCoord& c, bool warp_wide) -> bool {
-        bool ok = wait_or_abort(qfull_bar(qs), qp, abort_flag, args.status, args.timeout_ns);
-        if (warp_wide) ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return false;
+    // of a whole warp, the same answer in every lane; false on an abort
+    auto warp_await = [&](uint32_t bar, uint32_t parity) -> bool {
+        return warp_wait<false>(bar, parity, abort_flag, 0u, args.status, args.timeout_ns);
+    };
+    // Mixed launch: a consumer warp takes the next descriptor from the queue
+    // (lane 0 releases the slot for the warp).  False on an abort; expert -1
+    // ends the walk.
+    auto q_pop = [&](int& qs, uint32_t& qp, TileCoord& c) -> bool {
+        if (!warp_await(qfull_bar(qs), qp)) return false;
         const volatile int32_t* d = q_desc + 4 * qs;
         c.expert = d[0];
         c.row0 = d[1];
         c.rows = d[2];
         c.col0 = d[3];
-        if (warp_wide) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(qempty_bar(qs));
-        } else {
-            mbar_arrive(qempty_bar(qs));
-        }
+        c = uniform_tile(c);
+        if (lane == 0) mbar_arrive(qempty_bar(qs));
         if (++qs == kQueueDepth) {
             qs = 0;
             qp ^= 1u;
@@ -700,7 +699,8 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
         __syncwarp();
     } else if (warp == 0) {
         // ---------------------------------------------------- S4: TMA producer
-        if (lane == 0 && (args.debug_flags & kDebugProducerStall) == 0) {
+        if ((args.debug_flags & kDebugProducerStall) == 0) {
+            const uint32_t lead = elect_one();
             int st = 0;
             uint32_t ph = 0;
             uint32_t issued = 0;
@@ -712,28 +712,28 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
                 const uint32_t tx_bytes = (half ? 64u : static_cast<uint32_t>(BM)) * 128u + np * Cfg::kPanelB;
                 const CUtensorMap* xmap = (BM == 128 && half) ? &tmap_x64 : &tmap_x;
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!wait_or_abort(empty_bar(st), ph ^ 1u, abort_flag, args.status, args.timeout_ns)) {
+                    if (!warp_await(empty_bar(st), ph ^ 1u)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(full_bar(st), tx_bytes);
+                    expect_tx_if(lead, full_bar(st), tx_bytes);
                     if (RGG_BOUNDS_OK(x_box_ok(kb * Cfg::kKStage, c.row0, args.K, args.M_tot, kElemBytes),
                                       args.status))
-                        tma_load_2d(a0 + st * sp.a_stage, xmap, full_bar(st), kb * Cfg::kKStage, c.row0);
+                        load_2d_if<false>(lead, a0 + st * sp.a_stage, xmap, full_bar(st), kb * Cfg::kKStage, c.row0);
 #pragma unroll
                     for (int p = 0; p < kPanels; ++p) {
                         const int32_t wc = w_col(c.col0, p), wk = kb * Cfg::kKStage;
                         if constexpr (kTransW) {
                             if (p < np && RGG_BOUNDS_OK(w_box_ok(wk, wc, c.expert, args.K, args.N, E, kElemBytes),
                                                         args.status))
-                                tma_load_3d(b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w, full_bar(st), wk, wc,
-                                            c.expert);
+                                load_3d_if<false>(lead, b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w,
+                                                  full_bar(st), wk, wc, c.expert);
                         } else {
                             if (p < np && RGG_BOUNDS_OK(w_box_ok(wc, wk, c.expert, kNw, args.K, E, kElemBytes,
                                                                  kWOverhang),
                                                         args.status))
-                                tma_load_3d(b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w, full_bar(st), wc, wk,
-                                            c.expert);
+                                load_3d_if<false>(lead, b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w,
+                                                  full_bar(st), wc, wk, c.expert);
                         }
                     }
                     ++issued;
@@ -747,35 +747,44 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
                 ClassWalk cw;
                 cw.init(L, false, pair_units > 0);
                 for (int32_t p = blockIdx.x; ok && p < cw.n_positions; p += single_units) {
-                    const TileCoord c = cw.at(L, p);
+                    const TileCoord c = uniform_tile(cw.at(L, p));
                     if (c.rows > 0) produce(c);
                 }
             } else if constexpr (kDyn) {
-                // claim, hand the descriptor to the consumers, load the tile
+                // claim (lane 0), hand the descriptor to the consumers, load the tile
                 TileClaimer cl;
                 cl.init(args.sched, L, false, blockIdx.x, args.sched_pairs, args.sched_singles);
                 int qs = 0;
                 uint32_t qp = 0;
-                TileCoord c = cl.next(L);
+                auto claim = [&]() {
+                    TileCoord c = sentinel_tile();
+                    if (lane == 0) c = cl.next(L);
+                    return uniform_tile(c);
+                };
+                TileCoord c = claim();
                 while (ok) {
-                    if (!wait_or_abort(qempty_bar(qs), qp ^ 1u, abort_flag, args.status, args.timeout_ns)) {
+                    if (!warp_await(qempty_bar(qs), qp ^ 1u)) {
                         ok = false;
                         break;
                     }
-                    int32_t* d = q_desc + 4 * qs;
-                    d[0] = c.expert;
-                    d[1] = c.row0;
-                    d[2] = c.rows;
-                    d[3] = c.col0;
-                    mbar_arrive(qfull_bar(qs));
+                    if (lane == 0) {
+                        int32_t* d = q_desc + 4 * qs;
+                        d[0] = c.expert;
+                        d[1] = c.row0;
+                        d[2] = c.rows;
+                        d[3] = c.col0;
+                        mbar_arrive(qfull_bar(qs));
+                    }
+                    __syncwarp();
                     if (++qs == kQueueDepth) {
                         qs = 0;
                         qp ^= 1u;
                     }
                     if (c.expert < 0) break;
-                    cl.prefetch();
+                    if (lane == 0) cl.prefetch();
+                    __syncwarp();
                     produce(c);
-                    if (ok) c = cl.next(L);
+                    if (ok) c = claim();
                 }
             } else {
                 for (int32_t t = blockIdx.x; ok && t < T; t += gridDim.x) produce(tile_at(t));
@@ -790,7 +799,12 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------ S5: MMA issuer
-        if (lane == 0) {
+        {
+            const uint32_t lead = elect_one();
+            // a step's descriptors differ from the ring's first in their address field alone
+            const uint64_t a_desc = sw128_desc(a0, 16u, 1024u);
+            const uint64_t b_desc = kTransW ? sw128_desc(b0, 16u, 1024u) : sw128_desc(b0, Cfg::kPanelB, 1024u);
+            constexpr uint32_t kBStep = kTransW ? 32u : Cfg::kBStep;
             int st = 0;
             uint32_t ph = 0;
             int acc = 0;
@@ -799,37 +813,31 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
             auto mma_tile = [&](const TileCoord& c) {
                 const int np = tile_panels<kPanels, Cfg::kPanelN, kEpi>(c.col0, args.N);
                 const uint32_t idesc = Cfg::idesc(runs_as_64_rows<BM>(args, c) ? 64 : BM, np * Cfg::kPanelN, !kTransW);
-                if (!wait_or_abort(acce_bar(acc), acc_ph ^ 1u, abort_flag, args.status, args.timeout_ns)) {
+                if (!warp_await(acce_bar(acc), acc_ph ^ 1u)) {
                     ok = false;
                     return;
                 }
                 tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!wait_or_abort(full_bar(st), ph, abort_flag, args.status, args.timeout_ns)) {
+                    if (!warp_await(full_bar(st), ph)) {
                         ok = false;
                         return;
                     }
                     tc_fence_after_sync();
-                    const uint32_t a_st = a0 + st * sp.a_stage;
-                    const uint32_t b_st = b0 + st * sp.b_stage;
+                    const uint64_t ad = a_desc + st * (sp.a_stage >> 4);
+                    const uint64_t bd = b_desc + st * (sp.b_stage >> 4);
 #pragma unroll
-                    for (int j = 0; j < kMmasPerStage; ++j) {
-                        const uint64_t ad = sw128_desc(a_st + 32u * j, 16u, 1024u);
-                        const uint64_t bd = kTransW ? sw128_desc(b_st + 32u * j, 16u, 1024u)
-                                                    : sw128_desc(b_st + Cfg::kBStep * j, Cfg::kPanelB, 1024u);
-                        if constexpr (kFp8)
-                            mma_f8_ss(d_tmem, ad, bd, idesc, (kb | j) != 0 ? 1u : 0u);
-                        else
-                            mma_bf16_ss(d_tmem, ad, bd, idesc, (kb | j) != 0 ? 1u : 0u);
-                    }
-                    mma_commit(empty_bar(st));  // frees the stage once these MMAs have read it
+                    for (int j = 0; j < kMmasPerStage; ++j)
+                        mma_single_if<kFp8>(lead, d_tmem, ad + 2u * j, bd + (kBStep >> 4) * j, idesc,
+                                            (kb | j) != 0 ? 1u : 0u);
+                    commit_if<false>(lead, empty_bar(st));  // frees the stage once these MMAs have read it
                     if (++st == S) {
                         st = 0;
                         ph ^= 1u;
                     }
                 }
-                mma_commit(accf_bar(acc));      // accumulator buffer ready for the epilogue
+                commit_if<false>(lead, accf_bar(acc));  // accumulator buffer ready for the epilogue
                 if (++acc == 2) {
                     acc = 0;
                     acc_ph ^= 1u;
@@ -839,7 +847,7 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
                 ClassWalk cw;
                 cw.init(L, false, pair_units > 0);
                 for (int32_t p = blockIdx.x; ok && p < cw.n_positions; p += single_units) {
-                    const TileCoord c = cw.at(L, p);
+                    const TileCoord c = uniform_tile(cw.at(L, p));
                     if (c.rows > 0) mma_tile(c);
                 }
             } else if constexpr (kDyn) {
@@ -847,7 +855,7 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
                 uint32_t qp = 0;
                 TileCoord c;
                 while (ok) {
-                    if (!q_pop(qs, qp, c, false)) {
+                    if (!q_pop(qs, qp, c)) {
                         ok = false;
                         break;
                     }
@@ -858,7 +866,7 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
                 for (int32_t t = blockIdx.x; ok && t < T; t += gridDim.x) mma_tile(tile_at(t));
             }
             if (!ok) {
-                mma_commit(drain_bar);
+                commit_if<false>(lead, drain_bar);
                 wait_bounded(drain_bar, 0u, kDrainLimitNs);
             }
         }
@@ -878,9 +886,7 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
             // tile row 16q + i sits in TMEM lane 32q + i (i < 16).
             const bool half = runs_as_64_rows<BM>(args, c);
             const int r_local = half ? (q * 16 + (lane & 15)) : (q * 32 + lane);
-            bool ok = wait_or_abort(accf_bar(acc), acc_ph, abort_flag, args.status, args.timeout_ns);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return false;
+            if (!warp_await(accf_bar(acc), acc_ph)) return false;
             tc_fence_after_sync();
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
             epilogue_store_tile<BN, kEpi, kFp8>(args, c, half, r_local, t_row, lane, cc0, true, s_off[c.expert],
@@ -898,14 +904,14 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
             ClassWalk cw;
             cw.init(L, false, pair_units > 0);
             for (int32_t p = blockIdx.x; p < cw.n_positions; p += single_units) {
-                const TileCoord c = cw.at(L, p);
+                const TileCoord c = uniform_tile(cw.at(L, p));
                 if (c.rows > 0 && !epi_tile(c)) break;
             }
         } else if constexpr (kDyn) {
             int qs = 0;
             uint32_t qp = 0;
             TileCoord c;
-            while (q_pop(qs, qp, c, true) && c.expert >= 0)
+            while (q_pop(qs, qp, c) && c.expert >= 0)
                 if (!epi_tile(c)) break;
         } else {
             for (int32_t t = blockIdx.x; t < T; t += gridDim.x)

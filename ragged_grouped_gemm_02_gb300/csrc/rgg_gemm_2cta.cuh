@@ -12,12 +12,13 @@
 // 128 x BN tile.  Every CTA loads its own boxes into its own shared memory.
 //
 // Roles (both CTAs run the same code, rank = %cluster_ctarank):
-//   warp 0 lane 0 : producer.  Waits its own empty[s]; the leader (rank 0)
+//   warp 0        : producer.  Waits its own empty[s]; the leader (rank 0)
 //                   arms its full[s] for both CTAs' bytes; both CTAs' TMA
 //                   loads complete on the leader's full[s].
-//   warp 1        : allocates the pair's TMEM in both CTAs; lane 0 of the
-//                   leader issues every MMA and commits to the empty /
-//                   acc_full barriers of both CTAs with one commit.
+//   warp 1        : allocates the pair's TMEM in both CTAs; the leader's
+//                   issues every MMA and commits to the empty / acc_full
+//                   barriers of both CTAs with one commit.
+//   (both run in step, one lane issuing: rgg_warp_issue.cuh)
 //   warps 2-5     : epilogue of the CTA's own 128 rows (warps 2-9, two per
 //   (or 2-9)        TMEM lane quadrant, for the fused gate-up epilogue);
 //                   they arrive on the leader's acc_empty (one arrival per
@@ -104,7 +105,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
     };
     extern __shared__ __align__(1024) uint8_t smem_raw[];
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = uniform_warp();
     const int lane = threadIdx.x & 31;
     const int E = args.E;
     const int S = args.stages;
@@ -222,22 +223,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
     const int WO = args.walk_order;  // walk position t visits tile walk_tile(t, ...), the same in both CTAs
     const int32_t WS = walk_stride_for(T);
     auto tile_at = [&](int32_t p) -> TileCoord {
-        return walk_decode(s_off, s_pre, s_order, s_spre, E, BM, kOutN, nN, T, WO, WS, p);
+        return uniform_tile(walk_decode(s_off, s_pre, s_order, s_spre, E, BM, kOutN, nN, T, WO, WS, p));
     };
-    // Mixed launch: take the next descriptor from this CTA's queue and
-    // release the slot on the leader's q_empty (`warp_wide`: all lanes of an
-    // epilogue warp wait, lane 0 releases).  False on an abort.
-    auto q_pop = [&](int& qs, uint32_t& qp, TileCoord& c, bool warp_wide) -> bool {
-        bool ok = pair_wait_or_abort<true>(qfull_bar(qs), qp, abort_flag, peer_flag, args.status, args.timeout_ns);
-        if (warp_wide) ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return false;
+    // of a whole warp, the same answer in every lane; false on an abort
+    auto warp_await = [&](uint32_t bar, uint32_t parity) -> bool {
+        return warp_wait<true>(bar, parity, abort_flag, peer_flag, args.status, args.timeout_ns);
+    };
+    // Mixed launch: take the next descriptor from this CTA's queue (a whole
+    // warp) and release the slot on the leader's q_empty.  False on an abort.
+    auto q_pop = [&](int& qs, uint32_t& qp, TileCoord& c) -> bool {
+        if (!warp_wait<true, true>(qfull_bar(qs), qp, abort_flag, peer_flag, args.status, args.timeout_ns))
+            return false;
         const volatile int32_t* d = q_desc + 4 * qs;
         c.expert = d[0];
         c.row0 = d[1];
         c.rows = d[2];
         c.col0 = d[3];
-        if (warp_wide) __syncwarp();
-        if (!warp_wide || lane == 0) {
+        c = uniform_tile(c);
+        if (lane == 0) {
             if (rank == 0) mbar_arrive(qempty_bar(qs));
             else mbar_arrive_cluster(map_to_rank(qempty_bar(qs), 0));
         }
@@ -250,7 +253,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
 
     if (warp == 0) {
         // ---------------------------------------------------- S4: TMA producer
-        if (lane == 0 && (args.debug_flags & kDebugProducerStall) == 0) {
+        if ((args.debug_flags & kDebugProducerStall) == 0) {
+            const uint32_t lead = elect_one();
+            const uint32_t full_leader = map_to_rank(full_bar(0), 0);
             int st = 0;
             uint32_t ph = 0;
             uint32_t issued = 0;
@@ -267,47 +272,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                                                            : c.col0 + (ncols / 2) * static_cast<int32_t>(rank);
                 const CUtensorMap* xmap = half ? &tmap_x64 : &tmap_x;
                 const uint32_t tx_bytes = 2u * ((half ? 64u : 128u) * 128u + np * Cfg::kPanelB);
+                // first column of W of each panel this CTA loads
+                int32_t wcol[Cfg::kPanels];
+#pragma unroll
+                for (int p = 0; p < Cfg::kPanels; ++p)
+                    // a gate-up tail tile: panel 0 this CTA's 64 gate columns, panel 1 their up columns
+                    wcol[p] = (epi_gate_up(kEpi) && half)
+                                  ? (p == 0 ? c.col0 : args.N + c.col0) + Cfg::kPanelN * static_cast<int32_t>(rank)
+                                  : b_col + Cfg::kPanelN * p;
+                // static walk: the MMA warp reads it after its wait on the tile's first stage (the arrive
+                // below releases it)
+                if (!kDyn && rank == 0) {
+                    if (lead)
+                        info_ring[n_produced % kInfoSlots] =
+                            idesc_bf16_f32(half ? 128 : 256, pair_tile_cols<BN, kEpi>(c.col0, args.N), !kTransW);
+                    ++n_produced;
+                }
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!pair_wait_or_abort(empty_bar(st), ph ^ 1u, abort_flag, peer_flag, args.status,
-                                            args.timeout_ns)) {
+                    if (!warp_await(empty_bar(st), ph ^ 1u)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t full_leader = map_to_rank(full_bar(st), 0);
-                    if (rank == 0) {
-                        // static walk: the MMA thread reads it after its wait on this stage (this
-                        // arrive releases it)
-                        if (!kDyn && kb == 0)
-                            info_ring[n_produced++ % kInfoSlots] =
-                                idesc_bf16_f32(half ? 128 : 256, pair_tile_cols<BN, kEpi>(c.col0, args.N), !kTransW);
-                        mbar_arrive_expect_tx(full_bar(st), tx_bytes);
-                    }
+                    const uint32_t bar = full_leader + 8u * st;
+                    if (rank == 0) expect_tx_if(lead, full_bar(st), tx_bytes);
+                    const int32_t wk = kb * Cfg::kKStage;
                     // the second CTA's rows may start past M_tot (a short tile at the end of X): the copy
                     // zero-fills them, so the row check allows one tile of overhang
-                    if (RGG_BOUNDS_OK(x_box_ok(kb * Cfg::kKStage, a_row, args.K, args.M_tot + 128, 2), args.status))
-                        tma_load_2d_pair(a0 + st * sp.a_stage, xmap, full_leader, kb * Cfg::kKStage, a_row);
+                    if (RGG_BOUNDS_OK(x_box_ok(wk, a_row, args.K, args.M_tot + 128, 2), args.status))
+                        load_2d_if<true>(lead, a0 + st * sp.a_stage, xmap, bar, wk, a_row);
+                    const uint32_t b_st = b0 + st * sp.b_stage;
 #pragma unroll
                     for (int p = 0; p < Cfg::kPanels; ++p) {
-                        // a gate-up tail tile: panel 0 this CTA's 64 gate columns, panel 1 their up columns
-                        const int32_t wc = (epi_gate_up(kEpi) && half)
-                                               ? (p == 0 ? c.col0 : args.N + c.col0) +
-                                                     Cfg::kPanelN * static_cast<int32_t>(rank)
-                                               : b_col + Cfg::kPanelN * p;
-                        const int32_t wk = kb * Cfg::kKStage;
                         if constexpr (kTransW) {
                             // rows past the last (the second CTA's half of a narrow tile) are zero-filled
-                            if (p < np && RGG_BOUNDS_OK(w_box_ok(wk, wc, c.expert, args.K,
+                            if (p < np && RGG_BOUNDS_OK(w_box_ok(wk, wcol[p], c.expert, args.K,
                                                                  int64_t(args.N) + Cfg::kPanelN, E, 2),
                                                         args.status))
-                                tma_load_3d_pair(b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w, full_leader, wk,
-                                                 wc, c.expert);
+                                load_3d_if<true>(lead, b_st + p * Cfg::kPanelB, &tmap_w, bar, wk, wcol[p], c.expert);
                         } else {
-                            if (p < np && RGG_BOUNDS_OK(w_box_ok(wc, wk, c.expert,
+                            if (p < np && RGG_BOUNDS_OK(w_box_ok(wcol[p], wk, c.expert,
                                                                  epi_gate_up(kEpi) ? 2 * int64_t(args.N) : args.N,
                                                                  args.K, E, 2, Cfg::kPanelN),
                                                         args.status))
-                                tma_load_3d_pair(b0 + st * sp.b_stage + p * Cfg::kPanelB, &tmap_w, full_leader, wc,
-                                                 wk, c.expert);
+                                load_3d_if<true>(lead, b_st + p * Cfg::kPanelB, &tmap_w, bar, wcol[p], wk, c.expert);
                         }
                     }
                     ++issued;
@@ -320,42 +327,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
             if (kDyn && !args.sched_claims) {
                 ClassWalk cw;
                 cw.init(L, true, single_units > 0);
-                for (int32_t p = pair; ok && p < cw.n_positions; p += pair_units) produce(cw.at(L, p));
+                for (int32_t p = pair; ok && p < cw.n_positions; p += pair_units) produce(uniform_tile(cw.at(L, p)));
             } else if constexpr (kDyn) {
                 int qs = 0;
                 uint32_t qp = 0;
                 if (rank == 0) {
-                    // claim, write the descriptor into both CTAs' queues, load the leader's half
+                    // claim (lane 0), write the descriptor into both CTAs' queues, load the leader's half
                     TileClaimer cl;
                     cl.init(args.sched, L, true, static_cast<int32_t>(pair), args.sched_pairs, args.sched_singles);
-                    TileCoord c = cl.next(L);
+                    auto claim = [&]() {
+                        TileCoord c = sentinel_tile();
+                        if (lane == 0) c = cl.next(L);
+                        return uniform_tile(c);
+                    };
+                    TileCoord c = claim();
                     while (ok) {
-                        if (!pair_wait_or_abort<true>(qempty_bar(qs), qp ^ 1u, abort_flag, peer_flag, args.status,
-                                                      args.timeout_ns)) {
+                        if (!warp_wait<true, true>(qempty_bar(qs), qp ^ 1u, abort_flag, peer_flag, args.status,
+                                                   args.timeout_ns)) {
                             ok = false;
                             break;
                         }
-                        int32_t* d = q_desc + 4 * qs;
-                        d[0] = c.expert;
-                        d[1] = c.row0;
-                        d[2] = c.rows;
-                        d[3] = c.col0;
-                        st_shared_cluster_v4(map_to_rank(smem_addr(d), 1), c.expert, c.row0, c.rows, c.col0);
-                        mbar_arrive(qfull_bar(qs));
-                        mbar_arrive_cluster(map_to_rank(qfull_bar(qs), 1));
+                        if (lane == 0) {
+                            int32_t* d = q_desc + 4 * qs;
+                            d[0] = c.expert;
+                            d[1] = c.row0;
+                            d[2] = c.rows;
+                            d[3] = c.col0;
+                            st_shared_cluster_v4(map_to_rank(smem_addr(d), 1), c.expert, c.row0, c.rows, c.col0);
+                            mbar_arrive(qfull_bar(qs));
+                            mbar_arrive_cluster(map_to_rank(qfull_bar(qs), 1));
+                        }
+                        __syncwarp();
                         if (++qs == kQueueDepth) {
                             qs = 0;
                             qp ^= 1u;
                         }
                         if (c.expert < 0) break;
-                        cl.prefetch();
+                        if (lane == 0) cl.prefetch();
+                        __syncwarp();
                         produce(c);
-                        if (ok) c = cl.next(L);
+                        if (ok) c = claim();
                     }
                 } else {
                     TileCoord c;
                     while (ok) {
-                        if (!q_pop(qs, qp, c, false)) {
+                        if (!q_pop(qs, qp, c)) {
                             ok = false;
                             break;
                         }
@@ -382,7 +398,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------- S5: MMA issuer (leader only)
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const uint32_t lead = elect_one();
+            // a step's descriptors differ from the ring's first in their address field alone
+            const uint64_t a_desc = sw128_desc(a0, 16u, 1024u);
+            const uint64_t b_desc = kTransW ? sw128_desc(b0, 16u, 1024u) : sw128_desc(b0, Cfg::kPanelB, 1024u);
+            constexpr uint32_t kBStep = kTransW ? 32u : Cfg::kBStep;
             int st = 0;
             uint32_t ph = 0;
             int acc = 0;
@@ -393,36 +414,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
             // descriptor is the producer's ring entry, read once the tile's
             // first stage has landed; else `idesc`, decoded here.
             auto mma_tile = [&](uint32_t idesc, bool from_ring) {
-                if (!pair_wait_or_abort(acce_bar(acc), acc_ph ^ 1u, abort_flag, peer_flag, args.status,
-                                        args.timeout_ns)) {
+                if (!warp_await(acce_bar(acc), acc_ph ^ 1u)) {
                     ok = false;
                     return;
                 }
                 tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!pair_wait_or_abort(full_bar(st), ph, abort_flag, peer_flag, args.status, args.timeout_ns)) {
+                    if (!warp_await(full_bar(st), ph)) {
                         ok = false;
                         return;
                     }
                     tc_fence_after_sync();
-                    if (kb == 0 && from_ring) idesc = info_ring[n_tiles % kInfoSlots];
-                    const uint32_t a_st = a0 + st * sp.a_stage;
-                    const uint32_t b_st = b0 + st * sp.b_stage;
+                    if (kb == 0 && from_ring) idesc = __shfl_sync(0xffffffffu, info_ring[n_tiles % kInfoSlots], 0);
+                    const uint64_t ad = a_desc + st * (sp.a_stage >> 4);
+                    const uint64_t bd = b_desc + st * (sp.b_stage >> 4);
 #pragma unroll
-                    for (int j = 0; j < kMmasPerStage; ++j) {
-                        const uint64_t ad = sw128_desc(a_st + 32u * j, 16u, 1024u);
-                        const uint64_t bd = kTransW ? sw128_desc(b_st + 32u * j, 16u, 1024u)
-                                                    : sw128_desc(b_st + Cfg::kBStep * j, Cfg::kPanelB, 1024u);
-                        mma_bf16_ss_pair(d_tmem, ad, bd, idesc, (kb | j) != 0 ? 1u : 0u);
-                    }
-                    mma_commit_pair(empty_bar(st), 0x3);
+                    for (int j = 0; j < kMmasPerStage; ++j)
+                        mma_bf16_pair_if(lead, d_tmem, ad + 2u * j, bd + (kBStep >> 4) * j, idesc,
+                                         (kb | j) != 0 ? 1u : 0u);
+                    commit_if<true>(lead, empty_bar(st));
                     if (++st == S) {
                         st = 0;
                         ph ^= 1u;
                     }
                 }
-                mma_commit_pair(accf_bar(acc), 0x3);
+                commit_if<true>(lead, accf_bar(acc));
                 if (++acc == 2) {
                     acc = 0;
                     acc_ph ^= 1u;
@@ -433,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                 ClassWalk cw;
                 cw.init(L, true, single_units > 0);
                 for (int32_t p = pair; ok && p < cw.n_positions; p += pair_units) {
-                    const TileCoord c = cw.at(L, p);
+                    const TileCoord c = uniform_tile(cw.at(L, p));
                     mma_tile(idesc_bf16_f32(half_tile(c) ? 128 : 256, pair_tile_cols<BN, kEpi>(c.col0, args.N), !kTransW),
                              false);
                 }
@@ -442,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                 uint32_t qp = 0;
                 TileCoord c;
                 while (ok) {
-                    if (!q_pop(qs, qp, c, false)) {
+                    if (!q_pop(qs, qp, c)) {
                         ok = false;
                         break;
                     }
@@ -457,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                 for (int32_t i = 0; ok && i < count; ++i) mma_tile(0u, true);
             }
             if (!ok) {
-                mma_commit_pair(drain_bar, 0x1);
+                commit_if<true>(lead, drain_bar);
                 wait_bounded(drain_bar, 0u, kDrainLimitNs);
             }
         }
@@ -470,9 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
         uint32_t acc_ph = 0;
         // false when the pair aborts
         auto epi_tile = [&](const TileCoord& c) -> bool {
-            bool ok = pair_wait_or_abort(accf_bar(acc), acc_ph, abort_flag, peer_flag, args.status, args.timeout_ns);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return false;
+            if (!warp_await(accf_bar(acc), acc_ph)) return false;
             tc_fence_after_sync();
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
             // M = 256: this CTA's 128 rows, one per TMEM lane, all BN columns.
@@ -563,12 +578,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
             ClassWalk cw;
             cw.init(L, true, single_units > 0);
             for (int32_t p = pair; p < cw.n_positions; p += pair_units)
-                if (!epi_tile(cw.at(L, p))) break;
+                if (!epi_tile(uniform_tile(cw.at(L, p)))) break;
         } else if constexpr (kDyn) {
             int qs = 0;
             uint32_t qp = 0;
             TileCoord c;
-            while (q_pop(qs, qp, c, true) && c.expert >= 0)
+            while (q_pop(qs, qp, c) && c.expert >= 0)
                 if (!epi_tile(c)) break;
         } else {
             for (int32_t t = pair; t < T; t += npairs)

@@ -30,7 +30,7 @@
 #pragma once
 
 #include "rgg_mxfp4.h"
-#include "rgg_warp_issue.cuh"
+#include "rgg_gemm_2cta.cuh"
 
 namespace rgg {
 

@@ -26,6 +26,16 @@ struct TileCoord {
     int32_t col0;
 };
 
+// Lane 0's tile, in every lane, as warp-uniform values.
+__device__ __forceinline__ TileCoord uniform_tile(const TileCoord& c) {
+    TileCoord u;
+    u.expert = __shfl_sync(0xffffffffu, c.expert, 0);
+    u.row0 = __shfl_sync(0xffffffffu, c.row0, 0);
+    u.rows = __shfl_sync(0xffffffffu, c.rows, 0);
+    u.col0 = __shfl_sync(0xffffffffu, c.col0, 0);
+    return u;
+}
+
 // Load off[0..E] into shared memory and check validity:
 // 0 <= off[0] <= off[1] <= ... <= off[E] <= M_tot.  Every thread of the
 // block must call this; returns the same answer in every thread.

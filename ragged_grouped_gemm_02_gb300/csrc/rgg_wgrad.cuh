@@ -38,7 +38,7 @@
 // works on the one at hand.
 #pragma once
 
-#include "rgg_warp_issue.cuh"
+#include "rgg_gemm_2cta.cuh"
 
 namespace rgg {
 

@@ -21,11 +21,14 @@ struct HostDevice {
 HostDevice host_device(const rgg_handle* h);
 
 // Makes `device` current for the scope of a call and restores the caller's.
+// The device is set even where it is current already: a host thread that has
+// made no other CUDA call yet (an autograd engine's, say) has no context bound,
+// and the tensor-map encoder, a driver call, needs one.
 class HostDeviceScope {
 public:
     explicit HostDeviceScope(int device) {
         if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = -1;
-        if (prev_ != device) err_ = cudaSetDevice(device);
+        err_ = cudaSetDevice(device);
     }
     ~HostDeviceScope() {
         int cur = -1;

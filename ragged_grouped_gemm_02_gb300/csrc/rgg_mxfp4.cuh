@@ -282,23 +282,37 @@ __device__ __forceinline__ void mxfp4_tiles(const MxMaps& maps, const MxArgs& ar
                     if (rank == 0) expect_tx_if(lead, full_bar(st), bytes);
                     const uint32_t a = a0 + st * kMxTile, b = b0 + st * kMxTile, sc = s0 + 3u * st * kMxScales;
                     const int32_t kx = kb * 128, ks = kb * 256;
+                    auto x_ok = [&](int32_t row) {
+                        return RGG_BOUNDS_OK(x_box_ok(kx, row, args.K / 2, args.M_tot, 1), args.status);
+                    };
+                    // a thin tile's second CTA may start past the last column: the copy zero-fills its rows
+                    auto w_ok = [&](int32_t row) {
+                        return RGG_BOUNDS_OK(w_box_ok(kx, row, c.expert, args.K / 2, cols_w + 64, E, 1), args.status);
+                    };
+                    auto s_ok = [&](int64_t row, int64_t rows_all) {
+                        return RGG_BOUNDS_OK(x_box_ok(ks, row, mx_k_blocks(args.K) * 128, rows_all, 4), args.status);
+                    };
                     if (boxes == 4) {
-                        load_3d_if<kPair>(lead, a, &maps.x128, bar, kx, x_row, 0);
+                        if (x_ok(x_row)) load_3d_if<kPair>(lead, a, &maps.x128, bar, kx, x_row, 0);
                     } else {
                         for (int i = 0; i < boxes; ++i)
-                            load_3d_if<kPair>(lead, a + 4096u * i, &maps.x32, bar, kx, x_row + 32 * i, 0);
+                            if (x_ok(x_row + 32 * i))
+                                load_3d_if<kPair>(lead, a + 4096u * i, &maps.x32, bar, kx, x_row + 32 * i, 0);
                     }
-                    if (boxes > 0) load_2d_if<kPair>(lead, sc, &maps.sx, bar, ks, sx_row);
+                    if (boxes > 0 && s_ok(sx_row, mx_row_blocks(args.M_tot, E)))
+                        load_2d_if<kPair>(lead, sc, &maps.sx, bar, ks, sx_row);
                     if constexpr (!kPair && kGateUp) {
-                        load_3d_if<kPair>(lead, b, &maps.w64, bar, kx, w_row, c.expert);
-                        load_3d_if<kPair>(lead, b + kMxTile / 2, &maps.w64, bar, kx, N + w_row, c.expert);
-                    } else if (thin) {
-                        load_3d_if<kPair>(lead, b, &maps.w64, bar, kx, w_row, c.expert);
-                    } else {
-                        load_3d_if<kPair>(lead, b, &maps.w128, bar, kx, w_row, c.expert);
+                        if (w_ok(w_row)) load_3d_if<kPair>(lead, b, &maps.w64, bar, kx, w_row, c.expert);
+                        if (w_ok(N + w_row))
+                            load_3d_if<kPair>(lead, b + kMxTile / 2, &maps.w64, bar, kx, N + w_row, c.expert);
+                    } else if (w_ok(w_row)) {
+                        if (thin) load_3d_if<kPair>(lead, b, &maps.w64, bar, kx, w_row, c.expert);
+                        else load_3d_if<kPair>(lead, b, &maps.w128, bar, kx, w_row, c.expert);
                     }
-                    load_2d_if<kPair>(lead, sc + kMxScales, &maps.sw, bar, ks, sw_row);
-                    if (two) load_2d_if<kPair>(lead, sc + 2u * kMxScales, &maps.sw, bar, ks, sw_next);
+                    if (s_ok(sw_row, static_cast<int64_t>(E) * nblocks))
+                        load_2d_if<kPair>(lead, sc + kMxScales, &maps.sw, bar, ks, sw_row);
+                    if (two && s_ok(sw_next, static_cast<int64_t>(E) * nblocks))
+                        load_2d_if<kPair>(lead, sc + 2u * kMxScales, &maps.sw, bar, ks, sw_next);
                     ++issued;
                     if (++st == S) {
                         st = 0;
@@ -423,6 +437,9 @@ __device__ __forceinline__ void mxfp4_tiles(const MxMaps& maps, const MxArgs& ar
             for (int i = 0; i < kCols; i += 32) {
                 const int cc = part * kCols + i;
                 if (c.col0 + cc >= N) break;  // columns past N are not computed
+                if (!RGG_BOUNDS_OK(tmem_cols_ok((n & 1) * kAccStride + (kGateUp ? kOutN : 0) + cc, 32, kMxSfCol),
+                                   args.status))
+                    break;
                 tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(cc), *reinterpret_cast<uint32_t(*)[32]>(&v[i]));
                 if constexpr (kGateUp)
                     tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(kOutN + cc),
@@ -451,6 +468,7 @@ __device__ __forceinline__ void mxfp4_tiles(const MxMaps& maps, const MxArgs& ar
                     w[j] = pack_bf16x2(__float_as_uint(x[0]), __float_as_uint(x[1]));
                 }
                 __nv_bfloat16* dst = args.Y + row * N + col;
+                if (!RGG_BOUNDS_OK(store_ok(row, col, 8, s_off[c.expert], s_off[c.expert + 1], N), args.status)) break;
                 if (col + 16 <= N) {
                     if (args.y_vec32) {
                         st_global_v8(dst, w);

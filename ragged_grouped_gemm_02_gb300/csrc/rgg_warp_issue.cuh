@@ -112,51 +112,6 @@ __device__ __forceinline__ void load_3d_if(uint32_t lead, uint32_t dst, const CU
             : "memory");
 }
 
-// ------------------------------------------- tiles from the launch's own grid
-// A grid of one cluster per tile: a running cluster takes the next cluster that
-// has not started (cluster launch control) and does its work in its place, so
-// tiles go to whoever is free, without counters in memory.
-
-// Asks for the next cluster; the answer (16 bytes) comes to `slot` in shared
-// memory and is counted on `bar`, in every CTA of the cluster at that offset.
-__device__ __forceinline__ void take_cluster_if(uint32_t lead, uint32_t slot, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %2, 0;\n\t"
-        "@q clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
-        ".multicast::cluster::all.b128 [%0], [%1];\n\t}" ::"r"(slot),
-        "r"(bar), "r"(lead)
-        : "memory");
-}
-
-// As take_cluster_if, the answer to this CTA alone.
-__device__ __forceinline__ void take_cluster_alone_if(uint32_t lead, uint32_t slot, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %2, 0;\n\t"
-        "@q clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n\t}" ::
-            "r"(slot),
-        "r"(bar), "r"(lead)
-        : "memory");
-}
-
-// The answer at `slot`: the x index of the taken cluster's first CTA, or -1 when there was none left.
-__device__ __forceinline__ int32_t taken_cluster(uint32_t slot) {
-    uint32_t x;
-    asm volatile(
-        "{\n\t.reg .b128 h;\n\t"
-        ".reg .pred p;\n\t"
-        ".reg .b32 y, z, w;\n\t"
-        "ld.shared.b128 h, [%1];\n\t"
-        "mov.b32 %0, 0xffffffff;\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, h;\n\t}"
-        : "=&r"(x)
-        : "r"(slot)
-        : "memory");
-    return static_cast<int32_t>(x);
-}
-
 // Arrive once on `bar` (kPair: at that offset in both CTAs) when the lane's earlier tcgen05 operations are done.
 template <bool kPair>
 __device__ __forceinline__ void commit_if(uint32_t lead, uint32_t bar) {

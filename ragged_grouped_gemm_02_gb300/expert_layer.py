@@ -1,0 +1,65 @@
+"""One expert layer through the library's operators: forward and backward for
+training, and its 4-bit form for serving.
+
+The layer is ``Y_e = (silu(X_e . W13_e[:, :N]) * (X_e . W13_e[:, N:])) . W2_e`` on rows
+grouped by expert.  Its backward pass keeps nothing of the forward pass but the
+inputs: ``rgg_grouped_gemm_swiglu_backward`` computes gate and up again.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import (rgg_grouped_gemm, rgg_grouped_gemm_dgrad, rgg_grouped_gemm_mxfp4, rgg_grouped_gemm_swiglu,
+               rgg_grouped_gemm_swiglu_backward, rgg_grouped_gemm_swiglu_mxfp4, rgg_grouped_gemm_wgrad,
+               rgg_mxfp4_quantize, rgg_mxfp4_quantize_weights)
+
+__all__ = ["expert_ffn", "quantize_experts", "expert_ffn_mxfp4"]
+
+
+class _ExpertFFN(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W13, W2, group_offsets):
+        ctx.save_for_backward(X, W13, W2, group_offsets)
+        H = rgg_grouped_gemm_swiglu(X, W13, group_offsets)
+        Y = torch.zeros(X.shape[0], W2.shape[2], dtype=X.dtype, device=X.device)  # rows of no expert: zero
+        return rgg_grouped_gemm(H, W2, group_offsets, Y)
+
+    @staticmethod
+    def backward(ctx, dY):
+        X, W13, W2, group_offsets = ctx.saved_tensors
+        dY = dY.contiguous()
+        dH = rgg_grouped_gemm_dgrad(dY, W2, group_offsets)
+        dGU, H = rgg_grouped_gemm_swiglu_backward(X, W13, group_offsets, dH,
+                                                  H=None if ctx.needs_input_grad[2] else False)
+        dX = dW13 = dW2 = None
+        if ctx.needs_input_grad[2]:
+            dW2 = rgg_grouped_gemm_wgrad(H, dY, group_offsets)
+        if ctx.needs_input_grad[1]:
+            dW13 = rgg_grouped_gemm_wgrad(X, dGU, group_offsets)
+        if ctx.needs_input_grad[0]:
+            dX = rgg_grouped_gemm_dgrad(dGU, W13, group_offsets, torch.zeros_like(X))
+        return dX, dW13, dW2, None
+
+
+def expert_ffn(X, W13, W2, group_offsets):
+    """Y for routed rows X, with gradients by X, W13 and W2.
+
+    X: bf16 CUDA [M_tot, K], rows grouped by expert; W13: bf16 CUDA [E, K, 2N]
+    (gate columns first); W2: bf16 CUDA [E, N, K_out]; group_offsets: int32
+    CUDA [E+1].  Rows of no expert get zeros, in Y and in the gradient."""
+    return _ExpertFFN.apply(X, W13, W2, group_offsets)
+
+
+def quantize_experts(W13, W2):
+    """The layer's weights in MXFP4, laid out once: what ``expert_ffn_mxfp4`` takes."""
+    return rgg_mxfp4_quantize_weights(W13.detach()), rgg_mxfp4_quantize_weights(W2.detach())
+
+
+def expert_ffn_mxfp4(X, experts, group_offsets):
+    """Y for routed rows X with 4-bit weights (``quantize_experts``) and
+    activations quantised on the way.  K, N and K_out as the MXFP4 products want
+    them: K a multiple of 32, N of 128, K_out of 8.  Rows of no expert hold
+    unspecified values."""
+    w13, w2 = experts
+    H = rgg_grouped_gemm_swiglu_mxfp4(*rgg_mxfp4_quantize(X, group_offsets), *w13, group_offsets)
+    return rgg_grouped_gemm_mxfp4(*rgg_mxfp4_quantize(H, group_offsets), *w2, group_offsets)

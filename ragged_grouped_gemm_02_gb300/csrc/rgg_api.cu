@@ -1084,7 +1084,7 @@ rgg_status swiglu_call(rgg_handle* h, const void* X, const void* W13, const int3
     a.num_k_blocks = static_cast<int32_t>(ceil_div(K, rgg::kBK));
     a.n_tiles_n = static_cast<int32_t>(ceil_div(N, p.bn / 2));
     a.stages = p.stages;
-    a.y_vec32 = ((N % 16) == 0 && aligned(out, 32)) ? 1 : 0;
+    a.y_vec32 = ((N % 16) == 0 && aligned(out, 32) && aligned(act, 32)) ? 1 : 0;
     a.timeout_ns = (opt && opt->timeout_ns) ? opt->timeout_ns : kDefaultTimeoutNs;
     a.debug_flags = opt ? (opt->debug_flags & RGG_DEBUG_PRODUCER_STALL) : 0;
     a.tail64 = p.tail64;

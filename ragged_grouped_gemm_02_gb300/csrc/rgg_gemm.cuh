@@ -274,49 +274,70 @@ __host__ __device__ constexpr int cta_threads() {
 
 __device__ __forceinline__ float silu_f32(float z) { return z / (1.0f + __expf(-z)); }
 
+// The part of dH that a lane of the gate-up backward's epilogue needs: up to 64
+// columns of one row, read before the accumulators are waited for.
+struct GradRow {
+    uint4 d[8];
+
+    __device__ __forceinline__ void load(const GemmArgs& args, bool row_ok, int64_t row, int col, int cols) {
+        const uint4* p = reinterpret_cast<const uint4*>(args.dH + row * args.N + col);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            d[q] = (row_ok && 8 * q < cols && col + 8 * q < args.N) ? __ldg(p + q) : make_uint4(0u, 0u, 0u, 0u);
+    }
+};
+
 // The gate-up backward for 32 columns of one row (gate and up accumulators in
-// v and u, first output column `col`): with s = 1 / (1 + exp(-g)),
+// v and u, dH in grad's first or `second` 32 columns, first output column
+// `col`): with
+// s = 1 / (1 + exp(-g)),
 //     dG = dH * u * s * (1 + g * (1 - s)),  dU = dH * g * s,  H = g * s * u,
-// in fp32 from the unrounded accumulators, each rounded once to bf16.  dH is
-// read 8 columns (16 bytes) at a time, the granule N is a multiple of.
+// in fp32 from the unrounded accumulators, each rounded once to bf16.
 __device__ __forceinline__ void store_swiglu_backward(const GemmArgs& args, int64_t row, int col,
-                                                      const uint32_t (&v)[32], const uint32_t (&u)[32], int32_t row_lo,
+                                                      const uint32_t (&v)[32], const uint32_t (&u)[32],
+                                                      const GradRow& grad, bool second, int32_t row_lo,
                                                       int32_t row_hi) {
     const int N = args.N;
-    const __nv_bfloat16* dh = args.dH + row * N + col;
     __nv_bfloat16* dg_out = args.Y + row * (2 * static_cast<int64_t>(N)) + col;
     __nv_bfloat16* act_out = args.act ? args.act + row * N + col : nullptr;
-    uint4 d4[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        d4[q] = (col + 8 * q < N) ? __ldg(reinterpret_cast<const uint4*>(dh + 8 * q)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int h = 0; h < 2; ++h) {
+        const int at = 16 * h;  // 16 columns at a time, 32 bytes of each output
+        if (col + at >= N) break;
+        if (!RGG_BOUNDS_OK(store_ok(row, col + at, 8, row_lo, row_hi, N), args.status)) break;
+        const uint4 d0 = second ? grad.d[4 + 2 * h] : grad.d[2 * h];
+        const uint4 d1 = second ? grad.d[5 + 2 * h] : grad.d[2 * h + 1];
+        const uint32_t dw[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+        uint32_t wg[8], wu[8], wh[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        if (col + 8 * q >= N) break;
-        if (!RGG_BOUNDS_OK(store_ok(row, col + 8 * q, 8, row_lo, row_hi, N), args.status)) break;
-        const uint32_t dw[4] = {d4[q].x, d4[q].y, d4[q].z, d4[q].w};
-        uint32_t wg[4], wu[4], wh[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float dg[2], du[2], h[2];
+        for (int i = 0; i < 8; ++i) {
+            float dg[2], du[2], hh[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float g = __uint_as_float(v[8 * q + 2 * i + j]);
-                const float up = __uint_as_float(u[8 * q + 2 * i + j]);
+                const float g = __uint_as_float(v[at + 2 * i + j]);
+                const float up = __uint_as_float(u[at + 2 * i + j]);
                 const float d = __uint_as_float(j ? (dw[i] & 0xffff0000u) : (dw[i] << 16));
                 const float s = __fdividef(1.0f, 1.0f + __expf(-g));
                 const float gs = g * s;
-                h[j] = gs * up;
+                hh[j] = gs * up;
                 du[j] = d * gs;
                 dg[j] = d * up * s * (1.0f + (g - gs));
             }
             wg[i] = pack_bf16x2(__float_as_uint(dg[0]), __float_as_uint(dg[1]));
             wu[i] = pack_bf16x2(__float_as_uint(du[0]), __float_as_uint(du[1]));
-            wh[i] = pack_bf16x2(__float_as_uint(h[0]), __float_as_uint(h[1]));
+            wh[i] = pack_bf16x2(__float_as_uint(hh[0]), __float_as_uint(hh[1]));
         }
-        st_global_v4(dg_out + 8 * q, wg[0], wg[1], wg[2], wg[3]);
-        st_global_v4(dg_out + N + 8 * q, wu[0], wu[1], wu[2], wu[3]);
-        if (act_out) st_global_v4(act_out + 8 * q, wh[0], wh[1], wh[2], wh[3]);
+        auto store = [&](__nv_bfloat16* p, const uint32_t (&w)[8]) {
+            if (col + at + 16 <= N && args.y_vec32) {
+                st_global_v8(p, w);
+            } else {
+                st_global_v4(p, w[0], w[1], w[2], w[3]);
+                if (col + at + 16 <= N) st_global_v4(p + 8, w[4], w[5], w[6], w[7]);
+            }
+        };
+        store(dg_out + at, wg);
+        store(dg_out + N + at, wu);
+        if (act_out) store(act_out + at, wh);
     }
 }
 
@@ -333,7 +354,7 @@ __device__ __forceinline__ void store_swiglu_backward(const GemmArgs& args, int6
 template <int BN, int kEpi, bool kFp8>
 __device__ __forceinline__ void epilogue_store_tile(const GemmArgs& args, const TileCoord& c, bool half, int r_local,
                                                     uint32_t t_row, int lane, int cc0, bool store, int32_t row_lo,
-                                                    int32_t row_hi, uint32_t tcol) {
+                                                    int32_t row_hi, uint32_t tcol, const GradRow& grad) {
     constexpr int kOutN = epi_gate_up(kEpi) ? BN / 2 : BN;
     constexpr int kPartCols = kOutN / (epilogue_warps<kEpi, kFp8>() / 4);
     constexpr uint32_t kTmemCols = TileConfig<64, BN, kFp8>::kTmemCols;
@@ -358,7 +379,8 @@ __device__ __forceinline__ void epilogue_store_tile(const GemmArgs& args, const 
             if (!ld_ok)
                 for (int i = 0; i < 32; ++i) v[i] = 0u;
             if constexpr (kEpi == kEpiSwiGLUBwd) {
-                if (row_ok) store_swiglu_backward(args, row, c.col0 + cc, v, u, row_lo, row_hi);
+                if (row_ok)
+                    store_swiglu_backward(args, row, c.col0 + cc, v, u, grad, cc != cc0, row_lo, row_hi);
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -886,11 +908,15 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
             // tile row 16q + i sits in TMEM lane 32q + i (i < 16).
             const bool half = runs_as_64_rows<BM>(args, c);
             const int r_local = half ? (q * 16 + (lane & 15)) : (q * 32 + lane);
+            GradRow grad;
+            if constexpr (kEpi == kEpiSwiGLUBwd)
+                grad.load(args, (!half || lane < 16) && r_local < c.rows, static_cast<int64_t>(c.row0) + r_local,
+                          c.col0 + cc0, kPartCols);
             if (!warp_await(accf_bar(acc), acc_ph)) return false;
             tc_fence_after_sync();
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
             epilogue_store_tile<BN, kEpi, kFp8>(args, c, half, r_local, t_row, lane, cc0, true, s_off[c.expert],
-                                                s_off[c.expert + 1], static_cast<uint32_t>(acc * BN));
+                                                s_off[c.expert + 1], static_cast<uint32_t>(acc * BN), grad);
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(acce_bar(acc));

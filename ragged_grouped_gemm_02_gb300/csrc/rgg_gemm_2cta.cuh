@@ -487,8 +487,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
         uint32_t acc_ph = 0;
         // false when the pair aborts
         auto epi_tile = [&](const TileCoord& c) -> bool {
-            if (!warp_await(accf_bar(acc), acc_ph)) return false;
-            tc_fence_after_sync();
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
             // M = 256: this CTA's 128 rows, one per TMEM lane, all BN columns.
             // M = 128: this CTA's 64 rows fill the 128 lanes twice over (GB300
@@ -510,6 +508,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
             constexpr int kParts = pair_epilogue_warps<kEpi>() / 4;  // warps per lane quadrant
             const int pc = ncols / kParts;                                // columns each of them writes
             const int c0 = ((warp - 2) >> 2) * pc;
+            GradRow grad;
+            if constexpr (kEpi == kEpiSwiGLUBwd) grad.load(args, row_ok, row, c.col0 + cbase + c0, pc);
+            if (!warp_await(accf_bar(acc), acc_ph)) return false;
+            tc_fence_after_sync();
 #pragma unroll 1
             for (int cc = c0; cc < c0 + pc; cc += 32) {
                 if (c.col0 + cbase + cc >= N) break;  // columns past N: not computed, not stored
@@ -530,7 +532,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                     if (!ld_ok)
                         for (int i = 0; i < 32; ++i) v[i] = 0u;
                     if constexpr (kEpi == kEpiSwiGLUBwd) {
-                        if (row_ok) store_swiglu_backward(args, row, c.col0 + cbase + cc, v, u, row_lo, row_hi);
+                        if (row_ok)
+                            store_swiglu_backward(args, row, c.col0 + cbase + cc, v, u, grad, cc != c0, row_lo, row_hi);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)

@@ -540,7 +540,7 @@ rgg_status rgg_mxfp4_dequantize_weights(rgg_handle* h, const void* codes, const 
  * the weight has 2N columns, gate first, and H = silu(g) * u is bf16 [M_tot, N];
  * N must then be a multiple of 128.  Operands as the quantisers leave them.  Of
  * `opt` they read bn (256: 256 x 256 tiles on CTA pairs, 128: 128 x 128 tiles on
- * single CTAs, 0: by the rows per expert), bm (0 or the same), stages, max_ctas
+ * single CTAs, 0: by a cost estimate), bm (0 or the same), stages, max_ctas
  * (at least 2 for pairs), timeout_ns and debug_flags.  Other arguments, errors and
  * the stream contract as for rgg_grouped_gemm.
  */

@@ -804,7 +804,7 @@ def rgg_grouped_gemm_mxfp4(x_codes, x_scales, w_codes, w_scales, group_offsets, 
     """Y_e = X_e . W_e for every expert with MXFP4 operands, as
     ``rgg_mxfp4_quantize`` and ``rgg_mxfp4_quantize_weights`` leave them; Y:
     optional bf16 CUDA [M_tot, N].  bn: 256 (256 x 256 tiles on CTA pairs), 128
-    (128 x 128 on single CTAs) or 0, by the rows per expert."""
+    (128 x 128 on single CTAs) or 0, by a cost estimate."""
     return _mxfp4_call("rgg_grouped_gemm_mxfp4", x_codes, x_scales, w_codes, w_scales, group_offsets, Y, False, bn,
                        stages, max_ctas, timeout_ns, debug_flags, stream, check)
 

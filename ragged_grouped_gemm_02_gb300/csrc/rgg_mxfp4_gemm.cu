@@ -49,7 +49,22 @@ static rgg_status mxfp4_call(rgg_handle* h, const void* x_codes, const void* x_s
     const int64_t avg = (M_tot + E - 1) / E;
     auto tiles_n = [&](int b) { return (N + (gate_up ? b / 2 : b) - 1) / (gate_up ? b / 2 : b); };
     int b = want_bm ? want_bm : want_bn;
-    if (b == 0) b = (avg > 128 && cap >= 2) ? 256 : 128;
+    if (b == 0) {
+        // The shape with the shorter waves, experts taken as balanced: a tile
+        // costs a fixed part and a part per stage of 256 of K, fitted in us to
+        // 10 752 and 8 192 single tiles, 2 816 and 2 048 pair tiles of K = 1024
+        // and 6144 (single 1.78 and 5.86, gate-up 7.2; pair 3.5 and 9.0).
+        // Chosen by rows alone (pairs above 128), 64 experts x 256 rows of
+        // K = 1024 took 48 us on pairs, 40 on single CTAs.
+        const double kb = (K + kMxStageK - 1) / kMxStageK;
+        auto waves = [&](int bb, int units) {
+            const int64_t tiles = E * ((avg + bb - 1) / bb) * tiles_n(bb);
+            return static_cast<double>((tiles + units - 1) / units);
+        };
+        const double single = waves(128, cap) * (0.96 + (gate_up ? 0.26 : 0.204) * kb);
+        const double paired = cap >= 2 ? waves(256, cap / 2) * (2.4 + 0.275 * kb) : 1e300;
+        b = (avg > 128 && paired < single) ? 256 : 128;
+    }
     const bool pair = b == 256;
     if (pair && cap < 2) return RGG_ERR_INVALID_ARG;
     const int64_t most = (M_tot / b + E) * tiles_n(b);

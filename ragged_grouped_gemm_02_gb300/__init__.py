@@ -467,6 +467,16 @@ def _raw_stream(stream, device):
     return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor of the stream that will write it (None: the current one), so that the allocator
+    neither hands out memory that another stream's work still reads nor reuses it too early."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _finish(name, status, device, stream_ptr, check):
     if status != RGG_OK:
         _raise(status, name)
@@ -496,7 +506,7 @@ def rgg_grouped_gemm_dgrad(dY, W, group_offsets, dX=None, *, bm=0, bn=0, stages=
     _operand("W", W, torch.bfloat16, (E, K, N), dev)
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
     if dX is None:
-        dX = torch.empty(M_tot, K, dtype=torch.bfloat16, device=dev)
+        dX = _empty((M_tot, K), torch.bfloat16, dev, stream)
     else:
         _operand("dX", dX, torch.bfloat16, (M_tot, K), dev)
     device = dev.index
@@ -538,7 +548,7 @@ def rgg_grouped_gemm_wgrad(X, dY, group_offsets, dW=None, *, dtype=None, accumul
     _operand("dY", dY, torch.bfloat16, (M_tot, N), dev)
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
     if dW is None:
-        dW = torch.empty(E, K, N, dtype=dtype, device=dev)
+        dW = _empty((E, K, N), dtype, dev, stream)
     else:
         _operand("dW", dW, dtype, (E, K, N), dev)
     device = dev.index
@@ -575,11 +585,11 @@ def rgg_grouped_gemm_swiglu_backward(X, W13, group_offsets, dH, dGU=None, H=None
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
     _operand("dH", dH, torch.bfloat16, (M_tot, N), dev)
     if dGU is None:
-        dGU = torch.empty(M_tot, 2 * N, dtype=torch.bfloat16, device=dev)
+        dGU = _empty((M_tot, 2 * N), torch.bfloat16, dev, stream)
     else:
         _operand("dGU", dGU, torch.bfloat16, (M_tot, 2 * N), dev)
     if H is None:
-        H = torch.empty(M_tot, N, dtype=torch.bfloat16, device=dev)
+        H = _empty((M_tot, N), torch.bfloat16, dev, stream)
     elif H is False:
         H = None
     else:
@@ -649,12 +659,9 @@ def rgg_clip_grad_norm(grads, max_norm, out=None, *, stream=None):
     packed = array("q", packed)
     lib = load_library()
     bytes_ = lib.rgg_clip_grad_norm_workspace(len(grads))
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    workspace = torch.empty(bytes_ // 8, dtype=torch.float64, device=dev)
+    norm = _empty((), torch.float32, dev, stream)
+    workspace = _empty((bytes_ // 8,), torch.float64, dev, stream)
     st = _raw_stream(stream, dev.index)
-    if stream is not None:
-        # allocated on the current stream, used on another one
-        workspace.record_stream(stream)
     s = lib.rgg_clip_grad_norm(_handle(dev.index), packed.buffer_info()[0], len(grads), float(max_norm),
                                norm.data_ptr(), workspace.data_ptr(), bytes_, st)
     if s != RGG_OK:
@@ -687,11 +694,11 @@ def rgg_mxfp4_quantize(X, group_offsets, codes=None, scales=None, *, stream=None
     _operand("X", X, torch.bfloat16, (M_tot, K), dev)
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
     if codes is None:
-        codes = torch.empty(M_tot, K // 2, dtype=torch.uint8, device=dev)
+        codes = _empty((M_tot, K // 2), torch.uint8, dev, stream)
     else:
         _operand("codes", codes, torch.uint8, (M_tot, K // 2), dev)
     if scales is None:
-        scales = torch.empty(_mx_scale_shape(M_tot, E, K), dtype=torch.uint8, device=dev)
+        scales = _empty(_mx_scale_shape(M_tot, E, K), torch.uint8, dev, stream)
     else:
         _operand("scales", scales, torch.uint8, _mx_scale_shape(M_tot, E, K), dev)
     device = dev.index
@@ -714,7 +721,7 @@ def rgg_mxfp4_dequantize(codes, scales, group_offsets, X=None, *, stream=None, c
     _operand("scales", scales, torch.uint8, _mx_scale_shape(M_tot, E, K), dev)
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
     if X is None:
-        X = torch.empty(M_tot, K, dtype=torch.bfloat16, device=dev)
+        X = _empty((M_tot, K), torch.bfloat16, dev, stream)
     else:
         _operand("X", X, torch.bfloat16, (M_tot, K), dev)
     device = dev.index
@@ -734,9 +741,9 @@ def rgg_mxfp4_quantize_weights(W, codes=None, scales=None, *, stream=None):
         raise ValueError("W must be [E, K, N]")
     E, K, N = W.shape
     if codes is None:
-        codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=W.device)
+        codes = _empty((E, N, K // 2), torch.uint8, W.device, stream)
     if scales is None:
-        scales = torch.empty(_mx_weight_scale_shape(E, N, K), dtype=torch.uint8, device=W.device)
+        scales = _empty(_mx_weight_scale_shape(E, N, K), torch.uint8, W.device, stream)
     dev = W.device
     _operand("W", W, torch.bfloat16, (E, K, N), dev)
     _operand("codes", codes, torch.uint8, (E, N, K // 2), dev)
@@ -756,7 +763,7 @@ def rgg_mxfp4_dequantize_weights(codes, scales, W=None, *, stream=None):
         raise ValueError("codes must be [E, N, K/2]")
     E, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
     if W is None:
-        W = torch.empty(E, N, K, dtype=torch.bfloat16, device=codes.device)
+        W = _empty((E, N, K), torch.bfloat16, codes.device, stream)
     dev = codes.device
     _operand("codes", codes, torch.uint8, (E, N, K // 2), dev)
     _operand("scales", scales, torch.uint8, _mx_weight_scale_shape(E, N, K), dev)
@@ -784,7 +791,7 @@ def _mxfp4_call(name, x_codes, x_scales, w_codes, w_scales, group_offsets, out, 
     _operand("w_scales", w_scales, torch.uint8, _mx_weight_scale_shape(E, cols, 2 * half), dev)
     _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
     if out is None:
-        out = torch.empty(M_tot, N, dtype=torch.bfloat16, device=dev)
+        out = _empty((M_tot, N), torch.bfloat16, dev, stream)
     else:
         _operand("out", out, torch.bfloat16, (M_tot, N), dev)
     device = dev.index

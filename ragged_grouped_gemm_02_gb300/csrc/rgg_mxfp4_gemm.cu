@@ -67,6 +67,10 @@ static rgg_status mxfp4_call(rgg_handle* h, const void* x_codes, const void* x_s
     }
     const bool pair = b == 256;
     if (pair && cap < 2) return RGG_ERR_INVALID_ARG;
+    // blocks of scales are counted in 32 bits
+    if (static_cast<int64_t>(E) * ((static_cast<int64_t>(gate_up ? 2 : 1) * N + kMxRows - 1) / kMxRows) >=
+        (int64_t(1) << 31))
+        return RGG_ERR_UNSUPPORTED;
     const int64_t most = (M_tot / b + E) * tiles_n(b);
     if (most >= (int64_t(1) << 30)) return RGG_ERR_UNSUPPORTED;
     const int64_t room = static_cast<int64_t>(dev.smem_optin) - 1024 - mx_smem(0, E).total;

@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(kQuantThreads)
             word |= __shfl_xor_sync(0xffffffffu, word, 4);
             word |= __shfl_xor_sync(0xffffffffu, word, 8);
             const int kb = at / 16;
-            if ((lane & 15) == 0 && kb < kblocks) *reinterpret_cast<uint32_t*>(block + kb * kMxBlockBytes) = word;
+            if ((lane & 15) == 0 && kb < kblocks)
+                *reinterpret_cast<uint32_t*>(block + static_cast<int64_t>(kb) * kMxBlockBytes) = word;
         }
         if (!more) break;
     }
@@ -286,7 +287,8 @@ __global__ void __launch_bounds__(kQuantThreads)
         for (int i = 0; i < 4; ++i) {
             const int at = w.seg * (kSegment / 8) + i * 32 + lane;  // pieces of eight values
             c[i] = at < k8 ? __ldg(codes + w.row * k8 + at) : 0u;
-            b[i] = at < k8 ? __ldg(scales + w.scales + (at / 16) * kMxBlockBytes + (at / 4) % 4) : 0u;
+            const int64_t block = static_cast<int64_t>(at / 16) * kMxBlockBytes;  // the row's block along K
+            b[i] = at < k8 ? __ldg(scales + w.scales + block + (at / 4) % 4) : 0u;
         }
     };
     load();

@@ -444,12 +444,17 @@ rgg_status rgg_grouped_gemm_swiglu_backward(rgg_handle* h, const void* X, const 
  * give equal bits.
  *
  * The kernel runs on CTA pairs.  Of `opt` it reads bm (0 or 256), bn (0, 128 or
- * 256), stages (0 or 2..8), max_ctas (0 or at least 2), timeout_ns and
- * debug_flags.  M_tot may be 0.  Sizes, alignment, errors and the stream
+ * 256), stages (0 or 2..8), max_ctas (0 or at least 2), timeout_ns,
+ * debug_flags and workspace.  With a workspace (device memory, 16-byte aligned,
+ * at least rgg_grouped_gemm_wgrad_workspace bytes, not shared by calls that may
+ * overlap) products with few tiles and many rows split each expert's rows into
+ * parts whose fp32 sums a second launch adds in order; without one they run
+ * unsplit.  That function returns 0 where a split would not pay.  M_tot may be 0.  Sizes, alignment, errors and the stream
  * contract as for rgg_grouped_gemm; invalid offsets write nothing.
  */
 #define RGG_WGRAD_FP32 1
 #define RGG_WGRAD_ACCUMULATE 2
+int64_t rgg_grouped_gemm_wgrad_workspace(rgg_handle* h, int E, int64_t M_tot, int K, int N, int flags);
 rgg_status rgg_grouped_gemm_wgrad(rgg_handle* h, const void* X, const void* dY, const int32_t* group_offsets,
                                   void* dW, int E, int64_t M_tot, int K, int N, int flags, void* stream,
                                   const rgg_options* opt);

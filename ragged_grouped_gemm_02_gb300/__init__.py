@@ -50,6 +50,7 @@ EXPORTED_SYMBOLS = (
     "rgg_plan", "rgg_status_string", "rgg_last_cuda_error", "rgg_grouped_gemm_noalloc", "rgg_grouped_gemm_swiglu",
     "rgg_grouped_gemm_fp8", "rgg_grouped_gemm_gather", "rgg_grouped_gemm_swiglu_gather", "rgg_export_walk",
     "rgg_grouped_gemm_dgrad", "rgg_grouped_gemm_wgrad", "rgg_grouped_gemm_swiglu_backward",
+    "rgg_grouped_gemm_wgrad_workspace",
     "rgg_clip_grad_norm", "rgg_clip_grad_norm_workspace", "rgg_mxfp4_scale_bytes", "rgg_mxfp4_quantize",
     "rgg_mxfp4_dequantize", "rgg_mxfp4_quantize_weights", "rgg_mxfp4_dequantize_weights", "rgg_grouped_gemm_mxfp4",
     "rgg_grouped_gemm_swiglu_mxfp4",
@@ -140,6 +141,8 @@ def open_library(path: str) -> ctypes.CDLL:
     lib.rgg_grouped_gemm_dgrad.restype = I
     lib.rgg_grouped_gemm_wgrad.argtypes = [P, P, P, P, P, I, I64, I, I, I, P, ctypes.POINTER(_Options)]
     lib.rgg_grouped_gemm_wgrad.restype = I
+    lib.rgg_grouped_gemm_wgrad_workspace.argtypes = [P, I, I64, I, I, I]
+    lib.rgg_grouped_gemm_wgrad_workspace.restype = I64
     lib.rgg_clip_grad_norm.argtypes = [P, P, I, ctypes.c_float, P, P, I64, P]
     lib.rgg_clip_grad_norm.restype = I
     lib.rgg_clip_grad_norm_workspace.argtypes = [I]
@@ -552,11 +555,18 @@ def rgg_grouped_gemm_wgrad(X, dY, group_offsets, dW=None, *, dtype=None, accumul
     else:
         _operand("dW", dW, dtype, (E, K, N), dev)
     device = dev.index
-    opt = None
+    flags = (1 if dtype == torch.float32 else 0) | (2 if accumulate else 0)
+    opt = workspace = None
     if bn or stages or max_ctas or timeout_ns or debug_flags:
         opt, _ = _options(0, bn, stages, max_ctas, timeout_ns, None, debug_flags)
+    elif M_tot >= 512 * E and E * -(-K // 256) * -(-N // 256) <= 128:
+        # few tiles with many rows: the library may want to split the rows
+        bytes_ = load_library().rgg_grouped_gemm_wgrad_workspace(_handle(device), E, M_tot, K, N, flags)
+        if bytes_ > 0:
+            workspace = _empty((bytes_ // 4,), torch.float32, dev, stream)
+            opt, _ = _options()
+            _set_workspace(opt, workspace)
     st = _raw_stream(stream, device)
-    flags = (1 if dtype == torch.float32 else 0) | (2 if accumulate else 0)
     s = load_library().rgg_grouped_gemm_wgrad(_handle(device), X.data_ptr(), dY.data_ptr(), group_offsets.data_ptr(),
                                               dW.data_ptr(), E, M_tot, K, N, flags, st, opt)
     _finish("rgg_grouped_gemm_wgrad", s, device, st, check)

@@ -50,6 +50,7 @@ struct WgradArgs {
     int32_t* status;
     int64_t M_tot;
     int32_t E, K, N;
+    int32_t split;                  // parts of an expert's rows, each with sums of its own (dW is then [E * split, K, N])
     int32_t tiles_n;                // N tiles of one expert
     int32_t tiles_e;                // tiles of one expert
     uint32_t by_tiles_n, by_tiles_e;  // n / d = (n * by) >> shift for 0 <= n < 2^30 (wgrad_divide)
@@ -173,7 +174,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         if (threadIdx.x == 0 && rank == 0) atomicCAS(args.status, 0, kStatusBadOffsets);
         return;
     }
-    const int32_t T = E * args.tiles_e;  // below 2^30 by the host's check
+    const int32_t T = E * args.split * args.tiles_e;  // below 2^30 by the host's check
     if (pair >= T) return;
 
     if (threadIdx.x == 32) {
@@ -217,6 +218,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     // The tile a pair takes in pass i: the list of all experts' tiles, one per
     // pair and pass.  (Over experts sorted by size, large and small ones in
     // turn, it measured 1-5 % slower on even and skewed routings alike.)
+    // With `split` parts, part s of expert e counts as expert e * split + s: an
+    // equal share of e's rows, rounded up to whole stages.
     struct Tile {
         int32_t expert, row0, rows, k0, n0;  // expert -1: no more tiles
     };
@@ -227,8 +230,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         t.expert = wgrad_divide(p, args.by_tiles_e, args.shift_e);
         const int32_t local = p - t.expert * args.tiles_e;
         const int32_t kt = wgrad_divide(local, args.by_tiles_n, args.shift_n);
-        t.row0 = s_off[t.expert];
-        t.rows = s_off[t.expert + 1] - t.row0;
+        if (args.split == 1) {
+            t.row0 = s_off[t.expert];
+            t.rows = s_off[t.expert + 1] - t.row0;
+        } else {
+            const int32_t e = t.expert / args.split, part = t.expert - e * args.split;
+            const int32_t m = s_off[e + 1] - s_off[e];
+            const int32_t share = ((m + args.split - 1) / args.split + kWgradRows - 1) / kWgradRows * kWgradRows;
+            const int32_t first = min(m, part * share);  // share * split < m + 64 * split, far below 2^31
+            t.row0 = s_off[e] + first;
+            t.rows = min(share, m - first);
+        }
         t.k0 = kt * kWgradBM;
         t.n0 = (local - kt * args.tiles_n) * BN;
         return t;

@@ -88,6 +88,54 @@ def test_accumulate(dtype, N):
         assert torch.equal(got[e], old[e]), "an expert without rows is left alone"
 
 
+SPLIT = [[4096], [15000, 0, 3603], [2, 9000], [9000, 9001, 8999, 1]]
+
+
+def _splits(counts, K, N):
+    return rgg.load_library().rgg_grouped_gemm_wgrad_workspace(rgg._handle(0), len(counts), sum(counts), K, N, 0) > 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts", SPLIT)
+def test_rows_split_where_tiles_are_few(counts, dtype):
+    assert _splits(counts, 136, 264)
+    X, dY, off = _case(counts, 136, 264, seed=len(counts), lead=0, spare=0)
+    got = _run(X, dY, off, dtype=dtype)
+    _check(X, dY, off, got)
+    assert torch.equal(_run(X, dY, off, dtype=dtype), got), "equal calls give equal bits"
+    old = torch.randn(len(counts), 136, 264, generator=torch.Generator().manual_seed(21)).to(dtype)
+    old[counts.index(0) if 0 in counts else 0, 0, 0] = -0.0
+    added = _run(X, dY, off, old.cuda(), accumulate=True)
+    ref, mag = refs.wgrad(X, dY, off)
+    refs.assert_close(added, ref + old.double(), _limit(ref + old.double(), mag, off, dtype, old), "dW")
+    if 0 in counts:
+        e, bits = counts.index(0), torch.int16 if dtype == torch.bfloat16 else torch.int32
+        assert not bool(got[e].any()) and torch.equal(added[e].view(bits), old[e].view(bits))
+
+
+def test_split_rows_with_bad_offsets_write_nothing():
+    X, dY, _ = _case([4096, 4096], 64, 72, seed=22, lead=0, spare=0)
+    assert _splits([4096, 4096], 64, 72)
+    dW = torch.full((2, 64, 72), 3.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(rgg.RggError) as ei:
+        rgg.rgg_grouped_gemm_wgrad(X.cuda(), dY.cuda(), torch.tensor([0, 5000, 4000], dtype=torch.int32, device="cuda"),
+                                   dW, check=True)
+    assert ei.value.status == rgg.RGG_ERR_BAD_OFFSETS
+    assert bool((dW == 3).all())
+
+
+def test_workspace_too_small():
+    X, dY, off = _case([4096], 64, 72, seed=23, lead=0, spare=0)
+    X, dY, off = X.cuda(), dY.cuda(), torch.from_numpy(off).cuda()
+    dW = torch.empty(1, 64, 72, dtype=torch.bfloat16, device="cuda")
+    opt, _ = rgg._options()
+    rgg._set_workspace(opt, torch.empty(64, device="cuda"))
+    s = rgg.load_library().rgg_grouped_gemm_wgrad(rgg._handle(0), X.data_ptr(), dY.data_ptr(), off.data_ptr(),
+                                                  dW.data_ptr(), 1, 4096, 64, 72, 0,
+                                                  torch.cuda.current_stream().cuda_stream, opt)
+    assert s == rgg.RGG_ERR_INVALID_ARG
+
+
 def test_neighbours_may_hold_anything():
     # each expert's sums stay finite while its neighbours' rows are Inf and NaN
     counts = [5, 16, 21, 64, 77, 3]

@@ -1,7 +1,9 @@
 // The gradient by the activations, dX_e = dY_e . W_e^T: the grouped product with
 // W read as it lies (kTransW, a K-major B operand), on every tile shape of the
 // forward product.  What bounds it is what bounds the forward product: the
-// same bytes per stage, MMAs and epilogue.
+// same bytes per stage, MMAs and epilogue.  32 experts, 32,768 rows, K = 6144,
+// N = 4096: 922 us from a pause (1 788 TFLOP/s), 1 092 us in a row at the power
+// cap; the forward product of the same size 916.
 #include "rgg_gemm_launch.cuh"
 
 namespace rgg {

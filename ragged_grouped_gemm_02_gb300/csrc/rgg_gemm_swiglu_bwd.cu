@@ -1,7 +1,10 @@
 // The backward pass of the fused gate-up projection with SiLU (epilogue
 // kEpiSwiGLUBwd): gate and up are computed again on the forward op's tiles and
 // the epilogue turns them and dH into [dGate | dUp] and H, so neither the gate
-// nor the up product is ever stored.
+// nor the up product is ever stored.  Bound by the MMAs at many rows (32,768 rows,
+// K = 6144, N = 2048: 945 us, 1 746 TFLOP/s), by bytes at few: 64 experts x 256
+// rows, K = 1024, N = 1344 takes 99 us at 5.7 TB/s (134 us while dH was read
+// after the accumulators were ready and outputs went out 16 bytes at a time).
 #include "rgg_gemm_launch.cuh"
 
 namespace rgg {

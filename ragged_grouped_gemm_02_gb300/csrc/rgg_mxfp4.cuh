@@ -18,7 +18,7 @@
 // Persistent over the flat tile list; warp 0 copies, warp 1 issues, warps 2-9
 // write, as in rgg_gemm.cuh.  A stage holds 256 of K: 128 bytes a row, one
 // swizzle row, K-major on both sides, and 1 KB of scales per 128 rows, which the
-// issuing thread copies from shared memory to TMEM (tcgen05.cp, in order before
+// issuing warp copies from shared memory to TMEM (tcgen05.cp, in order before
 // the MMAs that read them).
 //
 // TMEM (512 columns): two accumulators of 256 columns and the scales do not fit
@@ -27,6 +27,12 @@
 // lets the next tile's MMAs go (acc_empty) once it has them; it has then also
 // finished the tile before, so one barrier orders both hazards.  The scales of
 // a stage take 24 columns, in two sets used in turn.
+//
+// Measured on a GB300: 32 experts, 32,768 rows, K = 6144, N = 4096 240 us (6 870
+// TFLOP/s), gate-up of the same size 232 us; 16 rows per expert, gate-up, 74 us
+// (5.8 TB/s).  At many rows the issuing warp sets the pace: four MMAs (0.19 us at
+// the nominal rate) and six scale copies take 0.275 us a stage; tiles of 256 x
+// 192 with two whole accumulators took as long a stage and lost (287 us).
 #pragma once
 
 #include "rgg_mxfp4.h"

@@ -7,7 +7,9 @@
 // by a power of two, exact in fp32, so a result is the definition's bit for bit.
 // A block that holds Inf or NaN gets the scale NaN and codes zero.
 //
-// Bound by memory: 2 bytes read and 17/32 written per value.  Rows are read
+// Bound by memory: 2 bytes read and 17/32 written per value.  Measured on a
+// GB300: a weight of 32 x 6144 x 4096 303 us (98 % of the copy rate), 32,768 x
+// 6,144 rows 91 us (83 %); back 328 and 87 us.  Rows are read
 // with four 16-byte loads in flight a lane, four lanes a block.  A weight
 // [E, K, N] becomes [E, N, K / 2] on the way: a thread holds 32 values of K for
 // two neighbouring columns, so a warp reads whole 128-byte rows, and a CTA

@@ -28,8 +28,9 @@
 // which topped out near 3 TB/s.  (With accumulation each lane reads and writes
 // dW itself.)
 //
-// What bounds it: at few rows per expert the E * K * N outputs (the epilogue's
-// stores), at many the MMAs.  Roles as in rgg_gemm_2cta.cuh: warp 0 copies,
+// What bounds it: at few rows per expert the E * K * N outputs (64 experts x 16
+// rows, K = 1024, N = 2688: 87 us, 4.2 TB/s), at many the MMAs (32 experts,
+// 32,768 rows, K = 6144, N = 4096: 908 us, 1 816 TFLOP/s from a pause).  Roles as in rgg_gemm_2cta.cuh: warp 0 copies,
 // warp 1 issues (leader), warps 2-9 write, warp 10 makes the partial steps; two accumulator
 // buffers let a tile's stores run under the next tile's MMAs.  The two issuing
 // warps set the pace (a stage is 0.27 us of MMAs): they run in step, one lane

@@ -187,7 +187,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(accf_bar(a), 1);
-            mbar_init(acce_bar(a), 2 * kWgradEpiWarps);
+            mbar_init(acce_bar(a), kWgradEpiWarps);  // the half of both CTAs' that reads it
         }
         mbar_init(drain_bar, 1);
         misc[1] = 0u;
@@ -341,8 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
             const uint32_t lead = elect_one();
             int st = 0;
             uint32_t full_ph = 0, tail_ph = 0;  // one parity bit per slot and barrier
-            int acc = 0;
-            uint32_t acc_ph = 0;
+            uint32_t acc_ph = 0;  // one parity bit per accumulator
             bool ok = true;
             const uint64_t a_desc = sw128_desc(a0, kWgradPanel, 1024u), b_desc = sw128_desc(b0, kWgradPanel, 1024u);
             Tile next = tile_of_pass(0);
@@ -351,9 +350,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
                 next = tile_of_pass(i + 1);
                 if (t.rows == 0) continue;  // the epilogue writes zeros on its own
                 const uint32_t idesc = idesc_bf16_f32(kWgradBM, tile_cols(t), true) | (1u << 15);  // A MN-major too
+                const int acc = i & 1;
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-                ok = wait(acce_bar(acc), acc_ph ^ 1u);
+                ok = wait(acce_bar(acc), (acc_ph >> acc & 1u) ^ 1u);
                 if (!ok) break;
+                acc_ph ^= 1u << acc;
                 tc_fence_after_sync();
                 // A step's descriptors differ from the slot's first in their
                 // address field alone, 2048 bytes a step.
@@ -395,10 +396,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
                 }
                 if (!ok) break;
                 commit_if<true>(lead, accf_bar(acc));
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_ph ^= 1u;
-                }
             }
             if (!ok) {
                 commit_if<true>(lead, drain_bar);
@@ -463,24 +460,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ epilogue
+        // Two groups of four warps take the passes in turn, each with an
+        // accumulator of its own: one group's waits (for the accumulator, for
+        // TMEM, for a buffer's last store) run under the other's stores.
         const int q = warp & 3;
-        const int part = (warp - 2) >> 2;
+        const int acc = (warp - 2) >> 2;
         const uint32_t boxes = base + sp.out_off + (warp - 2) * (kWgradBoxes * kWgradBox);
-        int acc = 0;
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
         uint32_t acc_ph = 0;
-        Tile next = tile_of_pass(0);
-        for (int32_t i = 0; next.expert >= 0; ++i) {
+        Tile next = tile_of_pass(acc);
+        for (int32_t i = acc; next.expert >= 0; i += 2) {
             const Tile t = next;
-            next = tile_of_pass(i + 1);
+            next = tile_of_pass(i + 2);
             if (kAdd && t.rows == 0) continue;  // nothing to add
             const int32_t ncols = tile_cols(t);
-            const int pc = ncols / 2;
             const int32_t k = t.k0 + 128 * static_cast<int32_t>(rank) + 32 * q;  // the warp's first row of dW
             if (t.rows > 0) {
                 if (!wait(accf_bar(acc), acc_ph)) break;
+                acc_ph ^= 1u;
                 tc_fence_after_sync();
             }
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
+            // 32 columns of the tile; the values are there after tmem_ld_wait
             auto load = [&](int cc, uint32_t (&v)[32]) {
                 if (t.rows > 0 &&
                     RGG_BOUNDS_OK(tmem_cols_ok(static_cast<uint32_t>(acc * BN + cc), 32, 512), args.status)) {
@@ -490,9 +490,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
                     for (int j = 0; j < 32; ++j) v[j] = 0u;
                 }
             };
+            auto release = [&]() {  // every value of the tile is in registers
+                if (t.rows == 0) return;
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(acce_bar(acc), 0));
+            };
             if constexpr (kAdd) {
 #pragma unroll 1
-                for (int cc = part * pc; cc < (part + 1) * pc; cc += 32) {
+                for (int cc = 0; cc < ncols; cc += 32) {
                     const int32_t col = t.n0 + cc;
                     if (col >= args.N) break;
                     uint32_t v[32];
@@ -503,63 +509,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
                         wgrad_add<kF32>(args.dW,
                                         (static_cast<int64_t>(t.expert) * args.K + k + lane) * args.N + col, cols, v);
                 }
+                release();
             } else {
-                // All of the warp's sums are taken from TMEM at once, so that
-                // the accumulator is free for the tile after the next before
-                // any is stored.
-                constexpr int kHalf = BN / 2;
-                uint32_t v[kHalf];
-#pragma unroll
-                for (int c = 0; c < kHalf; c += 32) {
-                    uint32_t(&x)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[c]);
-                    if (c < pc) load(part * pc + c, x);
-                }
-                if (t.rows > 0) {
-                    tmem_ld_wait();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_rank(acce_bar(acc), 0));
-                }
-                constexpr int kWords = kF32 ? kHalf : kHalf / 2;  // 32-bit words a lane stores
-                if constexpr (!kF32) {
-#pragma unroll
-                    for (int c = 0; c < kWords; ++c) v[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
-                }
+                // A box at a time, the next one's sums on their way from TMEM
+                // while this one is stored; a tile has an even number of boxes.
                 constexpr int kBoxCols = kF32 ? 32 : 64;
+                uint32_t v[kBoxCols];
+                auto load_box = [&](int b) {
 #pragma unroll
-                for (int c = 0; c < kWords; c += 32 * kWgradBoxes) {
-                    // the stores that last read these buffers are done with them
-                    if (lane == 0) bulk_wait<0, true>();
+                    for (int c = 0; c < kBoxCols; c += 32)
+                        load(b * kBoxCols + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+                };
+                load_box(0);
+#pragma unroll
+                for (int b = 0; b < BN / kBoxCols; ++b) {
+                    if (b * kBoxCols >= ncols) break;
+                    tmem_ld_wait();
+                    uint32_t w[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        if constexpr (kF32) {
+                            w[c] = v[c];
+                        } else {
+                            asm volatile("" : "+r"(v[2 * c]), "+r"(v[2 * c + 1]));  // not before the wait
+                            w[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
+                        }
+                    }
+                    if ((b + 1) * kBoxCols < ncols) load_box(b + 1);
+                    else release();
+                    // the store before the last is done with its buffer
+                    const uint32_t box = boxes + (b & 1) * kWgradBox;
+                    if (lane == 0) bulk_wait<kWgradBoxes - 1, true>();
                     __syncwarp();
-#pragma unroll
-                    for (int b = 0; b < kWgradBoxes; ++b)
-                        if (c + 32 * b < kWords)
-                            wgrad_stage(boxes + b * kWgradBox, lane,
-                                        *reinterpret_cast<uint32_t(*)[32]>(&v[(c + 32 * b) % kWords]));
+                    wgrad_stage(box, lane, w);
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-#pragma unroll
-                        for (int b = 0; b < kWgradBoxes; ++b) {
-                            const int32_t in = (c / 32 + b) * kBoxCols;  // first column of the box in the warp's half
-                            const int32_t col = t.n0 + part * pc + in;
-                            if (c + 32 * b < kWords && in < pc && col < args.N && k < args.K &&
-                                RGG_BOUNDS_OK(store_ok(k, col, 8, 0, args.K, args.N), args.status))
-                                tma_store_3d(&tmap_dw, boxes + b * kWgradBox, col, k, t.expert);
-                        }
+                        const int32_t col = t.n0 + b * kBoxCols;
+                        if (col < args.N && k < args.K &&
+                            RGG_BOUNDS_OK(store_ok(k, col, 8, 0, args.K, args.N), args.status))
+                            tma_store_3d(&tmap_dw, box, col, k, t.expert);
                         bulk_commit();
                     }
-                }
-            }
-            if (t.rows > 0) {
-                if (kAdd) {
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_rank(acce_bar(acc), 0));
-                }
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_ph ^= 1u;
                 }
             }
         }

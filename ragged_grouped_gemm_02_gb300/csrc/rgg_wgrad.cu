@@ -175,7 +175,7 @@ extern "C" rgg_status rgg_grouped_gemm_wgrad(rgg_handle* h, const void* X, const
     const int out_flags = split > 1 ? RGG_WGRAD_FP32 : flags;
     if (tiles(bn) * split >= (int64_t(1) << 30)) return RGG_ERR_UNSUPPORTED;
     const int64_t room = static_cast<int64_t>(dev.smem_optin) - 1024 - wgrad_smem(bn, 0, E).total;
-    const int per_stage = (2 + bn / 128) * static_cast<int>(kWgradPanel) + 32;
+    const int per_stage = (2 + bn / 128) * static_cast<int>(kWgradPanel) + 8 * (3 + kWgradTailWarps);
     const int fit = static_cast<int>(std::min<int64_t>(8, room / per_stage));
     const int stages = want_stages ? want_stages : fit;
     if (stages < 2 || stages > fit) return RGG_ERR_UNSUPPORTED;

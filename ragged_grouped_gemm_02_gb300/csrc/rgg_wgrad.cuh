@@ -21,7 +21,9 @@
 // global memory, ahead of time, and when the producer has the slot (tail[s])
 // writes them and zeros to the slot, makes that visible to the tensor core's
 // proxy and tells the leader (fixed[s]).  Copying whole steps and zeroing the
-// rows past the end once they had landed cost 1.1 us of each tile.
+// rows past the end once they had landed cost 1.1 us of each tile.  A step takes
+// such a warp 2.2 us, mostly the reads' latency, so two take the tiles in turn:
+// 64 experts of one row each went from 85 to 68 us; a third and fourth gain nothing.
 //
 // Results leave through shared memory and TMA stores, 128 bytes of a row at a
 // time: straight from registers each lane writes 32 bytes of a row of its own,
@@ -29,11 +31,14 @@
 // dW itself.)
 //
 // What bounds it: at few rows per expert the E * K * N outputs (64 experts x 16
-// rows, K = 1024, N = 2688: 87 us, 4.2 TB/s), at many the MMAs (32 experts,
-// 32,768 rows, K = 6144, N = 4096: 908 us, 1 816 TFLOP/s from a pause).  Roles as in rgg_gemm_2cta.cuh: warp 0 copies,
-// warp 1 issues (leader), warps 2-9 write, warp 10 makes the partial steps; two accumulator
-// buffers let a tile's stores run under the next tile's MMAs.  The two issuing
-// warps set the pace (a stage is 0.27 us of MMAs): they run in step, one lane
+// rows, K = 1024, N = 2688: 68 us, 5.3 TB/s), at many the MMAs (32 experts,
+// 32,768 rows, K = 6144, N = 4096: 920 us, 1 792 TFLOP/s from a pause).  Roles
+// as in rgg_gemm_2cta.cuh: warp 0 copies, warp 1 issues (leader), warps 2-9
+// write, warps 10 and 11 make the partial steps.  The writing warps are two
+// groups with an accumulator each that take the tiles in turn, so that one
+// group's waits run under the other's stores: with all eight on one tile a tile
+// took 1.4 us beside its stores (16 rows: 87 us).  The two issuing warps set the
+// pace at many rows (a stage is 0.27 us of MMAs): they run in step, one lane
 // issuing (rgg_warp_issue.cuh), and their loops over whole stages hold no more
 // than the waits, copies and MMAs.  Each role decodes its next tile before it
 // works on the one at hand.
@@ -64,8 +69,9 @@ struct WgradArgs {
 constexpr int kWgradBM = 256;        // K columns per pair tile
 constexpr int kWgradRows = 64;       // rows (reduction) per stage
 constexpr int kWgradEpiWarps = 8;
-constexpr int kWgradTailWarp = 2 + kWgradEpiWarps;
-constexpr int kWgradThreads = 96 + 32 * kWgradEpiWarps;
+constexpr int kWgradTailWarp = 2 + kWgradEpiWarps;  // the first of them
+constexpr int kWgradTailWarps = 2;
+constexpr int kWgradThreads = 32 * (2 + kWgradEpiWarps + kWgradTailWarps);
 constexpr uint32_t kWgradPanel = kWgradRows * 128u;
 constexpr uint32_t kWgradBox = 32u * 128u;  // one store: 32 rows of 128 bytes (64 bf16 or 32 fp32 columns)
 constexpr int kWgradBoxes = 2;              // store buffers of an epilogue warp
@@ -88,8 +94,9 @@ __host__ __device__ inline WgradSmem wgrad_smem(int BN, int stages, int E) {
     p.a_off = 0;
     p.b_off = p.a_off + stages * p.a_stage;
     p.out_off = p.b_off + stages * p.b_stage;
-    p.bar_off = p.out_off + kWgradEpiWarps * kWgradBoxes * kWgradBox;  // full[S], empty[S], tail[S], fixed[S], acc_full[2], acc_empty[2], drain
-    p.misc_off = p.bar_off + 8u * (4u * stages + 5u);
+    // full[S], empty[S], fixed[S], tail[warps][S], acc_full[2], acc_empty[2], drain
+    p.bar_off = p.out_off + kWgradEpiWarps * kWgradBoxes * kWgradBox;
+    p.misc_off = p.bar_off + 8u * ((3u + kWgradTailWarps) * stages + 5u);
     p.off_off = p.misc_off + 16u;  // tmem base, abort flag
     p.total = p.off_off + ex;
     return p;
@@ -159,11 +166,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     const uint32_t bars = base + sp.bar_off;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
-    auto tail_bar = [&](int s) { return bars + 8u * (2 * S + s); };
-    auto fixed_bar = [&](int s) { return bars + 8u * (3 * S + s); };
-    auto accf_bar = [&](int a) { return bars + 8u * (4 * S + a); };
-    auto acce_bar = [&](int a) { return bars + 8u * (4 * S + 2 + a); };
-    const uint32_t drain_bar = bars + 8u * (4 * S + 4);
+    auto fixed_bar = [&](int s) { return bars + 8u * (2 * S + s); };
+    auto tail_bar = [&](int w, int s) { return bars + 8u * ((3 + w) * S + s); };  // the tail warps' own
+    const uint32_t acc_bars = bars + 8u * (3 + kWgradTailWarps) * S;
+    auto accf_bar = [&](int a) { return acc_bars + 8u * a; };
+    auto acce_bar = [&](int a) { return acc_bars + 8u * (2 + a); };
+    const uint32_t drain_bar = acc_bars + 8u * 4;
     uint32_t* misc = reinterpret_cast<uint32_t*>(gbase + sp.misc_off);
     int32_t* s_off = reinterpret_cast<int32_t*>(gbase + sp.off_off);
 
@@ -182,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
-            mbar_init(tail_bar(s), 1);
+            for (int w = 0; w < kWgradTailWarps; ++w) mbar_init(tail_bar(w, s), 1);
             mbar_init(fixed_bar(s), 2);
         }
         for (int a = 0; a < 2; ++a) {
@@ -310,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
                     if (!ok) break;
                     const int steps = v / 16;  // whole ones; the tail warp makes the one after
                     counted &= ~(1u << st);
-                    if ((v & 15) != 0 && lead) mbar_arrive(tail_bar(st));
+                    if ((v & 15) != 0 && lead) mbar_arrive(tail_bar(i % kWgradTailWarps, st));
                     if (steps > 0) {
                         if (rank == 0) expect_tx_if(lead, full_bar(st), 2u * (2u + np) * steps * 2048u);
                         for (int j = 0; j < steps; ++j)
@@ -403,8 +411,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == kWgradTailWarp) {
-        // --------------------- steps that end inside, the whole warp of each CTA
+    } else if (warp >= kWgradTailWarp) {
+        // ------------- steps that end inside, whole warps that take the passes in turn
         int st = 0;
         uint32_t tail_ph = 0;
         Tile next = tile_of_pass(0);
@@ -414,7 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
             const int32_t whole = t.rows / kWgradRows, v = t.rows % kWgradRows;
             st = static_cast<int>(static_cast<uint32_t>(st + whole) % static_cast<uint32_t>(S));
             if (v == 0) continue;
-            if ((v & 15) != 0) {
+            if ((v & 15) != 0 && i % kWgradTailWarps == warp - kWgradTailWarp) {
                 // 16 rows of each panel: lane and i give the row and the 16-byte piece of it
                 const int np = tile_cols(t) / 128;
                 const int32_t first = v & ~15;
@@ -436,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
                                       : make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
-                if (!wait(tail_bar(st), tail_ph >> st & 1u)) break;
+                if (!wait(tail_bar(warp - kWgradTailWarp, st), tail_ph >> st & 1u)) break;
                 tail_ph ^= 1u << st;
 #pragma unroll
                 for (int p = 0; p < 2 + kBPanels; ++p) {

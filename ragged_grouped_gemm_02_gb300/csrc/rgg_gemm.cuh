@@ -263,13 +263,20 @@ __device__ __forceinline__ int tile_panels(int32_t col0, int32_t N) {
 // columns.  Measured on a GB300: FP8 uniform 975 -> 1 370 TFLOP/s, fused
 // gate-up uniform 914 -> 1 000 and skew16k 696 -> 816; for plain bf16 the
 // same split lost 3-5 %.
-template <int kEpi, bool kFp8>
+template <int kEpi, bool kFp8, bool kTransW = false>
 __host__ __device__ constexpr int epilogue_warps() {
-    return (kFp8 || epi_gate_up(kEpi)) ? 8 : 4;
+    return (kFp8 || epi_gate_up(kEpi) || kTransW) ? 8 : 4;
 }
-template <int kEpi, bool kFp8>
+// Groups of epilogue warps that take the tiles in turn, one per accumulator.
+// The transposed product has two, four warps each: a tile of few reduction
+// stages is bound by its stores, and one group's waits run under the other's.
+template <bool kTransW>
+__host__ __device__ constexpr int epilogue_groups() {
+    return kTransW ? 2 : 1;
+}
+template <int kEpi, bool kFp8, bool kTransW = false>
 __host__ __device__ constexpr int cta_threads() {
-    return 64 + 32 * epilogue_warps<kEpi, kFp8>();
+    return 64 + 32 * epilogue_warps<kEpi, kFp8, kTransW>();
 }
 
 __device__ __forceinline__ float silu_f32(float z) { return z / (1.0f + __expf(-z)); }
@@ -464,7 +471,7 @@ constexpr int kGatherTma = 1;
 // are the same.
 template <int BM, int BN, int kEpi = kEpiPlain, bool kFp8 = false, int kGather = kGatherNone, bool kDyn = false,
           bool kTransW = false>
-__global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
+__global__ void __launch_bounds__(cta_threads<kEpi, kFp8, kTransW>(), 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_x64,
                         const __grid_constant__ CUtensorMap tmap_w, const GemmArgs args) {
     using Cfg = TileConfig<BM, BN, kFp8>;
@@ -581,13 +588,13 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(accf_bar(a), 1);
-            mbar_init(acce_bar(a), epilogue_warps<kEpi, kFp8>());
+            mbar_init(acce_bar(a), epilogue_warps<kEpi, kFp8, kTransW>() / epilogue_groups<kTransW>());
         }
         mbar_init(drain_bar, 1);
         if constexpr (kDyn) {
             for (int i = 0; i < kQueueDepth; ++i) {
                 mbar_init(qfull_bar(i), 1);
-                mbar_init(qempty_bar(i), 1 + epilogue_warps<kEpi, kFp8>());
+                mbar_init(qempty_bar(i), 1 + epilogue_warps<kEpi, kFp8, kTransW>());
             }
         }
         misc[1] = 0u;
@@ -896,14 +903,23 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
     } else {
         // ------------------------------------------------------- S6: epilogue
         const int q = warp & 3;  // TMEM lane quadrant this warp may read
-        constexpr int kParts = epilogue_warps<kEpi, kFp8>() / 4;  // warps per quadrant
+        constexpr int kGroups = epilogue_groups<kTransW>();
+        constexpr int kParts = epilogue_warps<kEpi, kFp8, kTransW>() / 4 / kGroups;  // warps per quadrant and tile
         constexpr int kPartCols = kOutN / kParts;                  // tile columns each of them writes
         static_assert(kPartCols % 32 == 0, "each epilogue warp handles whole 32-column chunks");
-        const int cc0 = ((warp - 2) >> 2) * kPartCols;
+        const int cc0 = kGroups == 2 ? 0 : ((warp - 2) >> 2) * kPartCols;
         int acc = 0;
         uint32_t acc_ph = 0;
         // false when the CTA aborts
         auto epi_tile = [&](const TileCoord& c) -> bool {
+            auto advance = [&]() {
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_ph ^= 1u;
+                }
+                return true;
+            };
+            if (kGroups == 2 && acc != (warp - 2) >> 2) return advance();  // the other group's
             // M = 128: tile row 32q + lane sits in TMEM lane 32q + lane.  M = 64:
             // tile row 16q + i sits in TMEM lane 32q + i (i < 16).
             const bool half = runs_as_64_rows<BM>(args, c);
@@ -920,11 +936,7 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8>(), 1)
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(acce_bar(acc));
-            if (++acc == 2) {
-                acc = 0;
-                acc_ph ^= 1u;
-            }
-            return true;
+            return advance();
         };
         if (kDyn && !args.sched_claims) {
             ClassWalk cw;

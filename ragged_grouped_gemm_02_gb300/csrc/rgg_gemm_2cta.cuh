@@ -77,9 +77,10 @@ __device__ __forceinline__ bool pair_runs_as_128_rows(const GemmArgs& args, cons
 // lane quadrant, each on half of the columns) for the fused gate-up epilogue,
 // whose exponentials otherwise outlast the main loop (measured: uniform 845 ->
 // 1 018 TFLOP/s, prefill 1 417 -> 1 526).
-template <int kEpi>
+// The transposed product has eight in two groups (epilogue_groups).
+template <int kEpi, bool kTransW = false>
 __host__ __device__ constexpr int pair_epilogue_warps() {
-    return epi_gate_up(kEpi) ? 8 : 4;
+    return epi_gate_up(kEpi) || kTransW ? 8 : 4;
 }
 
 // kDyn: the pair kernel of the mixed launch (rgg_sched.cuh).  The leader's
@@ -92,7 +93,7 @@ __host__ __device__ constexpr int pair_epilogue_warps() {
 // kTransW: Y_e = X_e . W_e^T with W in [E, N, K] order (K contiguous): B panels
 // of 64 W rows by 64 K elements, as in the 1-CTA kernel.
 template <int BN, int kEpi = kEpiPlain, bool kDyn = false, bool kTransW = false>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilogue_warps<kEpi>(), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilogue_warps<kEpi, kTransW>(), 1)
     grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_x64,
                              const __grid_constant__ CUtensorMap tmap_w, const GemmArgs args) {
     using Cfg = PairConfig<BN>;
@@ -189,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(accf_bar(a), 1);
-            mbar_init(acce_bar(a), 2 * pair_epilogue_warps<kEpi>());
+            mbar_init(acce_bar(a), 2 * pair_epilogue_warps<kEpi, kTransW>() / epilogue_groups<kTransW>());
         }
         mbar_init(drain_bar, 1);
         if constexpr (kDyn) {
@@ -197,7 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
             // epilogue warps and the peer's producer and epilogue warps
             for (int i = 0; i < kQueueDepth; ++i) {
                 mbar_init(qfull_bar(i), 1);
-                mbar_init(qempty_bar(i), 2 + 2 * pair_epilogue_warps<kEpi>());
+                mbar_init(qempty_bar(i), 2 + 2 * pair_epilogue_warps<kEpi, kTransW>());
             }
         }
         misc[1] = 0u;
@@ -483,10 +484,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
         // ------------------------------------------------------- S6: epilogue
         const int q = warp & 3;
         const int N = args.N;
+        constexpr int kGroups = epilogue_groups<kTransW>();
         int acc = 0;
         uint32_t acc_ph = 0;
         // false when the pair aborts
         auto epi_tile = [&](const TileCoord& c) -> bool {
+            auto advance = [&]() {
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_ph ^= 1u;
+                }
+                return true;
+            };
+            if (kGroups == 2 && acc != (warp - 2) >> 2) return advance();  // the other group's
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
             // M = 256: this CTA's 128 rows, one per TMEM lane, all BN columns.
             // M = 128: this CTA's 64 rows fill the 128 lanes twice over (GB300
@@ -505,9 +515,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
             (void)row_lo;
             (void)row_hi;
             __nv_bfloat16* yrow = args.Y + row * N + c.col0 + cbase;
-            constexpr int kParts = pair_epilogue_warps<kEpi>() / 4;  // warps per lane quadrant
-            const int pc = ncols / kParts;                                // columns each of them writes
-            const int c0 = ((warp - 2) >> 2) * pc;
+            constexpr int kParts = pair_epilogue_warps<kEpi, kTransW>() / 4 / kGroups;  // warps per lane quadrant and tile
+            const int pc = ncols / kParts;                                               // columns each of them writes
+            const int c0 = kGroups == 2 ? 0 : ((warp - 2) >> 2) * pc;
             GradRow grad;
             if constexpr (kEpi == kEpiSwiGLUBwd) grad.load(args, row_ok, row, c.col0 + cbase + c0, pc);
             if (!warp_await(accf_bar(acc), acc_ph)) return false;
@@ -571,11 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_rank(acce_bar(acc), 0));
-            if (++acc == 2) {
-                acc = 0;
-                acc_ph ^= 1u;
-            }
-            return true;
+            return advance();
         };
         if (kDyn && !args.sched_claims) {
             ClassWalk cw;

@@ -15,7 +15,7 @@ cudaError_t launch_gemm_instance(int grid, size_t smem, cudaStream_t stream, con
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(smem));
     if (err != cudaSuccess) return err;
-    return launch_chained(kernel, grid, cta_threads<kEpi, kFp8>(), smem, stream, tmap_x, tmap_x64, tmap_w, args);
+    return launch_chained(kernel, grid, cta_threads<kEpi, kFp8, kTransW>(), smem, stream, tmap_x, tmap_x64, tmap_w, args);
 }
 
 template <int BN, int kEpi = kEpiPlain, bool kTransW = false>
@@ -26,7 +26,7 @@ cudaError_t launch_pair_instance(int grid, size_t smem, cudaStream_t stream, con
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(smem));
     if (err != cudaSuccess) return err;
-    return launch_chained(kernel, grid, 64 + 32 * pair_epilogue_warps<kEpi>(), smem, stream, tmap_x, tmap_x64, tmap_w,
+    return launch_chained(kernel, grid, 64 + 32 * pair_epilogue_warps<kEpi, kTransW>(), smem, stream, tmap_x, tmap_x64, tmap_w,
                           args);
 }
 
@@ -44,7 +44,7 @@ cudaError_t launch_mixed_instance(int pair_grid, size_t pair_smem, const GemmArg
         cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(pair_smem));
         if (err != cudaSuccess) return err;
-        err = launch_chained(kernel, pair_grid, 64 + 32 * pair_epilogue_warps<kEpi>(), pair_smem, stream, tmap_x,
+        err = launch_chained(kernel, pair_grid, 64 + 32 * pair_epilogue_warps<kEpi, kTransW>(), pair_smem, stream, tmap_x,
                              tmap_x64, tmap_w, pair_args);
         if (err != cudaSuccess) return err;
     }
@@ -60,7 +60,7 @@ cudaError_t launch_mixed_instance(int pair_grid, size_t pair_smem, const GemmArg
         // (no pair CTAs) it waits first, like every other kernel.
         GemmArgs a = single_args;
         a.pdl_wait_first = pair_grid > 0 ? 0 : 1;
-        return launch_chained(kernel, single_grid, cta_threads<kEpi, false>(), single_smem, stream, tmap_x, tmap_x64,
+        return launch_chained(kernel, single_grid, cta_threads<kEpi, false, kTransW>(), single_smem, stream, tmap_x, tmap_x64,
                               tmap_w, a);
     }
     return cudaSuccess;

@@ -281,6 +281,45 @@ __host__ __device__ constexpr int cta_threads() {
 
 __device__ __forceinline__ float silu_f32(float z) { return z / (1.0f + __expf(-z)); }
 
+// Stores 32 columns of the warp's rows (each lane's in w, four consecutive lanes
+// on consecutive rows of the output, `row_ok` where its row is written), the
+// first column `col` of `limit`, where rows are 16 but not 32 bytes aligned.
+// Every four lanes turn their 16-byte pieces round first (two exchanges), so
+// that they write 64 bytes of one row together: with 16 bytes a lane, each in a
+// row of its own, no sector is written whole.
+__device__ __forceinline__ void store_rows_turned(__nv_bfloat16* out, int64_t pitch, int64_t row, bool row_ok, int col,
+                                                  int limit, const uint32_t (&w)[16], int lane, int32_t row_lo,
+                                                  int32_t row_hi, int32_t* status) {
+    const uint32_t rows = __ballot_sync(0xffffffffu, row_ok);
+    uint32_t x[4][4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[p][k] = w[4 * p + k];
+#pragma unroll
+    for (int step = 1; step <= 2; step *= 2) {
+        const bool upper = (lane & step) != 0;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            if ((p & step) != 0) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[p][k] : x[p + step][k], step);
+                if (upper) x[p][k] = got;
+                else x[p + step][k] = got;
+            }
+        }
+    }
+    const int j = lane & 3, c = col + 8 * j;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int64_t r = row + p - j;
+        if ((rows >> ((lane & ~3) + p) & 1u) && c + 8 <= limit &&
+            RGG_BOUNDS_OK(store_ok(r, c, 8, row_lo, row_hi, limit), status))
+            st_global_v4(out + r * pitch + c, x[p][0], x[p][1], x[p][2], x[p][3]);
+    }
+}
+
 // The part of dH that a lane of the gate-up backward's epilogue needs: up to 64
 // columns of one row, read before the accumulators are waited for.
 struct GradRow {
@@ -300,29 +339,25 @@ struct GradRow {
 // s = 1 / (1 + exp(-g)),
 //     dG = dH * u * s * (1 + g * (1 - s)),  dU = dH * g * s,  H = g * s * u,
 // in fp32 from the unrounded accumulators, each rounded once to bf16.
-__device__ __forceinline__ void store_swiglu_backward(const GemmArgs& args, int64_t row, int col,
+__device__ __forceinline__ void store_swiglu_backward(const GemmArgs& args, int64_t row, bool row_ok, int col,
                                                       const uint32_t (&v)[32], const uint32_t (&u)[32],
-                                                      const GradRow& grad, bool second, int32_t row_lo,
+                                                      const GradRow& grad, bool second, int lane, int32_t row_lo,
                                                       int32_t row_hi) {
     const int N = args.N;
-    __nv_bfloat16* dg_out = args.Y + row * (2 * static_cast<int64_t>(N)) + col;
-    __nv_bfloat16* act_out = args.act ? args.act + row * N + col : nullptr;
+    const int64_t pitch = 2 * static_cast<int64_t>(N);
+    uint32_t wg[16], wu[16], wh[16];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int at = 16 * h;  // 16 columns at a time, 32 bytes of each output
-        if (col + at >= N) break;
-        if (!RGG_BOUNDS_OK(store_ok(row, col + at, 8, row_lo, row_hi, N), args.status)) break;
         const uint4 d0 = second ? grad.d[4 + 2 * h] : grad.d[2 * h];
         const uint4 d1 = second ? grad.d[5 + 2 * h] : grad.d[2 * h + 1];
         const uint32_t dw[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-        uint32_t wg[8], wu[8], wh[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float dg[2], du[2], hh[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float g = __uint_as_float(v[at + 2 * i + j]);
-                const float up = __uint_as_float(u[at + 2 * i + j]);
+                const float g = __uint_as_float(v[16 * h + 2 * i + j]);
+                const float up = __uint_as_float(u[16 * h + 2 * i + j]);
                 const float d = __uint_as_float(j ? (dw[i] & 0xffff0000u) : (dw[i] << 16));
                 const float s = __fdividef(1.0f, 1.0f + __expf(-g));
                 const float gs = g * s;
@@ -330,21 +365,30 @@ __device__ __forceinline__ void store_swiglu_backward(const GemmArgs& args, int6
                 du[j] = d * gs;
                 dg[j] = d * up * s * (1.0f + (g - gs));
             }
-            wg[i] = pack_bf16x2(__float_as_uint(dg[0]), __float_as_uint(dg[1]));
-            wu[i] = pack_bf16x2(__float_as_uint(du[0]), __float_as_uint(du[1]));
-            wh[i] = pack_bf16x2(__float_as_uint(hh[0]), __float_as_uint(hh[1]));
+            wg[8 * h + i] = pack_bf16x2(__float_as_uint(dg[0]), __float_as_uint(dg[1]));
+            wu[8 * h + i] = pack_bf16x2(__float_as_uint(du[0]), __float_as_uint(du[1]));
+            wh[8 * h + i] = pack_bf16x2(__float_as_uint(hh[0]), __float_as_uint(hh[1]));
         }
-        auto store = [&](__nv_bfloat16* p, const uint32_t (&w)[8]) {
-            if (col + at + 16 <= N && args.y_vec32) {
-                st_global_v8(p, w);
-            } else {
-                st_global_v4(p, w[0], w[1], w[2], w[3]);
-                if (col + at + 16 <= N) st_global_v4(p + 8, w[4], w[5], w[6], w[7]);
-            }
+    }
+    if (!args.y_vec32) {
+        store_rows_turned(args.Y, pitch, row, row_ok, col, N, wg, lane, row_lo, row_hi, args.status);
+        store_rows_turned(args.Y + N, pitch, row, row_ok, col, N, wu, lane, row_lo, row_hi, args.status);
+        if (args.act) store_rows_turned(args.act, N, row, row_ok, col, N, wh, lane, row_lo, row_hi, args.status);
+        return;
+    }
+    // whole 16 columns: N is a multiple of 16
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int c = col + 16 * h;
+        if (!row_ok || c >= N || !RGG_BOUNDS_OK(store_ok(row, c, 16, row_lo, row_hi, N), args.status)) continue;
+        auto store = [&](__nv_bfloat16* p, const uint32_t (&w)[16]) {
+            const uint32_t x[8] = {w[8 * h],     w[8 * h + 1], w[8 * h + 2], w[8 * h + 3],
+                                   w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]};
+            st_global_v8(p, x);
         };
-        store(dg_out + at, wg);
-        store(dg_out + N + at, wu);
-        if (act_out) store(act_out + at, wh);
+        store(args.Y + row * pitch + c, wg);
+        store(args.Y + row * pitch + N + c, wu);
+        if (args.act) store(args.act + row * N + c, wh);
     }
 }
 
@@ -386,8 +430,7 @@ __device__ __forceinline__ void epilogue_store_tile(const GemmArgs& args, const 
             if (!ld_ok)
                 for (int i = 0; i < 32; ++i) v[i] = 0u;
             if constexpr (kEpi == kEpiSwiGLUBwd) {
-                if (row_ok)
-                    store_swiglu_backward(args, row, c.col0 + cc, v, u, grad, cc != cc0, row_lo, row_hi);
+                store_swiglu_backward(args, row, row_ok, c.col0 + cc, v, u, grad, cc != cc0, lane, row_lo, row_hi);
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -420,7 +463,12 @@ __device__ __forceinline__ void epilogue_store_tile(const GemmArgs& args, const 
                 }
             }
         }
-        if (kEpi != kEpiSwiGLUBwd && row_ok) {
+        if (kEpi != kEpiSwiGLUBwd && !args.y_vec32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            store_rows_turned(args.Y, N, row, row_ok, c.col0 + cc, N, w, lane, row_lo, row_hi, args.status);
+        } else if (kEpi != kEpiSwiGLUBwd && row_ok) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int col = c.col0 + cc + 16 * h;
@@ -429,14 +477,7 @@ __device__ __forceinline__ void epilogue_store_tile(const GemmArgs& args, const 
                 for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[16 * h + 2 * i], v[16 * h + 2 * i + 1]);
                 __nv_bfloat16* dst = yrow + cc + 16 * h;
                 if (col + 16 <= N) {
-                    if (RGG_BOUNDS_OK(store_ok(row, col, 16, row_lo, row_hi, N), args.status)) {
-                        if (args.y_vec32) {
-                            st_global_v8(dst, w);
-                        } else {
-                            st_global_v4(dst, w[0], w[1], w[2], w[3]);
-                            st_global_v4(dst + 8, w[4], w[5], w[6], w[7]);
-                        }
-                    }
+                    if (RGG_BOUNDS_OK(store_ok(row, col, 16, row_lo, row_hi, N), args.status)) st_global_v8(dst, w);
                 } else if (col + 8 <= N) {
                     if (RGG_BOUNDS_OK(store_ok(row, col, 8, row_lo, row_hi, N), args.status))
                         st_global_v4(dst, w[0], w[1], w[2], w[3]);

@@ -542,8 +542,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                     if (!ld_ok)
                         for (int i = 0; i < 32; ++i) v[i] = 0u;
                     if constexpr (kEpi == kEpiSwiGLUBwd) {
-                        if (row_ok)
-                            store_swiglu_backward(args, row, c.col0 + cbase + cc, v, u, grad, cc != c0, row_lo, row_hi);
+                        store_swiglu_backward(args, row, row_ok, c.col0 + cbase + cc, v, u, grad, cc != c0, lane,
+                                              row_lo, row_hi);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -554,7 +554,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                     if (!ld_ok)
                         for (int i = 0; i < 32; ++i) v[i] = 0u;
                 }
-                if (kEpi != kEpiSwiGLUBwd && row_ok) {
+                if (kEpi != kEpiSwiGLUBwd && !args.y_vec32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+                    store_rows_turned(args.Y, N, row, row_ok, c.col0 + cbase + cc, N, w, lane, row_lo, row_hi,
+                                      args.status);
+                } else if (kEpi != kEpiSwiGLUBwd && row_ok) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int col = c.col0 + cbase + cc + 16 * h;
@@ -563,14 +569,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
                         for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[16 * h + 2 * i], v[16 * h + 2 * i + 1]);
                         __nv_bfloat16* dst = yrow + cc + 16 * h;
                         if (col + 16 <= N) {
-                            if (RGG_BOUNDS_OK(store_ok(row, col, 16, row_lo, row_hi, N), args.status)) {
-                                if (args.y_vec32) {
-                                    st_global_v8(dst, w);
-                                } else {
-                                    st_global_v4(dst, w[0], w[1], w[2], w[3]);
-                                    st_global_v4(dst + 8, w[4], w[5], w[6], w[7]);
-                                }
-                            }
+                            if (RGG_BOUNDS_OK(store_ok(row, col, 16, row_lo, row_hi, N), args.status))
+                                st_global_v8(dst, w);
                         } else if (col + 8 <= N) {
                             if (RGG_BOUNDS_OK(store_ok(row, col, 8, row_lo, row_hi, N), args.status))
                                 st_global_v4(dst, w[0], w[1], w[2], w[3]);

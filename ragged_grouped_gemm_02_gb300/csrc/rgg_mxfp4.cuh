@@ -453,14 +453,13 @@ __device__ __forceinline__ void mxfp4_tiles(const MxMaps& maps, const MxArgs& ar
             }
             tmem_ld_wait();
             if (shares) release();
-            if (!row_ok) continue;
 #pragma unroll
-            for (int i = 0; i < kCols; i += 16) {
+            for (int i = 0; i < kCols; i += 32) {
                 const int col = c.col0 + part * kCols + i;
                 if (col >= N) break;
-                uint32_t w[8];
+                uint32_t w[16];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 16; ++j) {
                     float x[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -473,17 +472,20 @@ __device__ __forceinline__ void mxfp4_tiles(const MxMaps& maps, const MxArgs& ar
                     }
                     w[j] = pack_bf16x2(__float_as_uint(x[0]), __float_as_uint(x[1]));
                 }
-                __nv_bfloat16* dst = args.Y + row * N + col;
-                if (!RGG_BOUNDS_OK(store_ok(row, col, 8, s_off[c.expert], s_off[c.expert + 1], N), args.status)) break;
-                if (col + 16 <= N) {
-                    if (args.y_vec32) {
-                        st_global_v8(dst, w);
-                    } else {
-                        st_global_v4(dst, w[0], w[1], w[2], w[3]);
-                        st_global_v4(dst + 8, w[4], w[5], w[6], w[7]);
-                    }
-                } else {
-                    st_global_v4(dst, w[0], w[1], w[2], w[3]);
+                if (!args.y_vec32) {
+                    store_rows_turned(args.Y, N, row, row_ok, col, N, w, lane, s_off[c.expert], s_off[c.expert + 1],
+                                      args.status);
+                    continue;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // whole 16 columns: N is a multiple of 16
+                    if (!row_ok || col + 16 * h >= N ||
+                        !RGG_BOUNDS_OK(store_ok(row, col + 16 * h, 16, s_off[c.expert], s_off[c.expert + 1], N),
+                                       args.status))
+                        continue;
+                    const uint32_t x[8] = {w[8 * h],     w[8 * h + 1], w[8 * h + 2], w[8 * h + 3],
+                                           w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]};
+                    st_global_v8(args.Y + row * N + col + 16 * h, x);
                 }
             }
         }

@@ -109,8 +109,8 @@ struct WgradShape {
 
 // The tile width and the parts an expert's rows are split into, by the time of
 // the waves with the rows taken as even (us, fitted to this kernel: 0.30 a
-// stage and 0.9 a tile of 256 columns, 0.6 of that for 128), the sums' way
-// through memory and the second launch.  The rows are split where the tiles are
+// stage and 0.9 a tile of 256 columns, 0.6 of that for 128, over an expert's
+// tiles in the mean), the sums' way through memory and the second launch.  The rows are split where the tiles are
 // too few to fill the GPU: one expert of 16,384 rows, K = N = 1024 takes 37 us
 // split and 48 unsplit, of 32,768 rows, K = N = 256, 23 and 76.
 static WgradShape wgrad_shape(int pairs, int E, int64_t M_tot, int K, int N, bool f32, int want_bn, bool may_split) {
@@ -123,7 +123,10 @@ static WgradShape wgrad_shape(int pairs, int E, int64_t M_tot, int K, int N, boo
             const double stages = static_cast<double>(M_tot) / E / kWgradRows / split;
             if (split > 1 && (stages < 4.0 || tiles * split > 2 * pairs)) break;
             const double waves = static_cast<double>((tiles * split + pairs - 1) / pairs);
-            double us = waves * (std::max(1.0, stages) * 0.30 + 0.9) * (bn + 64) / 320.0;
+            // a last tile of up to 128 columns multiplies 128
+            const int whole = N / bn, last = N % bn == 0 ? 0 : N % bn <= 128 ? 128 : bn;
+            const double width = (whole * (bn + 64.0) + (last ? last + 64.0 : 0.0)) / (whole + (last ? 1 : 0)) / 320.0;
+            double us = waves * (std::max(1.0, stages) * 0.30 + 0.9) * width;
             if (split > 1) {
                 const double values = static_cast<double>(E) * K * N;
                 us += 6.0 + values * (8.0 * split + (f32 ? 4.0 : 2.0)) / 4e6;  // parts written and read, at 4 TB/s

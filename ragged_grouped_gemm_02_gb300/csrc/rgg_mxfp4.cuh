@@ -24,9 +24,9 @@
 // TMEM (512 columns): two accumulators of 256 columns and the scales do not fit
 // side by side, so a pair's second accumulator starts at column 192 and shares
 // 64 columns with the first.  The epilogue reads the shared columns first and
-// lets the next tile's MMAs go (acc_empty) once it has them; it has then also
-// finished the tile before, so one barrier orders both hazards.  The scales of
-// a stage take 24 columns, in two sets used in turn.
+// lets the next tile's MMAs go (shared) once it has them, where the accumulator
+// itself has been read as well (acc_empty).  The scales of a stage take 24
+// columns, in two sets used in turn.
 //
 // Measured on a GB300: 32 experts, 32,768 rows, K = 6144, N = 4096 240 us (6 870
 // TFLOP/s), gate-up of the same size 232 us; 16 rows per expert, gate-up, 74 us
@@ -79,8 +79,8 @@ __host__ __device__ inline MxSmem mx_smem(int stages, int E) {
     const uint32_t ex = 4u * static_cast<uint32_t>(E + 1);
     p.b_off = stages * kMxTile;
     p.s_off = 2u * stages * kMxTile;
-    p.bar_off = p.s_off + 3u * stages * kMxScales;  // full[S], empty[S], acc_full[2], acc_empty, drain
-    p.misc_off = p.bar_off + 8u * (2u * stages + 4u);
+    p.bar_off = p.s_off + 3u * stages * kMxScales;  // full[S], empty[S], acc_full[2], acc_empty[2], shared, drain
+    p.misc_off = p.bar_off + 8u * (2u * stages + 6u);
     p.off_off = p.misc_off + 16u;
     p.pre_off = p.off_off + ex;
     p.total = p.pre_off + ex;
@@ -181,8 +181,9 @@ __device__ __forceinline__ void mxfp4_tiles(const MxMaps& maps, const MxArgs& ar
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
     auto accf_bar = [&](int a) { return bars + 8u * (2 * S + a); };
-    const uint32_t acce_bar = bars + 8u * (2 * S + 2);
-    const uint32_t drain_bar = bars + 8u * (2 * S + 3);
+    auto acce_bar = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
+    const uint32_t shared_bar = bars + 8u * (2 * S + 4);
+    const uint32_t drain_bar = bars + 8u * (2 * S + 5);
     uint32_t* misc = reinterpret_cast<uint32_t*>(gbase + sp.misc_off);
     int32_t* s_off = reinterpret_cast<int32_t*>(gbase + sp.off_off);
     int32_t* s_pre = reinterpret_cast<int32_t*>(gbase + sp.pre_off);
@@ -204,9 +205,11 @@ __device__ __forceinline__ void mxfp4_tiles(const MxMaps& maps, const MxArgs& ar
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
-        mbar_init(accf_bar(0), 1);
-        mbar_init(accf_bar(1), 1);
-        mbar_init(acce_bar, (kPair ? 2 : 1) * kMxEpiWarps);
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(accf_bar(a), 1);
+            mbar_init(acce_bar(a), (kPair ? 2 : 1) * kMxEpiWarps / 2);
+        }
+        mbar_init(shared_bar, (kPair ? 2 : 1) * kMxEpiWarps / 2);
         mbar_init(drain_bar, 1);
         misc[1] = 0u;
         fence_mbar_init();
@@ -353,12 +356,11 @@ __device__ __forceinline__ void mxfp4_tiles(const MxMaps& maps, const MxArgs& ar
                 const uint32_t idesc = idesc_mxf4(BM, kPair ? (two ? 256 : 128) : (kGateUp ? 64 : 128));
                 // single CTA, gate-up: the tile's 64 columns are the first or the second half of their blocks
                 const uint32_t sub = (!kPair && kGateUp) ? static_cast<uint32_t>(c.col0 % kMxRows) / 32u : 0u;
-                // the tile before has left the columns that both accumulators
-                // share, and its epilogue warps the one before that
-                if (n > 0 && !wait(acce_bar, (n - 1) & 1u)) {
-                    ok = false;
-                    break;
-                }
+                // the accumulator's last tile has been read, and in a pair the
+                // columns it shares with the tile before
+                if (n >= 2) ok = wait(acce_bar(n & 1), ((n >> 1) - 1) & 1u);
+                if (kPair && ok && n >= 1) ok = wait(shared_bar, (n - 1) & 1u);
+                if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + (n & 1) * kAccStride;
                 uint32_t accumulate = 0;
@@ -410,72 +412,38 @@ __device__ __forceinline__ void mxfp4_tiles(const MxMaps& maps, const MxArgs& ar
         __syncwarp();
     } else {
         // ---------------------------------------------------------- epilogue
+        // Two groups of four warps take the tiles in turn, each with an
+        // accumulator of its own, so that one group's waits run under the
+        // other's stores.
         const int q = warp & 3;
-        const int part = (warp - 2) >> 2;  // half of the tile's output columns
-        const uint32_t acce_leader = kPair ? map_to_rank(acce_bar, 0) : acce_bar;
-        int32_t n = 0;
-        for (int32_t t = unit; t < T; t += units, ++n) {
+        const int acc = (warp - 2) >> 2;
+        const uint32_t acc_col = acc * kAccStride;
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc_col;
+        auto arrive = [&](uint32_t bar) {  // the warp's loads from TMEM are done
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (kPair) mbar_arrive_cluster(map_to_rank(bar, 0));
+                else mbar_arrive(bar);
+            }
+        };
+        auto load = [&](int cc, uint32_t* v) {  // 32 columns of the accumulator
+            if (RGG_BOUNDS_OK(tmem_cols_ok(acc_col + cc, 32, kMxSfCol), args.status))
+                tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(cc), *reinterpret_cast<uint32_t(*)[32]>(v));
+        };
+        for (int32_t t = unit + acc * units, n = acc; t < T; t += 2 * units, n += 2) {
             const TileCoord c = tile_at(t);
-            if (!wait(accf_bar(n & 1), (n >> 1) & 1u)) break;
+            if (!wait(accf_bar(acc), (n >> 1) & 1u)) break;
             tc_fence_after_sync();
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (n & 1) * kAccStride;
             const int r_local = 128 * static_cast<int>(rank) + 32 * q + lane;
             const bool row_ok = r_local < c.rows;
             const int64_t row = static_cast<int64_t>(c.row0) + r_local;
-            // Everything the warp writes is taken from TMEM before any of it
-            // is stored: in a pair the next tile's MMAs wait for the columns
-            // that the accumulators share (in the first, the second half's;
-            // in the second, the first half's; the other half's warps let go
-            // at once, having finished the tile before).
-            constexpr int kCols = kOutN / 2;
-            uint32_t v[kCols], u[kGateUp ? kCols : 1];
-            auto release = [&]() {
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (kPair) mbar_arrive_cluster(acce_leader);
-                    else mbar_arrive(acce_leader);
-                }
-            };
-            const bool shares = kPair && part == ((n & 1) == 0 ? 1 : 0);
-            if (!shares) release();
-#pragma unroll
-            for (int i = 0; i < kCols; i += 32) {
-                const int cc = part * kCols + i;
-                if (c.col0 + cc >= N) break;  // columns past N are not computed
-                if (!RGG_BOUNDS_OK(tmem_cols_ok((n & 1) * kAccStride + (kGateUp ? kOutN : 0) + cc, 32, kMxSfCol),
-                                   args.status))
-                    break;
-                tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(cc), *reinterpret_cast<uint32_t(*)[32]>(&v[i]));
-                if constexpr (kGateUp)
-                    tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(kOutN + cc),
-                                       *reinterpret_cast<uint32_t(*)[32]>(&u[i]));
-            }
-            tmem_ld_wait();
-            if (shares) release();
-#pragma unroll
-            for (int i = 0; i < kCols; i += 32) {
-                const int col = c.col0 + part * kCols + i;
-                if (col >= N) break;
-                uint32_t w[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float x[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        x[h] = __uint_as_float(v[i + 2 * j + h]);
-                        // silu by the approximate division (2 ulp; 0 where the denominator passes
-                        // 2^126): with the exact one the epilogue outlasted the tile's MMAs (408 us
-                        // against 228 on 32 experts x 1,024 rows, K = 6144, N = 2048)
-                        if constexpr (kGateUp)
-                            x[h] = __fdividef(x[h], 1.0f + __expf(-x[h])) * __uint_as_float(u[i + 2 * j + h]);
-                    }
-                    w[j] = pack_bf16x2(__float_as_uint(x[0]), __float_as_uint(x[1]));
-                }
+            auto store = [&](int cc, const uint32_t (&w)[16]) {  // output columns cc .. cc + 31 of the tile
+                const int col = c.col0 + cc;
                 if (!args.y_vec32) {
                     store_rows_turned(args.Y, N, row, row_ok, col, N, w, lane, s_off[c.expert], s_off[c.expert + 1],
                                       args.status);
-                    continue;
+                    return;
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {  // whole 16 columns: N is a multiple of 16
@@ -486,6 +454,78 @@ __device__ __forceinline__ void mxfp4_tiles(const MxMaps& maps, const MxArgs& ar
                     const uint32_t x[8] = {w[8 * h],     w[8 * h + 1], w[8 * h + 2], w[8 * h + 3],
                                            w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]};
                     st_global_v8(args.Y + row * N + col + 16 * h, x);
+                }
+            };
+            // 64 columns at a time, from the side that the accumulators of a
+            // pair share: the first's last 64 columns, the second's first.
+            constexpr int kChunks = kOutN / 64;
+            auto chunk = [&](int j) { return acc == 0 ? kChunks - 1 - j : j; };
+            if constexpr (!kGateUp) {
+                uint32_t v[64];
+                auto load_chunk = [&](int j) {
+                    const int cc = 64 * chunk(j);
+                    if (c.col0 + cc >= N) return;  // columns past N are not computed
+                    load(cc, v);
+                    load(cc + 32, v + 32);
+                };
+                load_chunk(0);
+#pragma unroll
+                for (int j = 0; j < kChunks; ++j) {
+                    tmem_ld_wait();
+                    if (kPair && j == 0) arrive(shared_bar);
+                    uint32_t w[2][16];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        asm volatile("" : "+r"(v[2 * i]), "+r"(v[2 * i + 1]));  // not before the wait
+                        w[i / 16][i % 16] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+                    }
+                    if (j + 1 < kChunks) load_chunk(j + 1);
+                    else arrive(acce_bar(acc));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (c.col0 + 64 * chunk(j) + 32 * h < N) store(64 * chunk(j) + 32 * h, w[h]);
+                }
+            } else {
+                // all 64 of the half (up or gate) with the shared columns, 32 at a time of the other
+                uint32_t held[64], other[32];
+                const int held_at = acc == 0 ? kOutN : 0, other_at = kOutN - held_at;
+                load(held_at + 64 * chunk(0), held);
+                load(held_at + 64 * chunk(0) + 32, held + 32);
+                load(other_at + 64 * chunk(0), other);
+#pragma unroll
+                for (int j = 0; j < kChunks; ++j) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tmem_ld_wait();
+                        if (kPair && j == 0 && h == 0) arrive(shared_bar);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float x[2];
+#pragma unroll
+                            for (int p = 0; p < 2; ++p) {
+                                asm volatile("" : "+r"(held[32 * h + 2 * i + p]), "+r"(other[2 * i + p]));
+                                const float a = __uint_as_float(held[32 * h + 2 * i + p]);
+                                const float b = __uint_as_float(other[2 * i + p]);
+                                const float g = acc == 0 ? b : a, up = acc == 0 ? a : b;
+                                // silu by the approximate division (2 ulp; 0 where the denominator passes
+                                // 2^126): with the exact one the epilogue outlasted the tile's MMAs (408 us
+                                // against 228 on 32 experts x 1,024 rows, K = 6144, N = 2048)
+                                x[p] = __fdividef(g, 1.0f + __expf(-g)) * up;
+                            }
+                            w[i] = pack_bf16x2(__float_as_uint(x[0]), __float_as_uint(x[1]));
+                        }
+                        if (h == 0) {
+                            load(other_at + 64 * chunk(j) + 32, other);
+                        } else if (j + 1 < kChunks) {
+                            load(held_at + 64 * chunk(j + 1), held);
+                            load(held_at + 64 * chunk(j + 1) + 32, held + 32);
+                            load(other_at + 64 * chunk(j + 1), other);
+                        } else {
+                            arrive(acce_bar(acc));
+                        }
+                        store(64 * chunk(j) + 32 * h, w);
+                    }
                 }
             }
         }

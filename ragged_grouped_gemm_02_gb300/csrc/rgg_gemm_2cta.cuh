@@ -20,9 +20,10 @@
 //                   barriers of both CTAs with one commit.
 //   (both run in step, one lane issuing: rgg_warp_issue.cuh)
 //   warps 2-5     : epilogue of the CTA's own 128 rows (warps 2-9, two per
-//   (or 2-9)        TMEM lane quadrant, for the fused gate-up epilogue);
-//                   they arrive on the leader's acc_empty (one arrival per
-//                   epilogue warp of both CTAs).
+//   (or 2-9)        TMEM lane quadrant, for the fused gate-up epilogue, or two
+//                   groups that take the tiles in turn, for the transposed
+//                   product); they arrive on the leader's acc_empty (one arrival per
+//                   epilogue warp of both CTAs that read the tile).
 // All waits are bounded; an abort raised in either CTA is mirrored into the
 // other CTA's flag so the pair leaves its loops together.
 #pragma once
@@ -568,13 +569,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * pair_epilo
 #pragma unroll
                         for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[16 * h + 2 * i], v[16 * h + 2 * i + 1]);
                         __nv_bfloat16* dst = yrow + cc + 16 * h;
-                        if (col + 16 <= N) {
-                            if (RGG_BOUNDS_OK(store_ok(row, col, 16, row_lo, row_hi, N), args.status))
-                                st_global_v8(dst, w);
-                        } else if (col + 8 <= N) {
-                            if (RGG_BOUNDS_OK(store_ok(row, col, 8, row_lo, row_hi, N), args.status))
-                                st_global_v4(dst, w[0], w[1], w[2], w[3]);
-                        }
+                        // N is a multiple of 16 here
+                        if (col < N && RGG_BOUNDS_OK(store_ok(row, col, 16, row_lo, row_hi, N), args.status))
+                            st_global_v8(dst, w);
                     }
                 }
             }

@@ -3,7 +3,9 @@
 // forward product.  What bounds it is what bounds the forward product: the
 // same bytes per stage, MMAs and epilogue.  32 experts, 32,768 rows, K = 6144,
 // N = 4096: 922 us from a pause (1 788 TFLOP/s), 1 092 us in a row at the power
-// cap; the forward product of the same size 916.
+// cap; the forward product of the same size 916.  Few reduction stages are bound
+// by the stores (epilogue_groups), few tiles by the weights each SM streams,
+// which the narrowest tiles make least (few_tiles_options).
 #include "rgg_gemm_launch.cuh"
 
 namespace rgg {

@@ -5,6 +5,7 @@
 // K = 6144, N = 2048: 945 us, 1 746 TFLOP/s), by bytes at few: 64 experts x 256
 // rows, K = 1024, N = 1344 takes 99 us at 5.7 TB/s (134 us while dH was read
 // after the accumulators were ready and outputs went out 16 bytes at a time).
+// Few tiles are 64 x 128, as for the gradient by the activations.
 #include "rgg_gemm_launch.cuh"
 
 namespace rgg {

@@ -349,9 +349,7 @@ __device__ __forceinline__ void store_swiglu_backward(const GemmArgs& args, int6
                                                       int32_t row_hi) {
     const int N = args.N;
     const int64_t pitch = 2 * static_cast<int64_t>(N);
-    uint32_t wg[16], wu[16], wh[16];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    auto compute = [&](int h, uint32_t* wg, uint32_t* wu, uint32_t* wh) {  // columns 16 h to 16 h + 15
         const uint4 d0 = second ? grad.d[4 + 2 * h] : grad.d[2 * h];
         const uint4 d1 = second ? grad.d[5 + 2 * h] : grad.d[2 * h + 1];
         const uint32_t dw[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
@@ -369,30 +367,29 @@ __device__ __forceinline__ void store_swiglu_backward(const GemmArgs& args, int6
                 du[j] = d * gs;
                 dg[j] = d * up * s * (1.0f + (g - gs));
             }
-            wg[8 * h + i] = pack_bf16x2(__float_as_uint(dg[0]), __float_as_uint(dg[1]));
-            wu[8 * h + i] = pack_bf16x2(__float_as_uint(du[0]), __float_as_uint(du[1]));
-            wh[8 * h + i] = pack_bf16x2(__float_as_uint(hh[0]), __float_as_uint(hh[1]));
+            wg[i] = pack_bf16x2(__float_as_uint(dg[0]), __float_as_uint(dg[1]));
+            wu[i] = pack_bf16x2(__float_as_uint(du[0]), __float_as_uint(du[1]));
+            wh[i] = pack_bf16x2(__float_as_uint(hh[0]), __float_as_uint(hh[1]));
         }
-    }
+    };
     if (!args.y_vec32) {
+        uint32_t wg[16], wu[16], wh[16];
+        compute(0, wg, wu, wh);
+        compute(1, wg + 8, wu + 8, wh + 8);
         store_rows_turned(args.Y, pitch, row, row_ok, col, N, wg, lane, row_lo, row_hi, args.status);
         store_rows_turned(args.Y + N, pitch, row, row_ok, col, N, wu, lane, row_lo, row_hi, args.status);
         if (args.act) store_rows_turned(args.act, N, row, row_ok, col, N, wh, lane, row_lo, row_hi, args.status);
         return;
     }
-    // whole 16 columns: N is a multiple of 16
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int c = col + 16 * h;
+        const int c = col + 16 * h;  // N is a multiple of 16 here
         if (!row_ok || c >= N || !RGG_BOUNDS_OK(store_ok(row, c, 16, row_lo, row_hi, N), args.status)) continue;
-        auto store = [&](__nv_bfloat16* p, const uint32_t (&w)[16]) {
-            const uint32_t x[8] = {w[8 * h],     w[8 * h + 1], w[8 * h + 2], w[8 * h + 3],
-                                   w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]};
-            st_global_v8(p, x);
-        };
-        store(args.Y + row * pitch + c, wg);
-        store(args.Y + row * pitch + N + c, wu);
-        if (args.act) store(args.act + row * N + c, wh);
+        uint32_t wg[8], wu[8], wh[8];
+        compute(h, wg, wu, wh);
+        st_global_v8(args.Y + row * pitch + c, wg);
+        st_global_v8(args.Y + row * pitch + N + c, wu);
+        if (args.act) st_global_v8(args.act + row * N + c, wh);
     }
 }
 

@@ -167,18 +167,21 @@ typedef struct rgg_plan_info {
 /*
  * Create a handle bound to CUDA device `device`: queries the SM count and the
  * shared-memory limit, checks for compute capability 10.3 (sm_103), and
- * allocates the handle's 256-byte device word, zeroed (once per handle; no
- * call allocates device memory after this).  Its first int32 is the status
- * word; three int32 at byte 64 are the mixed launch's tile counters, which
- * each mixed launch leaves at zero again when its last CTA ends.  On success
- * *out owns the handle; release it with rgg_destroy.  Returns
- * RGG_ERR_UNSUPPORTED on any other GPU.
+ * allocates the handle's device memory, zeroed (once per handle; no call
+ * allocates device memory after this): the status word, and 4096 sets of tile
+ * counters for mixed launches with claims, which each such launch leaves at
+ * zero again when its last CTA ends.  On success *out owns the handle; release
+ * it with rgg_destroy.  Returns RGG_ERR_UNSUPPORTED on any other GPU.
  *
- * Concurrency: calls on one handle may run on any streams, but they share the
- * handle's status word (rgg_query_status returns the first error any of them
- * recorded); mixed launches (rgg_options.mixed) on one handle must not overlap
- * on the GPU, since they share the tile counters: order them on one stream.
- * Use a handle from several host threads only under the caller's own lock.
+ * Concurrency: calls on one handle may run on any streams, captured in graphs
+ * or not, and come from several host threads.  They share the handle's status
+ * word (rgg_query_status returns the first error any of them recorded).  A
+ * mixed launch with claims takes the set of counters of its stream, or of its
+ * stream in its capture, so launches that overlap on the GPU never share one;
+ * the handle keeps a set for each stream and each capture that it has seen,
+ * and once all are taken further ones run the mixed launch without claims
+ * (same results).  A stream that takes part in a capture must live until the
+ * capture ends, and two instances of one graph must not run side by side.
  */
 rgg_status rgg_create(rgg_handle** out, int device);
 

@@ -14,9 +14,11 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <string>
 
 #include "rgg.h"
+#include "rgg_counters.h"
 #include "rgg_host.h"
 #include "rgg_internal.h"
 
@@ -24,10 +26,13 @@ struct rgg_handle {
     int device;
     int num_sms;
     int smem_optin;
-    int32_t* d_status;
+    int32_t* d_status;    // the status word; the counter sets follow it at kCountersAt
+    rgg::CounterSets sets;
 };
 
 namespace {
+
+constexpr size_t kCountersAt = 256;  // bytes after the status word
 
 thread_local std::string g_last_cuda_error;
 
@@ -565,6 +570,42 @@ rgg_status swiglu_call(rgg_handle* h, const void* X, const void* W13, const int3
                        void* out, void* act, int E, int64_t M_tot, int K, int N, void* stream, const rgg_options* opt,
                        bool backward);
 
+// The tile counters of a launch with claims on `stream`: the set that the handle
+// keeps for the stream, or null where it has none left or the stream's state
+// cannot be read (the launch itself then reports what is wrong).
+int32_t* claim_counters(rgg_handle* h, cudaStream_t stream) {
+    unsigned long long id = 0, capture = 0;
+    cudaStreamCaptureStatus state = cudaStreamCaptureStatusNone;
+    if (cudaStreamGetCaptureInfo(stream, &state, &capture) != cudaSuccess) return nullptr;
+    if (state == cudaStreamCaptureStatusNone) {
+        if (cudaStreamGetId(stream, &id) != cudaSuccess) return nullptr;
+        capture = 0;
+    } else {
+        id = reinterpret_cast<uintptr_t>(stream);  // cudaStreamGetId would end the capture
+    }
+    const int set = h->sets.set_of(id, capture);
+    return set < 0 ? nullptr : h->d_status + kCountersAt / 4 + set * rgg::kCounterSetWords;
+}
+
+// The mixed launch's arguments.  Without counters it runs without claims: each
+// kernel then walks its own class, on the SMs that the plan gives it.
+void set_mixed_args(const Plan& p, int32_t* counters, rgg::GemmArgs* a) {
+    a->sched = counters;
+    a->sched_total = p.grid + p.single_grid;
+    a->sched_pairs = p.grid / 2;
+    a->sched_singles = p.single_grid;
+    a->sched_claims = (p.mixed == 1 && counters) ? 1 : 0;
+    a->pair_min_rows = p.pair_min_rows;
+    a->sched_split = p.device_split;
+    a->split_sms = p.split_sms;
+}
+
+// After a mixed launch that failed: a kernel that did launch still counts its
+// CTAs, so the counters are zeroed behind it.
+void clear_counters(const rgg::GemmArgs& a, cudaStream_t stream) {
+    if (a.sched_claims) cudaMemsetAsync(a.sched, 0, 3 * sizeof(int32_t), stream);
+}
+
 }  // namespace
 
 namespace rgg {
@@ -685,7 +726,7 @@ static const rgg_options* few_tiles_options(int num_sms, int E, int64_t M_tot, i
 
 rgg_status host_grouped_gemm(int num_sms, int smem_optin, int32_t* status, const void* X, const void* W,
                              const int32_t* group_offsets, void* Y, int E, int64_t M_tot, int K, int N,
-                             cudaStream_t st, const rgg_options* opt, bool trans_w) {
+                             cudaStream_t st, const rgg_options* opt, rgg_handle* h, bool trans_w) {
     if (M_tot == 0) {
         cudaError_t err = launch_validate_offsets(group_offsets, E, M_tot, status, st);
         return err == cudaSuccess ? RGG_OK : cuda_failure(err, "validate_offsets launch");
@@ -715,23 +756,15 @@ rgg_status host_grouped_gemm(int num_sms, int smem_optin, int32_t* status, const
     a.tail64 = p.tail64;
     a.walk_order = p.walk_order;
     if (p.mixed) {
-        // the claim counters and the count of finished CTAs sit 64 bytes after the status word; they
-        // start at zero and the launch's last CTA sets them back to zero
-        a.sched = status + 16;
-        a.sched_total = p.grid + p.single_grid;
-        a.sched_pairs = p.grid / 2;
-        a.sched_singles = p.single_grid;
-        a.sched_claims = (p.mixed == 1) ? 1 : 0;
-        a.pair_min_rows = p.pair_min_rows;
-        a.sched_split = p.device_split;
-        a.split_sms = p.split_sms;
+        // the claim counters and the count of finished CTAs start at zero and the launch's last CTA sets
+        // them back to zero; without a handle they sit 64 bytes after the status word
+        set_mixed_args(p, p.mixed != 1 ? nullptr : h ? claim_counters(h, st) : status + 16, &a);
         GemmArgs as = a;
         as.stages = p.single_stages;
         auto launch = trans_w ? launch_gemm_mixed_dgrad : launch_gemm_mixed;
         cudaError_t err = launch(p.grid, p.smem_bytes, a, p.single_grid, p.single_smem, as, st, tx, tx64, tw);
         if (err != cudaSuccess) {
-            // a kernel that did launch still counts its CTAs: zero the counters behind it
-            cudaMemsetAsync(a.sched, 0, 3 * sizeof(int32_t), st);
+            clear_counters(a, st);
             return cuda_failure(err, "grouped_gemm (mixed) launch");
         }
         return RGG_OK;
@@ -785,13 +818,20 @@ rgg_status rgg_create(rgg_handle** out, int device) {
     }
     DeviceScope scope(device);
     if (scope.error() != cudaSuccess) return cuda_failure(scope.error(), "cudaSetDevice");
-    int32_t* status = nullptr;
-    if ((err = cudaMalloc(&status, 256)) != cudaSuccess) return cuda_failure(err, "cudaMalloc(status)");
-    if ((err = cudaMemset(status, 0, 256)) != cudaSuccess) {
-        cudaFree(status);
-        return cuda_failure(err, "cudaMemset(status)");
+    rgg_handle* h = new (std::nothrow) rgg_handle;
+    if (!h) {
+        g_last_cuda_error = "rgg_create: out of host memory";
+        return RGG_ERR_CUDA;
     }
-    rgg_handle* h = new rgg_handle;
+    constexpr size_t bytes = kCountersAt + sizeof(int32_t) * rgg::kCounterSets * rgg::kCounterSetWords;
+    int32_t* status = nullptr;
+    err = cudaMalloc(&status, bytes);
+    if (err == cudaSuccess) err = cudaMemset(status, 0, bytes);
+    if (err != cudaSuccess) {
+        if (status) cudaFree(status);
+        delete h;
+        return cuda_failure(err, "rgg_create: status word and counters");
+    }
     h->device = device;
     h->num_sms = sms;
     h->smem_optin = smem;
@@ -868,7 +908,7 @@ rgg_status rgg_grouped_gemm(rgg_handle* h, const void* X, const void* W, const i
     DeviceScope scope(h->device);
     if (scope.error() != cudaSuccess) return cuda_failure(scope.error(), "cudaSetDevice");
     return rgg::host_grouped_gemm(h->num_sms, h->smem_optin, h->d_status, X, W, group_offsets, Y, E, M_tot, K, N,
-                                  static_cast<cudaStream_t>(stream), opt);
+                                  static_cast<cudaStream_t>(stream), opt, h);
 }
 
 rgg_status rgg_grouped_gemm_dgrad(rgg_handle* h, const void* dY, const void* W, const int32_t* group_offsets, void* dX,
@@ -880,7 +920,7 @@ rgg_status rgg_grouped_gemm_dgrad(rgg_handle* h, const void* dY, const void* W, 
     DeviceScope scope(h->device);
     if (scope.error() != cudaSuccess) return cuda_failure(scope.error(), "cudaSetDevice");
     return rgg::host_grouped_gemm(h->num_sms, h->smem_optin, h->d_status, dY, W, group_offsets, dX, E, M_tot, N, K,
-                                  static_cast<cudaStream_t>(stream), opt, true);
+                                  static_cast<cudaStream_t>(stream), opt, h, true);
 }
 
 rgg_status rgg_grouped_gemm_swiglu(rgg_handle* h, const void* X, const void* W13, const int32_t* group_offsets,
@@ -1113,20 +1153,13 @@ rgg_status swiglu_call(rgg_handle* h, const void* X, const void* W13, const int3
     a.walk_order = p.walk_order;
     if (p.mixed) {
         // as for rgg_grouped_gemm's mixed launch
-        a.sched = h->d_status + 16;
-        a.sched_total = p.grid + p.single_grid;
-        a.sched_pairs = p.grid / 2;
-        a.sched_singles = p.single_grid;
-        a.sched_claims = (p.mixed == 1) ? 1 : 0;
-        a.pair_min_rows = p.pair_min_rows;
-        a.sched_split = p.device_split;
-        a.split_sms = p.split_sms;
+        set_mixed_args(p, p.mixed == 1 ? claim_counters(h, st) : nullptr, &a);
         rgg::GemmArgs as = a;
         as.stages = p.single_stages;
         auto launch = backward ? rgg::launch_gemm_mixed_swiglu_bwd : rgg::launch_gemm_mixed_swiglu;
         cudaError_t err = launch(p.grid, p.smem_bytes, a, p.single_grid, p.single_smem, as, st, tx, tx64, tw);
         if (err != cudaSuccess) {
-            cudaMemsetAsync(a.sched, 0, 3 * sizeof(int32_t), st);
+            clear_counters(a, st);
             return cuda_failure(err, "grouped_gemm_swiglu (mixed) launch");
         }
         return RGG_OK;

@@ -130,11 +130,14 @@ rgg_status host_check_gemm_args(const void* X, const void* W, const int32_t* gro
 // Plan, encode and launch rgg_grouped_gemm on the current device for a GPU of
 // `num_sms` SMs and `smem_optin` bytes of shared memory per block, recording
 // device-detected errors in the device word `status`.  Arguments already
-// checked by host_check_gemm_args.  `trans_w`: Y_e = X_e . W_e^T with W
-// [E, N, K] (rgg_grouped_gemm_dgrad).
+// checked by host_check_gemm_args.  `h`: whose tile counters a launch with
+// claims takes; without one they are three int32 64 bytes after `status`, and
+// calls must not overlap.  `trans_w`: Y_e = X_e . W_e^T with W [E, N, K]
+// (rgg_grouped_gemm_dgrad).
 rgg_status host_grouped_gemm(int num_sms, int smem_optin, int32_t* status, const void* X, const void* W,
                              const int32_t* group_offsets, void* Y, int E, int64_t M_tot, int K, int N,
-                             cudaStream_t stream, const rgg_options* opt, bool trans_w = false);
+                             cudaStream_t stream, const rgg_options* opt, rgg_handle* h = nullptr,
+                             bool trans_w = false);
 
 // Offsets check alone (used when there are no rows to multiply).
 cudaError_t launch_validate_offsets(const int32_t* offsets, int E, int64_t M_tot, int32_t* status,

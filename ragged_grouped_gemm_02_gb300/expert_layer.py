@@ -8,6 +8,7 @@ inputs: ``rgg_grouped_gemm_swiglu_backward`` computes gate and up again.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (rgg_grouped_gemm, rgg_grouped_gemm_dgrad, rgg_grouped_gemm_mxfp4, rgg_grouped_gemm_swiglu,
                rgg_grouped_gemm_swiglu_backward, rgg_grouped_gemm_swiglu_mxfp4, rgg_grouped_gemm_wgrad,
@@ -25,6 +26,7 @@ class _ExpertFFN(torch.autograd.Function):
         return rgg_grouped_gemm(H, W2, group_offsets, Y)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, W13, W2, group_offsets = ctx.saved_tensors
         dY = dY.contiguous()
@@ -42,7 +44,8 @@ class _ExpertFFN(torch.autograd.Function):
 
 
 def expert_ffn(X, W13, W2, group_offsets):
-    """Y for routed rows X, with gradients by X, W13 and W2.
+    """Y for routed rows X, with gradients by X, W13 and W2 (first derivatives: the
+    gradients cannot be differentiated again, and autograd raises if asked to).
 
     X: bf16 CUDA [M_tot, K], rows grouped by expert; W13: bf16 CUDA [E, K, 2N]
     (gate columns first); W2: bf16 CUDA [E, N, K_out]; group_offsets: int32

@@ -452,8 +452,10 @@ rgg_status rgg_grouped_gemm_swiglu_backward(rgg_handle* h, const void* X, const 
  * at least rgg_grouped_gemm_wgrad_workspace bytes, not shared by calls that may
  * overlap) products with few tiles and many rows split each expert's rows into
  * parts whose fp32 sums a second launch adds in order; without one they run
- * unsplit.  That function returns 0 where a split would not pay.  M_tot may be 0.  Sizes, alignment, errors and the stream
- * contract as for rgg_grouped_gemm; invalid offsets write nothing.
+ * unsplit.  That size is enough whatever the other options are: a call splits
+ * into no more parts than fit.  The function returns 0 where a split would not
+ * pay.  M_tot may be 0.  Sizes, alignment, errors and the stream contract as
+ * for rgg_grouped_gemm; invalid offsets write nothing.
  */
 #define RGG_WGRAD_FP32 1
 #define RGG_WGRAD_ACCUMULATE 2

@@ -107,21 +107,28 @@ struct WgradShape {
     int bn, split;
 };
 
+// What the parts' sums take; for a split that wgrad_shape considers at most two tiles of 256 KB a pair.
+static int64_t wgrad_parts_bytes(int split, int E, int K, int N) { return static_cast<int64_t>(split) * E * K * N * 4; }
+
+constexpr int64_t kAnyRoom = INT64_MAX;
+
 // The tile width and the parts an expert's rows are split into, by the time of
 // the waves with the rows taken as even (us, fitted to this kernel: 0.30 a
 // stage and 0.9 a tile of 256 columns, 0.6 of that for 128, over an expert's
 // tiles in the mean), the sums' way through memory and the second launch.  The rows are split where the tiles are
 // too few to fill the GPU: one expert of 16,384 rows, K = N = 1024 takes 37 us
-// split and 48 unsplit, of 32,768 rows, K = N = 256, 23 and 76.
-static WgradShape wgrad_shape(int pairs, int E, int64_t M_tot, int K, int N, bool f32, int want_bn, bool may_split) {
+// split and 48 unsplit, of 32,768 rows, K = N = 256, 23 and 76.  The parts take
+// `room` bytes at most.
+static WgradShape wgrad_shape(int pairs, int E, int64_t M_tot, int K, int N, bool f32, int want_bn, int64_t room) {
     WgradShape best = {want_bn ? want_bn : 256, 1};
     double least = 1e300;
     for (int bn : {256, 128}) {
         if (want_bn != 0 && bn != want_bn) continue;
         const int64_t tiles = static_cast<int64_t>(E) * ((K + kWgradBM - 1) / kWgradBM) * ((N + bn - 1) / bn);
-        for (int split = 1; split <= (may_split ? 32 : 1); split *= 2) {
+        for (int split = 1; split <= 32; split *= 2) {
             const double stages = static_cast<double>(M_tot) / E / kWgradRows / split;
-            if (split > 1 && (stages < 4.0 || tiles * split > 2 * pairs)) break;
+            if (split > 1 && (stages < 4.0 || tiles * split > 2 * pairs || wgrad_parts_bytes(split, E, K, N) > room))
+                break;
             const double waves = static_cast<double>((tiles * split + pairs - 1) / pairs);
             // a last tile of up to 128 columns multiplies 128
             const int whole = N / bn, last = N % bn == 0 ? 0 : N % bn <= 128 ? 128 : bn;
@@ -167,12 +174,17 @@ extern "C" rgg_status rgg_grouped_gemm_wgrad(rgg_handle* h, const void* X, const
     auto tiles = [&](int bn) {
         return static_cast<int64_t>(E) * ((K + kWgradBM - 1) / kWgradBM) * ((N + bn - 1) / bn);
     };
-    const WgradShape shape = wgrad_shape(pairs, E, M_tot, K, N, (flags & RGG_WGRAD_FP32) != 0, want_bn,
-                                         opt && opt->workspace);
+    // A workspace of the size that the query gives is enough whatever the
+    // options are: the rows are split into as many parts as fit it.
+    const bool f32 = (flags & RGG_WGRAD_FP32) != 0;
+    const int64_t room_bytes = opt && opt->workspace ? opt->workspace_bytes : 0;
+    const WgradShape shape = wgrad_shape(pairs, E, M_tot, K, N, f32, want_bn, room_bytes);
     const int bn = shape.bn, split = shape.split;
-    if (split > 1 && (opt->workspace_bytes < static_cast<int64_t>(split) * E * K * N * 4 ||
-                      !host_aligned(opt->workspace, 16)))
-        return RGG_ERR_INVALID_ARG;
+    if (split > 1 && !host_aligned(opt->workspace, 16)) return RGG_ERR_INVALID_ARG;
+    if (opt && opt->workspace && room_bytes < rgg_grouped_gemm_wgrad_workspace(h, E, M_tot, K, N, flags)) {
+        const int wanted = wgrad_shape(pairs, E, M_tot, K, N, f32, want_bn, kAnyRoom).split;
+        if (wanted > 1 && room_bytes < wgrad_parts_bytes(wanted, E, K, N)) return RGG_ERR_INVALID_ARG;
+    }
     // where the tiles' sums go: dW, or each part's place in the workspace
     void* out = split > 1 ? opt->workspace : dW;
     const int out_flags = split > 1 ? RGG_WGRAD_FP32 : flags;
@@ -229,6 +241,6 @@ extern "C" rgg_status rgg_grouped_gemm_wgrad(rgg_handle* h, const void* X, const
 extern "C" int64_t rgg_grouped_gemm_wgrad_workspace(rgg_handle* h, int E, int64_t M_tot, int K, int N, int flags) {
     if (!h || host_check_sizes(E, M_tot, K, N) != RGG_OK) return 0;
     const WgradShape shape = wgrad_shape(std::max(1, host_device(h).num_sms / 2), E, M_tot, K, N,
-                                         (flags & RGG_WGRAD_FP32) != 0, 0, true);
-    return shape.split > 1 ? static_cast<int64_t>(shape.split) * E * K * N * 4 : 0;
+                                         (flags & RGG_WGRAD_FP32) != 0, 0, kAnyRoom);
+    return shape.split > 1 ? wgrad_parts_bytes(shape.split, E, K, N) : 0;
 }

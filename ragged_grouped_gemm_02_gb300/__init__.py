@@ -559,12 +559,13 @@ def rgg_grouped_gemm_wgrad(X, dY, group_offsets, dW=None, *, dtype=None, accumul
     opt = workspace = None
     if bn or stages or max_ctas or timeout_ns or debug_flags:
         opt, _ = _options(0, bn, stages, max_ctas, timeout_ns, None, debug_flags)
-    elif M_tot >= 512 * E and E * -(-K // 256) * -(-N // 256) <= 128:
+    if M_tot >= 512 * E and E * -(-K // 256) * -(-N // 256) <= 128:
         # few tiles with many rows: the library may want to split the rows
         bytes_ = load_library().rgg_grouped_gemm_wgrad_workspace(_handle(device), E, M_tot, K, N, flags)
         if bytes_ > 0:
             workspace = _empty((bytes_ // 4,), torch.float32, dev, stream)
-            opt, _ = _options()
+            if opt is None:
+                opt, _ = _options()
             _set_workspace(opt, workspace)
     st = _raw_stream(stream, device)
     s = load_library().rgg_grouped_gemm_wgrad(_handle(device), X.data_ptr(), dY.data_ptr(), group_offsets.data_ptr(),

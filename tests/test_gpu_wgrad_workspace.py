@@ -1,5 +1,5 @@
 """rgg_grouped_gemm_wgrad's workspace on a GB300: the queried size is enough for every option, no call writes past the
-workspace.  Sums: as in test_gpu_wgrad.py."""
+workspace, and options do not keep the Python function from splitting the rows.  Sums: as in test_gpu_wgrad.py."""
 import numpy as np
 import pytest
 import torch
@@ -51,3 +51,13 @@ def test_the_queried_size_is_enough(counts, K, N, flags):
         assert rgg.rgg_query_status(0) == rgg.RGG_OK
         refs.assert_close(dW, ref, limit, "dW with %s" % opts)
         assert bool((space[need:] == 0x5A).all()), opts
+
+
+def test_options_keep_the_split():
+    # the order of the sums depends on the sizes alone: an option that changes none of it changes no bit
+    X, dY, off = _case([4096], 136, 264, seed=1)
+    args = X.cuda(), dY.cuda(), torch.from_numpy(off).cuda()
+    assert rgg.load_library().rgg_grouped_gemm_wgrad_workspace(rgg._handle(0), 1, 4096, 136, 264, 1) > 0
+    want = rgg.rgg_grouped_gemm_wgrad(*args, dtype=torch.float32, check=True)
+    got = rgg.rgg_grouped_gemm_wgrad(*args, dtype=torch.float32, timeout_ns=1_000_000_000, check=True)
+    assert torch.equal(got, want)

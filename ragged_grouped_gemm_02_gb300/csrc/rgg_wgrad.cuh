@@ -45,6 +45,7 @@
 #pragma once
 
 #include "rgg_gemm_2cta.cuh"
+#include "rgg_wgrad_parts.h"
 
 namespace rgg {
 
@@ -67,7 +68,6 @@ struct WgradArgs {
 };
 
 constexpr int kWgradBM = 256;        // K columns per pair tile
-constexpr int kWgradRows = 64;       // rows (reduction) per stage
 constexpr int kWgradEpiWarps = 8;
 constexpr int kWgradTailWarp = 2 + kWgradEpiWarps;  // the first of them
 constexpr int kWgradTailWarps = 2;
@@ -227,8 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     // The tile a pair takes in pass i: the list of all experts' tiles, one per
     // pair and pass.  (Over experts sorted by size, large and small ones in
     // turn, it measured 1-5 % slower on even and skewed routings alike.)
-    // With `split` parts, part s of expert e counts as expert e * split + s: an
-    // equal share of e's rows, rounded up to whole stages.
+    // With `split` parts, part s of expert e counts as expert e * split + s.
     struct Tile {
         int32_t expert, row0, rows, k0, n0;  // expert -1: no more tiles
     };
@@ -244,11 +243,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
             t.rows = s_off[t.expert + 1] - t.row0;
         } else {
             const int32_t e = t.expert / args.split, part = t.expert - e * args.split;
-            const int32_t m = s_off[e + 1] - s_off[e];
-            const int32_t share = ((m + args.split - 1) / args.split + kWgradRows - 1) / kWgradRows * kWgradRows;
-            const int32_t first = min(m, part * share);  // share * split < m + 64 * split, far below 2^31
-            t.row0 = s_off[e] + first;
-            t.rows = min(share, m - first);
+            const WgradPart p = wgrad_part(s_off[e + 1] - s_off[e], args.split, part);
+            t.row0 = s_off[e] + p.first;
+            t.rows = p.rows;
         }
         t.k0 = kt * kWgradBM;
         t.n0 = (local - kt * args.tiles_n) * BN;

@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(cta_threads<kEpi, kFp8, kTransW>(), 1)
     if constexpr (kDyn) {
         // both class lists (class P in s_pre, class S in s_order)
         if (warp == 0) build_class_prefix_warp(s_off, s_pre, E, 256, args.n_tiles_n, args.pair_min_rows, 0x7fffffff);
-        if (warp == 1) build_class_prefix_warp(s_off, s_order, E, 128, args.n_tiles_n, 0, args.pair_min_rows);
+        if (warp == 1) build_class_prefix_warp(s_off, s_order, E, 128, args.n_tiles_n, 0, args.pair_min_rows - 1);
         if (warp == 2 && args.sched_split) {
             const int ps = mixed_pair_sms_from_offsets(s_off, E, epi_gate_up(kEpi) ? 2 * args.N : args.N,
                                                        args.pair_min_rows, args.split_sms);

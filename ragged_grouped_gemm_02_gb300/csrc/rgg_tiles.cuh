@@ -54,6 +54,11 @@ __device__ __forceinline__ bool load_and_check_offsets(const int32_t* __restrict
     return __syncthreads_or(bad) == 0;
 }
 
+// Tiles of BM rows of an expert with m rows (m may be up to 2^31 - 1, so m + BM - 1 is unsigned).
+__device__ __forceinline__ int32_t row_tiles(int32_t m, int BM) {
+    return static_cast<int32_t>((static_cast<uint32_t>(m) + static_cast<uint32_t>(BM) - 1u) / static_cast<uint32_t>(BM));
+}
+
 // Exclusive prefix of tiles per expert, s_pre[0..E], computed by one warp
 // (lane = threadIdx.x & 31 of the calling warp).  Each lane sums a contiguous
 // chunk of experts, the warp scans the chunk sums, then each lane writes its
@@ -68,7 +73,7 @@ __device__ __forceinline__ void build_tile_prefix_warp(const int32_t* s_off, int
     int32_t local = 0;
     for (int e = e0; e < e1; ++e) {
         const int32_t m = s_off[e + 1] - s_off[e];
-        local += ((m + BM - 1) / BM) * n_tiles_n;
+        local += row_tiles(m, BM) * n_tiles_n;
     }
     int32_t incl = local;
 #pragma unroll
@@ -80,13 +85,13 @@ __device__ __forceinline__ void build_tile_prefix_warp(const int32_t* s_off, int
     for (int e = e0; e < e1; ++e) {
         s_pre[e] = run;
         const int32_t m = s_off[e + 1] - s_off[e];
-        run += ((m + BM - 1) / BM) * n_tiles_n;
+        run += row_tiles(m, BM) * n_tiles_n;
     }
     if (lane == 31) s_pre[E] = incl;
 }
 
 // The same prefix over one class of experts: expert e counts only when
-// lo <= m_e < hi (its tiles of BM rows), the others add no tiles.  Used by the
+// lo <= m_e <= hi (its tiles of BM rows), the others add no tiles.  Used by the
 // mixed launch, whose CTA pairs take the experts of at least `pair_min_rows`
 // rows in 256-row tiles and whose 1-CTA kernel takes the rest in 128-row
 // tiles, each class with its own flat list in the worklog's order.
@@ -98,7 +103,7 @@ __device__ __forceinline__ void build_class_prefix_warp(const int32_t* s_off, in
     const int e1 = min(E, e0 + per);
     auto tiles = [&](int e) -> int32_t {
         const int32_t m = s_off[e + 1] - s_off[e];
-        return (m >= lo && m < hi) ? ((m + BM - 1) / BM) * n_tiles_n : 0;
+        return (m >= lo && m <= hi) ? row_tiles(m, BM) * n_tiles_n : 0;
     };
     int32_t local = 0;
     for (int e = e0; e < e1; ++e) local += tiles(e);
@@ -133,7 +138,7 @@ __device__ __forceinline__ TileCoord decode_tile(const int32_t* s_off, const int
     const int32_t m_e = s_off[lo + 1] - s_off[lo];
     int32_t mt, nt;
     if (n_major) {
-        const int32_t nm = (m_e + BM - 1) / BM;
+        const int32_t nm = row_tiles(m_e, BM);
         nt = local / nm;
         mt = local - nt * nm;
     } else {
@@ -197,7 +202,7 @@ __device__ __forceinline__ void build_size_order(const int32_t* s_off, int32_t* 
         int32_t local = 0;
         for (int r = r0; r < r1; ++r) {
             const int e = s_order[r];
-            local += ((s_off[e + 1] - s_off[e] + BM - 1) / BM) * n_tiles_n;
+            local += row_tiles(s_off[e + 1] - s_off[e], BM) * n_tiles_n;
         }
         int32_t incl = local;
 #pragma unroll
@@ -209,7 +214,7 @@ __device__ __forceinline__ void build_size_order(const int32_t* s_off, int32_t* 
         for (int r = r0; r < r1; ++r) {
             s_spre[r] = run;
             const int e = s_order[r];
-            run += ((s_off[e + 1] - s_off[e] + BM - 1) / BM) * n_tiles_n;
+            run += row_tiles(s_off[e + 1] - s_off[e], BM) * n_tiles_n;
         }
         if (lane == 31) s_spre[E] = incl;
     }

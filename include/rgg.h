@@ -197,7 +197,8 @@ void rgg_destroy(rgg_handle* h);
  * X, W, Y: device pointers, 16-byte aligned.  group_offsets: device int32
  * [E+1].  Requirements: 1 <= E <= 4096, 0 <= M_tot < 2^31, K >= 8 and
  * N >= 8 with K % 8 == 0 and N % 8 == 0 (the 16-byte row-stride rule of the
- * tensor-memory accelerator).  `opt` may be NULL.
+ * tensor-memory accelerator), both at most 2^31 - 1024 (the gate-up calls: 2N,
+ * the columns of the weight).  `opt` may be NULL.
  *
  * Returns RGG_OK once the launch is queued.  Invalid offsets or a device
  * timeout are reported later by rgg_query_status.  The call allocates

@@ -95,6 +95,7 @@ rgg_status check_sizes(int E, int64_t M_tot, int K, int N) {
     if (E < 1 || E > rgg::kMaxExperts) return E < 1 ? RGG_ERR_INVALID_ARG : RGG_ERR_UNSUPPORTED;
     if (M_tot < 0 || M_tot >= (int64_t(1) << 31)) return RGG_ERR_INVALID_ARG;
     if (K < 8 || N < 8 || (K % 8) != 0 || (N % 8) != 0) return RGG_ERR_INVALID_ARG;
+    if (K > rgg::kMaxWidth || N > rgg::kMaxWidth) return RGG_ERR_INVALID_ARG;
     return RGG_OK;
 }
 
@@ -856,7 +857,7 @@ rgg_status rgg_plan(int num_sms, int smem_optin, int E, int64_t M_tot, int K, in
     const int op = opt ? opt->op : 0;
     if (op < 0 || op > 4) return RGG_ERR_INVALID_ARG;
     const bool swiglu = (op == 1 || op == 4);
-    if (swiglu && (N < 8 || N % 8 != 0 || N > (1 << 30))) return RGG_ERR_INVALID_ARG;
+    if (swiglu && (N < 8 || N % 8 != 0 || N > rgg::kMaxWidth / 2)) return RGG_ERR_INVALID_ARG;
     if (op == 2 && (K % 16 != 0 || N % 16 != 0)) return RGG_ERR_INVALID_ARG;
     const bool gather = (op == 3 || op == 4);
     int mode = 0;
@@ -1047,7 +1048,7 @@ rgg_status gather_call(rgg_handle* h, const void* X_tok, int64_t T, const int32_
     if (!h || !group_offsets || !W) return RGG_ERR_INVALID_ARG;
     rgg_status s = check_sizes(E, M_tot, K, N);
     if (s != RGG_OK) return s;
-    if (swiglu && N > (1 << 30)) return RGG_ERR_INVALID_ARG;
+    if (swiglu && N > rgg::kMaxWidth / 2) return RGG_ERR_INVALID_ARG;
     if (T < 0 || T >= (int64_t(1) << 31)) return RGG_ERR_INVALID_ARG;
     if (M_tot > 0 && (!X_tok || !row_index || !Y || T < 1)) return RGG_ERR_INVALID_ARG;
     if (!aligned(W, 16) || !aligned(group_offsets, 4) ||
@@ -1113,7 +1114,7 @@ rgg_status swiglu_call(rgg_handle* h, const void* X, const void* W13, const int3
     if (!h || !group_offsets || !W13) return RGG_ERR_INVALID_ARG;
     rgg_status s = check_sizes(E, M_tot, K, N);
     if (s != RGG_OK) return s;
-    if (N > (1 << 30)) return RGG_ERR_INVALID_ARG;
+    if (N > rgg::kMaxWidth / 2) return RGG_ERR_INVALID_ARG;
     if (M_tot > 0 && (!X || !out || (backward && !dH))) return RGG_ERR_INVALID_ARG;
     if (!aligned(W13, 16) || !aligned(group_offsets, 4) ||
         (M_tot > 0 && (!aligned(X, 16) || !aligned(out, 16) || !aligned(dH, 16) || !aligned(act, 16))))

@@ -43,7 +43,11 @@ private:
 
 inline bool host_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// 1 <= E <= 4096, 0 <= M_tot < 2^31, K and N at least 8 and multiples of 8.
+// The widest K and N (gate-up: 2N).  Tiles, panels and the quantisers' segments
+// are placed by 32-bit column numbers and end up to 1023 columns past the last.
+constexpr int kMaxWidth = 2147483647 - 1023;
+
+// 1 <= E <= 4096, 0 <= M_tot < 2^31, K and N multiples of 8 from 8 to kMaxWidth.
 rgg_status host_check_sizes(int E, int64_t M_tot, int K, int N);
 
 // The tensor map of a row-major bf16 matrix [rows, cols] with boxes of 64

@@ -24,7 +24,7 @@ static rgg_status mxfp4_call(rgg_handle* h, const void* x_codes, const void* x_s
     if (!h || !group_offsets || !w_codes || !w_scales) return RGG_ERR_INVALID_ARG;
     rgg_status s = host_check_sizes(E, M_tot, K, N);
     if (s != RGG_OK) return s;
-    if (K % kMxBlock != 0 || (gate_up && (N % kMxRows != 0 || N > (1 << 30)))) return RGG_ERR_INVALID_ARG;
+    if (K % kMxBlock != 0 || (gate_up && (N % kMxRows != 0 || N > kMaxWidth / 2))) return RGG_ERR_INVALID_ARG;
     if (M_tot > 0 && (!x_codes || !x_scales || !Y)) return RGG_ERR_INVALID_ARG;
     if (!host_aligned(x_codes, 16) || !host_aligned(x_scales, 16) || !host_aligned(w_codes, 16) ||
         !host_aligned(w_scales, 16) || !host_aligned(Y, 16) || !host_aligned(group_offsets, 4))

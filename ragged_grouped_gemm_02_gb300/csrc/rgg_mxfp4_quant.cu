@@ -356,7 +356,7 @@ rgg_status rgg_mxfp4_quantize_weights(rgg_handle* h, const void* W, void* codes,
                                       void* stream) {
     rgg_status s = mx_check(h, E, 0, K);
     if (s != RGG_OK) return s;
-    if (N < 8 || N % 8 != 0 || !W || !codes || !scales) return RGG_ERR_INVALID_ARG;
+    if (N < 8 || N % 8 != 0 || N > kMaxWidth || !W || !codes || !scales) return RGG_ERR_INVALID_ARG;
     if (!host_aligned(W, 16) || !host_aligned(codes, 16) || !host_aligned(scales, 16)) return RGG_ERR_INVALID_ARG;
     const HostDevice dev = host_device(h);
     HostDeviceScope scope(dev.device);
@@ -392,7 +392,7 @@ rgg_status rgg_mxfp4_dequantize_weights(rgg_handle* h, const void* codes, const 
                                         int N, void* stream) {
     rgg_status s = mx_check(h, E, 0, K);
     if (s != RGG_OK) return s;
-    if (N < 8 || N % 8 != 0 || !W || !codes || !scales) return RGG_ERR_INVALID_ARG;
+    if (N < 8 || N % 8 != 0 || N > kMaxWidth || !W || !codes || !scales) return RGG_ERR_INVALID_ARG;
     if (!host_aligned(W, 16) || !host_aligned(codes, 16) || !host_aligned(scales, 16)) return RGG_ERR_INVALID_ARG;
     const HostDevice dev = host_device(h);
     HostDeviceScope scope(dev.device);

@@ -492,10 +492,11 @@ typedef struct rgg_tensor {
  * are rounded once to their type.  Where the factor is 1, tensors clipped in
  * place are not written.
  *
- * A norm that is not finite (a gradient holds Inf or NaN) leaves the values
- * unscaled: `out` is then a copy of `in`, and norm_out says so to the caller,
- * who skips the step or handles it.  max_norm may be 0 (all results 0) or Inf
- * (the norm alone); a negative one or NaN is RGG_ERR_INVALID_ARG.
+ * A norm that is not finite (a gradient holds Inf or NaN, or the norm passes
+ * fp32's range) leaves the values unscaled: `out` is then a copy of `in`, and
+ * norm_out says so to the caller, who skips the step or handles it.  max_norm
+ * may be 0 (all results 0) or Inf (the norm alone); a negative one or NaN is
+ * RGG_ERR_INVALID_ARG.
  *
  * workspace: device memory of at least rgg_clip_grad_norm_workspace(count)
  * bytes, 8-byte aligned, not shared by calls that may overlap.  Nothing is

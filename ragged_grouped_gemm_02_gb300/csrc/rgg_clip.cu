@@ -263,10 +263,11 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas)
     double sum = 0.0;
     for (int i = threadIdx.x; i < n_partial; i += kClipThreads) sum += partial[i];
     const double norm = sqrt(clip_block_sum(sum));
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
-    // a norm that is not finite leaves the gradients unscaled (see rgg.h)
+    const float told = static_cast<float>(norm);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = told;
+    // a norm that is not finite, as the caller sees it, leaves the gradients unscaled (see rgg.h)
     const double factor = max_norm / (norm + 1e-6);
-    const float scale = (isfinite(norm) && factor < 1.0) ? static_cast<float>(factor) : 1.0f;
+    const float scale = (isfinite(told) && factor < 1.0) ? static_cast<float>(factor) : 1.0f;
     for (int32_t c = list.chunks - 1 - static_cast<int32_t>(blockIdx.x); c >= 0; c -= gridDim.x) {
         const ClipPart p = clip_part(list, c);
         const ClipTensor& t = list.t[p.index];

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas)
 }
 
 template <int kDtype>
-__device__ __forceinline__ void clip_scale(const ClipTensor& t, const ClipPart& p, float scale) {
+__device__ __forceinline__ void clip_scale(const ClipTensor& t, const ClipPart& p, float shift, float scale) {
     constexpr int kSize = ClipType<kDtype>::kSize;
     const char* in = static_cast<const char*>(t.in) + p.first * kSize;
     char* out = static_cast<char*>(t.out) + p.first * kSize;
@@ -230,7 +230,7 @@ __device__ __forceinline__ void clip_scale(const ClipTensor& t, const ClipPart& 
     for (int32_t i = threadIdx.x; i < loose; i += kClipThreads) {
         const int32_t at = i < head ? i : tail0 + (i - head);
         if (scale != 1.0f)
-            clip_store_one<kDtype>(out, at, clip_load_one<kDtype>(in, at) * scale);
+            clip_store_one<kDtype>(out, at, clip_load_one<kDtype>(in, at) * shift * scale);
         else if constexpr (kSize == 4)
             reinterpret_cast<uint32_t*>(out)[at] = reinterpret_cast<const uint32_t*>(in)[at];
         else
@@ -245,10 +245,10 @@ __device__ __forceinline__ void clip_scale(const ClipTensor& t, const ClipPart& 
         for (int j = 0; j < 4; ++j) {
             if (scale == 1.0f) break;  // a copy, NaN payloads included
             if constexpr (kDtype == RGG_FP32)
-                w[j] = __float_as_uint(__uint_as_float(w[j]) * scale);
+                w[j] = __float_as_uint(__uint_as_float(w[j]) * shift * scale);
             else
-                w[j] = ClipType<kDtype>::pack(ClipType<kDtype>::low(w[j]) * scale,
-                                              ClipType<kDtype>::high(w[j]) * scale);
+                w[j] = ClipType<kDtype>::pack(ClipType<kDtype>::low(w[j]) * shift * scale,
+                                              ClipType<kDtype>::high(w[j]) * shift * scale);
         }
         st_global_v4(body_out + at, w[0], w[1], w[2], w[3]);
     }
@@ -267,14 +267,19 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas)
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = told;
     // a norm that is not finite, as the caller sees it, leaves the gradients unscaled (see rgg.h)
     const double factor = max_norm / (norm + 1e-6);
-    const float scale = (isfinite(told) && factor < 1.0) ? static_cast<float>(factor) : 1.0f;
+    // A factor below fp32's normal range has a power of two taken out, which the
+    // values are multiplied by first: exactly, or so far down that the result is
+    // 0 either way.
+    double shift = 1.0;
+    if (factor < 0x1p-126) shift = factor < 0x1p-190 ? 0x1p-128 : 0x1p-64;
+    const float scale = (isfinite(told) && factor < 1.0) ? static_cast<float>(factor / shift) : 1.0f;
     for (int32_t c = list.chunks - 1 - static_cast<int32_t>(blockIdx.x); c >= 0; c -= gridDim.x) {
         const ClipPart p = clip_part(list, c);
         const ClipTensor& t = list.t[p.index];
         if (scale == 1.0f && t.in == t.out) continue;
-        if (t.dtype == RGG_BF16) clip_scale<RGG_BF16>(t, p, scale);
-        else if (t.dtype == RGG_FP32) clip_scale<RGG_FP32>(t, p, scale);
-        else clip_scale<RGG_FP16>(t, p, scale);
+        if (t.dtype == RGG_BF16) clip_scale<RGG_BF16>(t, p, static_cast<float>(shift), scale);
+        else if (t.dtype == RGG_FP32) clip_scale<RGG_FP32>(t, p, static_cast<float>(shift), scale);
+        else clip_scale<RGG_FP16>(t, p, static_cast<float>(shift), scale);
     }
 }
 

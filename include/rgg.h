@@ -492,6 +492,11 @@ typedef struct rgg_tensor {
  * are rounded once to their type.  Where the factor is 1, tensors clipped in
  * place are not written.
  *
+ * Nothing that the call writes may overlap anything else that it reads or
+ * writes (a tensor listed twice, views of one memory): RGG_ERR_INVALID_ARG.
+ * Inputs may overlap one another, and in place with max_norm Inf, which writes
+ * no tensor, anything may.
+ *
  * A norm that is not finite (a gradient holds Inf or NaN, or the norm passes
  * fp32's range) leaves the values unscaled: `out` is then a copy of `in`, and
  * norm_out says so to the caller, who skips the step or handles it.  max_norm

@@ -625,7 +625,8 @@ def rgg_clip_grad_norm(grads, max_norm, out=None, *, stream=None):
     ``min(1, max_norm / (norm + 1e-6))``: in place, or into the tensors ``out``.
 
     grads: contiguous CUDA tensors on one device, bf16, fp16 or fp32 (types
-    may differ); out: as many, each of its gradient's type and size.  Returns
+    may differ); out: as many, each of its gradient's type and size.  What is
+    written must not overlap any other tensor of the call.  Returns
     the norm before clipping, an fp32 CUDA scalar (nothing is synchronised).
     If it is not finite the gradients are left (or copied) unscaled."""
     import torch

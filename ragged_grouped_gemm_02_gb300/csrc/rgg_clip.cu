@@ -27,6 +27,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "rgg_host.h"
 #include "rgg_internal.h"
@@ -283,6 +285,35 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas)
     }
 }
 
+// Memory that a call reads or writes.
+struct ClipRange {
+    uintptr_t first, end;
+    bool written;
+};
+
+// Whether something the call writes overlaps anything else it reads or writes:
+// the chunks are scaled in any order, so such elements would be scaled twice or
+// not.  `ranges` has room for two of each tensor.
+static bool clip_overlaps(const rgg_tensor* tensors, int count, bool norm_alone, ClipRange* ranges) {
+    size_t n = 0;
+    for (int i = 0; i < count; ++i) {
+        const rgg_tensor& t = tensors[i];
+        if (t.numel == 0) continue;
+        const uintptr_t in = reinterpret_cast<uintptr_t>(t.in), out = reinterpret_cast<uintptr_t>(t.out);
+        const uintptr_t bytes = static_cast<uintptr_t>(t.numel) * (t.dtype == RGG_FP32 ? 4 : 2);
+        if (in != out) ranges[n++] = ClipRange{in, in + bytes, false};
+        ranges[n++] = ClipRange{out, out + bytes, in != out || !norm_alone};
+    }
+    std::sort(ranges, ranges + n, [](const ClipRange& a, const ClipRange& b) { return a.first < b.first; });
+    uintptr_t end = 0, written_end = 0;  // of the ranges so far
+    for (size_t i = 0; i < n; ++i) {
+        if (ranges[i].first < (ranges[i].written ? end : written_end)) return true;
+        end = std::max(end, ranges[i].end);
+        if (ranges[i].written) written_end = std::max(written_end, ranges[i].end);
+    }
+    return false;
+}
+
 static int clip_launches(int count) { return count <= kClipFew ? 1 : (count + kClipMany - 1) / kClipMany; }
 
 static int clip_grid(int num_sms, int32_t chunks) {
@@ -354,6 +385,16 @@ extern "C" rgg_status rgg_clip_grad_norm(rgg_handle* h, const rgg_tensor* tensor
         if (t.numel < 0 || (t.numel > 0 && (!t.in || !t.out || !host_aligned(t.in, size) || !host_aligned(t.out, size))))
             return RGG_ERR_INVALID_ARG;
     }
+    ClipRange few[2 * kClipFew];
+    std::unique_ptr<ClipRange[]> many;
+    if (count > kClipFew) {
+        many.reset(new (std::nothrow) ClipRange[2 * static_cast<size_t>(count)]);
+        if (!many) {
+            host_set_last_error("rgg_clip_grad_norm: out of host memory");
+            return RGG_ERR_CUDA;
+        }
+    }
+    if (clip_overlaps(tensors, count, std::isinf(max_norm), many ? many.get() : few)) return RGG_ERR_INVALID_ARG;
     const HostDevice dev = host_device(h);
     HostDeviceScope scope(dev.device);
     if (scope.error() != cudaSuccess) return host_cuda_failure(scope.error(), "cudaSetDevice");

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kQuantThreads)
 __global__ void __launch_bounds__(kQuantThreads)
     mx_quantize_weights_kernel(const __nv_bfloat16* __restrict__ W, int K, int N, uint8_t* __restrict__ codes,
                                uint8_t* __restrict__ scales, int nblocks, int kblocks) {
-    __shared__ uint8_t s_scale[kMxBlockBytes];
+    __shared__ __align__(16) uint8_t s_scale[kMxBlockBytes];  // read 16 bytes at a time
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

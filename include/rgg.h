@@ -88,7 +88,9 @@ typedef struct rgg_options {
     int op;                      /* for rgg_plan only: 0 = plan rgg_grouped_gemm, 1 = plan
                                     rgg_grouped_gemm_swiglu (then N is the output width), 2 = plan
                                     rgg_grouped_gemm_fp8, 3 = plan rgg_grouped_gemm_gather, 4 = plan
-                                    rgg_grouped_gemm_swiglu_gather (N is the output width) */
+                                    rgg_grouped_gemm_swiglu_gather (N is the output width), 5 = plan
+                                    rgg_grouped_gemm_dgrad, 6 = plan rgg_grouped_gemm_swiglu_backward (N is the
+                                    width of H); K and N as the call takes them */
     int walk_order;              /* order of the persistent CTAs' walk over the tile list (any order gives the
                                     same result): 0 = automatic (list order, or 3 when host_counts show a
                                     strong skew, or 4 when experts average three M tiles or more),
@@ -405,10 +407,11 @@ rgg_status rgg_grouped_gemm_swiglu_gather(rgg_handle* h, const void* X_tok, int6
  *     dX[i, :] = dY[i, :] . W[e]^T      for every row i of expert e
  *
  * dY: bf16 [M_tot, N]; W: bf16 [E, K, N], as the forward call has it; dX: bf16
- * [M_tot, K], written only on rows some expert owns.  The same kernels, plans,
- * requirements, options, errors and stream contract as rgg_grouped_gemm, with N
- * as the reduction and K as the output width (rgg_plan with K and N exchanged
- * shows the configuration).
+ * [M_tot, K], written only on rows some expert owns.  Kernels, requirements,
+ * options, errors and stream contract as for rgg_grouped_gemm, with N as the
+ * reduction and K as the output width.  Where few tiles are to be computed it
+ * plans smaller ones than rgg_grouped_gemm; rgg_plan with op 5 shows the
+ * configuration.
  */
 rgg_status rgg_grouped_gemm_dgrad(rgg_handle* h, const void* dY, const void* W, const int32_t* group_offsets,
                                   void* dX, int E, int64_t M_tot, int K, int N, void* stream,
@@ -428,7 +431,8 @@ rgg_status rgg_grouped_gemm_dgrad(rgg_handle* h, const void* dY, const void* W, 
  * [M_tot, N]; dGU: bf16 [M_tot, 2N]; H: bf16 [M_tot, N] or NULL.  dX is then
  * rgg_grouped_gemm_dgrad(dGU, W13), dW13 is rgg_grouped_gemm_wgrad(X, dGU), and
  * the down projection's weight gradient reads H.  Other arguments, options
- * and errors as for rgg_grouped_gemm_swiglu.
+ * and errors as for rgg_grouped_gemm_swiglu; rgg_plan with op 6 shows the
+ * configuration.
  */
 rgg_status rgg_grouped_gemm_swiglu_backward(rgg_handle* h, const void* X, const void* W13,
                                             const int32_t* group_offsets, const void* dH, void* dGU, void* H, int E,

@@ -886,14 +886,18 @@ def rgg_query_status(device: int | None = None, stream=None) -> int:
 def rgg_plan(E: int, M_tot: int, K: int, N: int, *, num_sms: int = 0, smem_optin: int = 0, bm=0, bn=0,
              stages=0, max_ctas=0, host_counts=None, tail64=0, op: str = "gemm",
              walk_order=0, gather_mode=0, workspace=None, mixed=0, mixed_pair_sms=0, pair_min_rows=0) -> dict:
-    """The launch configuration rgg_grouped_gemm (op="gemm") or
-    rgg_grouped_gemm_swiglu (op="swiglu", N = output width) would use (host-only).
+    """The launch configuration rgg_grouped_gemm (op="gemm"),
+    rgg_grouped_gemm_swiglu (op="swiglu", N = output width), the FP8 and gather
+    calls ("fp8", "gather", "swiglu_gather"), rgg_grouped_gemm_dgrad ("dgrad") or
+    rgg_grouped_gemm_swiglu_backward ("swiglu_backward", N = width of H) would use
+    for the K and N that the call takes (host-only).
     For the gather ops, ``workspace`` (the tensor the call would get, True
     for "a workspace will be given", or None) decides whether the two-pass
     mode can run; the planner only looks at whether there is one."""
     lib = load_library()
     opt, keep = _options(bm, bn, stages, max_ctas, 0, host_counts, 0, tail64,
-                         {"gemm": 0, "swiglu": 1, "fp8": 2, "gather": 3, "swiglu_gather": 4}[op], walk_order,
+                         {"gemm": 0, "swiglu": 1, "fp8": 2, "gather": 3, "swiglu_gather": 4, "dgrad": 5,
+                          "swiglu_backward": 6}[op], walk_order,
                          gather_mode, mixed=mixed, mixed_pair_sms=mixed_pair_sms, pair_min_rows=pair_min_rows)
     if workspace is True:
         opt.workspace = 16  # never dereferenced: rgg_plan reads only whether a workspace is given

@@ -16,6 +16,7 @@
 #include <mutex>
 #include <new>
 #include <string>
+#include <utility>
 
 #include "rgg.h"
 #include "rgg_counters.h"
@@ -197,9 +198,31 @@ rgg_status plan_mixed(int grid_cap, int smem_optin, int E, int64_t M_tot, int N,
 // 1 291, prefill 2 714 vs 2 775 -- so it has no pair form) and the fused
 // token gather take both; the fused gate-up + SiLU op (N then counts the 2N
 // weight columns) takes kPlanNoBn192; the plain token-gather GEMM kPlanNoPair.
+// kPlanGradient, beside either: dgrad and the gate-up backward, whose plan differs
+// from the forward one where tiles are few (few_tiles_options).
 constexpr int kPlanNoPair = 1;
 constexpr int kPlanNoBn192 = 2;
+constexpr int kPlanGradient = 4;
 constexpr int kPlanFused = kPlanNoPair | kPlanNoBn192;
+
+// The gradients' tiles where they are few: 64 x 128, the smallest, where one
+// wave holds them all (counted with every expert's last tile partial).  Each SM
+// then streams the least weight per stage, which is what such a call waits for.
+// Back to back in a graph, dX of one expert, 533 rows, 504 x 1768: 17.3 -> 11.4
+// us; the gate-up backward of two experts with 5 rows each, 3048 x 280: 25.1 ->
+// 15.1 us.  The forward calls keep the plan that their workloads were measured
+// with; the rule was not measured on them.
+const rgg_options* few_tiles_options(int num_sms, int E, int64_t M_tot, int columns, const rgg_options* opt,
+                                     rgg_options* own) {
+    if (opt && (opt->bm != 0 || opt->bn != 0 || opt->mixed != 0)) return opt;
+    const int64_t tiles = (M_tot / 64 + std::min<int64_t>(E, M_tot)) * ceil_div(columns, 128);
+    const int sms = (opt && opt->max_ctas > 0) ? std::min(num_sms, opt->max_ctas) : num_sms;
+    if (tiles > sms) return opt;
+    *own = opt ? *opt : rgg_options{};
+    own->bm = 64;
+    own->bn = 128;
+    return own;
+}
 
 rgg_status make_plan(int num_sms, int smem_optin, int E, int64_t M_tot, int K, int N, const rgg_options* opt,
                      Plan* out, int kind = 0) {
@@ -209,6 +232,9 @@ rgg_status make_plan(int num_sms, int smem_optin, int E, int64_t M_tot, int K, i
     if (s != RGG_OK) return s;
     if (num_sms <= 0) num_sms = kDefaultSms;
     if (smem_optin <= 0) smem_optin = kDefaultSmemOptin;
+    rgg_options few;
+    if ((kind & kPlanGradient) != 0) opt = few_tiles_options(num_sms, E, M_tot, N, opt, &few);
+    kind &= ~kPlanGradient;
     const int want_bm = opt ? opt->bm : 0;
     const int want_bn = opt ? opt->bn : 0;
     const int want_stages = opt ? opt->stages : 0;
@@ -707,24 +733,6 @@ rgg_status host_check_gemm_args(const void* X, const void* W, const int32_t* gro
     return RGG_OK;
 }
 
-// The gradients' tiles where they are few: 64 x 128, the smallest, where one
-// wave holds them all (counted with every expert's last tile partial).  Each SM
-// then streams the least weight per stage, which is what such a call waits for.
-// dX of one expert, 533 rows, 504 x 1768: 23 -> 17 us; the gate-up backward of
-// two experts with 5 rows each, 3048 x 280: 29 -> 19 us.
-static const rgg_options* few_tiles_options(int num_sms, int E, int64_t M_tot, int columns, const rgg_options* opt,
-                                            rgg_options* own) {
-    if (opt && (opt->bm != 0 || opt->bn != 0 || opt->mixed != 0)) return opt;
-    const int64_t tiles = (M_tot / 64 + std::min<int64_t>(E, M_tot)) * ceil_div(columns, 128);
-    int sms = num_sms > 0 ? num_sms : kDefaultSms;
-    if (opt && opt->max_ctas > 0) sms = std::min(sms, opt->max_ctas);
-    if (tiles > sms) return opt;
-    *own = opt ? *opt : rgg_options{};
-    own->bm = 64;
-    own->bn = 128;
-    return own;
-}
-
 rgg_status host_grouped_gemm(int num_sms, int smem_optin, int32_t* status, const void* X, const void* W,
                              const int32_t* group_offsets, void* Y, int E, int64_t M_tot, int K, int N,
                              cudaStream_t st, const rgg_options* opt, rgg_handle* h, bool trans_w) {
@@ -732,10 +740,8 @@ rgg_status host_grouped_gemm(int num_sms, int smem_optin, int32_t* status, const
         cudaError_t err = launch_validate_offsets(group_offsets, E, M_tot, status, st);
         return err == cudaSuccess ? RGG_OK : cuda_failure(err, "validate_offsets launch");
     }
-    rgg_options few;
-    if (trans_w) opt = few_tiles_options(num_sms, E, M_tot, N, opt, &few);
     Plan p;
-    rgg_status s = make_plan(num_sms, smem_optin, E, M_tot, K, N, opt, &p, 0);
+    rgg_status s = make_plan(num_sms, smem_optin, E, M_tot, K, N, opt, &p, trans_w ? kPlanGradient : 0);
     if (s != RGG_OK) return s;
     CUtensorMap tx, tx64, tw;
     s = encode_maps(X, W, E, M_tot, K, N, p.bm, &tx, &tx64, &tw, trans_w);
@@ -855,8 +861,9 @@ rgg_status rgg_plan(int num_sms, int smem_optin, int E, int64_t M_tot, int K, in
     if (!out) return RGG_ERR_INVALID_ARG;
     Plan p;
     const int op = opt ? opt->op : 0;
-    if (op < 0 || op > 4) return RGG_ERR_INVALID_ARG;
-    const bool swiglu = (op == 1 || op == 4);
+    if (op < 0 || op > 6) return RGG_ERR_INVALID_ARG;
+    const bool swiglu = (op == 1 || op == 4 || op == 6);
+    if (op == 5) std::swap(K, N);  // dgrad's reduction and output width
     if (swiglu && (N < 8 || N % 8 != 0 || N > rgg::kMaxWidth / 2)) return RGG_ERR_INVALID_ARG;
     if (op == 2 && (K % 16 != 0 || N % 16 != 0)) return RGG_ERR_INVALID_ARG;
     const bool gather = (op == 3 || op == 4);
@@ -872,6 +879,8 @@ rgg_status rgg_plan(int num_sms, int smem_optin, int E, int64_t M_tot, int K, in
     const int kind = (op == 2)                   ? kPlanFused
                      : (op == 4 && fused_gather) ? kPlanFused
                      : (op == 3 && fused_gather) ? kPlanNoPair
+                     : (op == 5)                 ? kPlanGradient
+                     : (op == 6)                 ? (kPlanNoBn192 | kPlanGradient)
                      : swiglu                    ? kPlanNoBn192
                                                  : 0;
     rgg_status s = make_plan(num_sms, smem_optin, E, M_tot, K, swiglu ? 2 * N : N, opt, &p, kind);
@@ -881,8 +890,8 @@ rgg_status rgg_plan(int num_sms, int smem_optin, int E, int64_t M_tot, int K, in
     out->bk = (op == 2) ? 128 : rgg::kBK;
     out->stages = p.stages;
     out->grid = p.grid;
-    // FP8 and the fused gate-up op run eight epilogue warps (on CTA pairs: per CTA)
-    out->threads = (op == 2 || swiglu) ? rgg::cta_threads<rgg::kEpiSwiGLU, false>() : rgg::kThreads;  // 320 or 192
+    // FP8, the gate-up ops and dgrad run eight epilogue warps (on CTA pairs: per CTA)
+    out->threads = (op == 2 || op == 5 || swiglu) ? rgg::cta_threads<rgg::kEpiSwiGLU, false>() : rgg::kThreads;  // 320 or 192
     out->smem_bytes = p.smem_bytes;
     out->tmem_cols = (p.bm == 256 || 2 * p.bn > 256) ? 512 : 256;
     out->max_tiles = p.max_tiles;
@@ -1127,9 +1136,8 @@ rgg_status swiglu_call(rgg_handle* h, const void* X, const void* W13, const int3
         return err == cudaSuccess ? RGG_OK : cuda_failure(err, "validate_offsets launch");
     }
     Plan p;
-    rgg_options few;
-    if (backward) opt = rgg::few_tiles_options(h->num_sms, E, M_tot, 2 * N, opt, &few);
-    s = make_plan(h->num_sms, h->smem_optin, E, M_tot, K, 2 * N, opt, &p, kPlanNoBn192);
+    s = make_plan(h->num_sms, h->smem_optin, E, M_tot, K, 2 * N, opt, &p,
+                  kPlanNoBn192 | (backward ? kPlanGradient : 0));
     if (s != RGG_OK) return s;
     CUtensorMap tx, tx64, tw;
     s = encode_maps(X, W13, E, M_tot, K, 2 * N, p.bm, &tx, &tx64, &tw);

@@ -54,15 +54,26 @@ def expert_ffn(X, W13, W2, group_offsets):
 
 
 def quantize_experts(W13, W2):
-    """The layer's weights in MXFP4, laid out once: what ``expert_ffn_mxfp4`` takes."""
-    return rgg_mxfp4_quantize_weights(W13.detach()), rgg_mxfp4_quantize_weights(W2.detach())
+    """The layer's weights in MXFP4, laid out once: what ``expert_ffn_mxfp4`` takes.
+
+    The gate-up product takes widths N of whole 128s, so other widths are filled
+    up with zero columns of gate and up and zero rows of W2: their activations are
+    0 and add nothing.  (A width of 1344 becomes 1408: 5 % more weight.)"""
+    W13, W2 = W13.detach(), W2.detach()
+    N = W2.shape[1]
+    if W13.shape[2] != 2 * N:
+        raise ValueError("W13 must be [E, K, 2N] and W2 [E, N, K_out], not %s and %s" % (tuple(W13.shape), tuple(W2.shape)))
+    fill = -N % 128
+    if fill:
+        W13 = torch.cat([torch.nn.functional.pad(half, (0, fill)) for half in W13.split(N, 2)], 2)
+        W2 = torch.nn.functional.pad(W2, (0, 0, 0, fill))
+    return rgg_mxfp4_quantize_weights(W13), rgg_mxfp4_quantize_weights(W2)
 
 
 def expert_ffn_mxfp4(X, experts, group_offsets):
     """Y for routed rows X with 4-bit weights (``quantize_experts``) and
-    activations quantised on the way.  K, N and K_out as the MXFP4 products want
-    them: K a multiple of 32, N of 128, K_out of 8.  Rows of no expert hold
-    unspecified values."""
+    activations quantised on the way.  K must be a multiple of 32, K_out of 8.
+    Rows of no expert hold unspecified values."""
     w13, w2 = experts
     H = rgg_grouped_gemm_swiglu_mxfp4(*rgg_mxfp4_quantize(X, group_offsets), *w13, group_offsets)
     return rgg_grouped_gemm_mxfp4(*rgg_mxfp4_quantize(H, group_offsets), *w2, group_offsets)

@@ -168,29 +168,6 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint
     return true;
 }
 
-// Kernels on clusters of two CTAs: as wait_or_abort, and a timeout also raises
-// the other CTA's abort flag (its shared::cluster address), so both leave
-// their loops instead of waiting on arrivals that will not come.
-// kClusterAcquire: the barrier is arrived on by the other CTA after it wrote
-// (or read) this CTA's shared memory, so the wait acquires at cluster scope.
-template <bool kClusterAcquire = false>
-__device__ __forceinline__ bool pair_wait_or_abort(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                                   uint32_t peer_flag_cluster, int32_t* status, uint64_t timeout_ns) {
-    auto probe = [&]() { return kClusterAcquire ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-    if (probe()) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-        if (probe()) return true;
-        if (*abort_flag) return false;
-        if (global_timer_ns() - t0 > timeout_ns) {
-            *abort_flag = 1u;
-            st_shared_cluster_u32(peer_flag_cluster, 1u);
-            atomicCAS(status, 0, kStatusTimeout);
-            return false;
-        }
-    }
-}
-
 __device__ __forceinline__ void spin_ns(uint64_t ns) {
     const uint64_t t0 = global_timer_ns();
     while (global_timer_ns() - t0 < ns) {

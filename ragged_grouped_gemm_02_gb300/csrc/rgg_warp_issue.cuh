@@ -31,8 +31,12 @@ __device__ __forceinline__ int uniform_warp() {
     return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
 }
 
-// Bounded wait of a whole warp, the same answer in every lane; kPair mirrors a
-// timeout into the peer CTA's abort flag, kAcquire acquires at cluster scope.
+// Bounded wait of a whole warp, the same answer in every lane.  kPair: on a
+// cluster of two CTAs, where a timeout also raises the other CTA's abort flag
+// (its shared::cluster address), so that both leave their loops instead of
+// waiting on arrivals that will not come.  kAcquire: the barrier is arrived on
+// by the other CTA after it wrote (or read) this CTA's shared memory, so the
+// wait acquires at cluster scope.
 template <bool kPair, bool kAcquire>
 __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
                                             uint32_t peer_flag, int32_t* status, uint64_t timeout_ns) {
@@ -132,7 +136,8 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint32_t bar) {
             : "memory");
 }
 
-// D[tmem] (+)= A * B with bf16 (kFp8: E4M3) operands, as mma_bf16_ss and mma_f8_ss.
+// D[tmem] (+)= A[smem] * B[smem], both operands bf16 (K = 16 an instruction) or,
+// kFp8, E4M3 (kind::f8f6f4, K = 32), fp32 accumulator.
 template <bool kFp8>
 __device__ __forceinline__ void mma_single_if(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate) {
@@ -154,7 +159,8 @@ __device__ __forceinline__ void mma_single_if(uint32_t lead, uint32_t d_tmem, ui
             : "memory");
 }
 
-// D[tmem of both CTAs] (+)= A * B, bf16, as mma_bf16_ss_pair.
+// D[tmem of both CTAs] (+)= A[smem of both CTAs] * B[smem of both CTAs], bf16:
+// M = 256 rows split 128/128 over the pair, B's N columns split in halves.
 __device__ __forceinline__ void mma_bf16_pair_if(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                                  uint32_t idesc, uint32_t accumulate) {
     asm volatile(

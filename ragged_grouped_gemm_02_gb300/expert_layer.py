@@ -60,8 +60,8 @@ def quantize_experts(W13, W2):
     up with zero columns of gate and up and zero rows of W2: their activations are
     0 and add nothing.  (A width of 1344 becomes 1408: 5 % more weight.)"""
     W13, W2 = W13.detach(), W2.detach()
-    N = W2.shape[1]
-    if W13.shape[2] != 2 * N:
+    N = W2.shape[1] if W2.dim() == 3 else 0
+    if W13.dim() != 3 or N == 0 or W13.shape[2] != 2 * N:
         raise ValueError("W13 must be [E, K, 2N] and W2 [E, N, K_out], not %s and %s" % (tuple(W13.shape), tuple(W2.shape)))
     fill = -N % 128
     if fill:

@@ -73,3 +73,7 @@ def test_refusals():
         quantize_experts(W13.cuda(), W2[:, :128].contiguous().cuda())
     with pytest.raises(ValueError):
         quantize_experts(W13[:, :, :256].contiguous().cuda(), W2.cuda())
+    with pytest.raises(ValueError):
+        quantize_experts(W13[0].cuda(), W2.cuda())
+    with pytest.raises(ValueError):
+        quantize_experts(W13.cuda(), W2[0, 0].cuda())

@@ -341,8 +341,9 @@ const char* rgg_last_cuda_error(void);
  * and, when status_out is not NULL, copies the final status word into
  * *status_out (device memory or pinned host memory, int32): RGG_OK,
  * RGG_ERR_BAD_OFFSETS or RGG_ERR_DEVICE_TIMEOUT, valid once the stream has
- * reached that point.  All calls share the one array, so calls that overlap
- * on the GPU (other streams, other threads) race on it.
+ * reached that point.  All calls share the one array, status word and tile
+ * counters, so calls must not overlap on the GPU: keep them in order on one
+ * stream.  (Calls on a handle may overlap.)
  *
  * Arguments, layouts and ownership as for rgg_grouped_gemm; asynchronous on
  * `stream` (a cudaStream_t, NULL = legacy default stream).
@@ -559,7 +560,8 @@ rgg_status rgg_mxfp4_dequantize_weights(rgg_handle* h, const void* codes, const 
  * in fp32 on the tensor core (tcgen05.mma kind::mxf4 with block scaling),
  * rounded once to bf16.  rgg_grouped_gemm_swiglu_mxfp4 is the gate-up projection:
  * the weight has 2N columns, gate first, and H = silu(g) * u is bf16 [M_tot, N];
- * N must then be a multiple of 128.  Operands as the quantisers leave them.  Of
+ * N must then be a multiple of 128 (fill gate and up with zero columns before
+ * quantising a weight of another width; their outputs are 0).  Operands as the quantisers leave them.  Of
  * `opt` they read bn (256: 256 x 256 tiles on CTA pairs, 128: 128 x 128 tiles on
  * single CTAs, 0: by a cost estimate), bm (0 or the same), stages, max_ctas
  * (at least 2 for pairs), timeout_ns and debug_flags.  Other arguments, errors and

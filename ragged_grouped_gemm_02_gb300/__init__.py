@@ -831,7 +831,8 @@ def rgg_grouped_gemm_mxfp4(x_codes, x_scales, w_codes, w_scales, group_offsets, 
 def rgg_grouped_gemm_swiglu_mxfp4(x_codes, x_scales, w13_codes, w13_scales, group_offsets, H=None, *, bn=0, stages=0,
                                   max_ctas=0, timeout_ns=0, debug_flags=0, stream=None, check=False):
     """H = silu(gate) * up for every expert with MXFP4 operands: w13_codes hold
-    the 2N columns of W13 (gate first), N a multiple of 128; H: optional bf16
+    the 2N columns of W13 (gate first), N a multiple of 128 (``expert_layer``
+    fills other widths up with zero columns); H: optional bf16
     CUDA [M_tot, N]."""
     return _mxfp4_call("rgg_grouped_gemm_swiglu_mxfp4", x_codes, x_scales, w13_codes, w13_scales, group_offsets, H,
                        True, bn, stages, max_ctas, timeout_ns, debug_flags, stream, check)

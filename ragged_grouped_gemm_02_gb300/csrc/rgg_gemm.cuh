@@ -319,7 +319,9 @@ struct GradRow {
 // `col`): with
 // s = 1 / (1 + exp(-g)),
 //     dG = dH * u * s * (1 + g * (1 - s)),  dU = dH * g * s,  H = g * s * u,
-// in fp32 from the unrounded accumulators, each rounded once to bf16.
+// in fp32 from the unrounded accumulators, each rounded once to bf16.  s comes
+// from the approximate division (2 ulp, far below bf16's rounding; 0 where the
+// denominator passes 2^126, that is for g below -87).
 __device__ __forceinline__ void store_swiglu_backward(const GemmArgs& args, int64_t row, bool row_ok, int col,
                                                       const uint32_t (&v)[32], const uint32_t (&u)[32],
                                                       const GradRow& grad, bool second, int lane, int32_t row_lo,

@@ -28,11 +28,12 @@
 // itself has been read as well (acc_empty).  The scales of a stage take 24
 // columns, in two sets used in turn.
 //
-// Measured on a GB300: 32 experts, 32,768 rows, K = 6144, N = 4096 240 us (6 870
-// TFLOP/s), gate-up of the same size 232 us; 16 rows per expert, gate-up, 74 us
-// (5.8 TB/s).  At many rows the issuing warp sets the pace: four MMAs (0.19 us at
-// the nominal rate) and six scale copies take 0.275 us a stage; tiles of 256 x
-// 192 with two whole accumulators took as long a stage and lost (287 us).
+// Measured on GB300 machines: 32 experts, 32,768 rows, K = 6144, N = 4096 240 to 263
+// us (6 870 to 6 280 TFLOP/s), gate-up of the same size 232 to 259 us; 16 rows per
+// expert, gate-up, 69 us (6.3 TB/s).  At many rows the issuing warp sets the pace:
+// four MMAs (0.19 us at the nominal rate) and six scale copies take 0.275 us a
+// stage; tiles of 256 x 192 with two whole accumulators took as long a stage and
+// lost (287 us).
 #pragma once
 
 #include "rgg_mxfp4.h"

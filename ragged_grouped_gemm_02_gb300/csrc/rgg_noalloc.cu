@@ -14,7 +14,8 @@
 // The array is small and fixed: every GPU that loads librgg.so holds it until
 // the process exits.  All calls share it, so calls that run at the same time
 // on the GPU (on different streams, or from different threads) race on the
-// status word; serialise them if you read status_out.
+// status word and on the mixed launch's tile counters: keep them in order on one
+// stream.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -182,7 +182,7 @@ typedef struct rgg_plan_info {
  * stream in its capture, so launches that overlap on the GPU never share one;
  * the handle keeps a set for each stream and each capture that it has seen,
  * and once all are taken further ones run the mixed launch without claims
- * (same results).  A stream that takes part in a capture must live until the
+ * (same results), as captures of cudaStreamPerThread do.  A stream that takes part in a capture must live until the
  * capture ends, and two instances of one graph must not run side by side.
  */
 rgg_status rgg_create(rgg_handle** out, int device);

@@ -598,8 +598,9 @@ rgg_status swiglu_call(rgg_handle* h, const void* X, const void* W13, const int3
                        bool backward);
 
 // The tile counters of a launch with claims on `stream`: the set that the handle
-// keeps for the stream, or null where it has none left or the stream's state
-// cannot be read (the launch itself then reports what is wrong).
+// keeps for the stream, or null where it has none left, the streams of a capture
+// cannot be told apart, or the stream's state cannot be read (the launch itself
+// then reports what is wrong).
 int32_t* claim_counters(rgg_handle* h, cudaStream_t stream) {
     unsigned long long id = 0, capture = 0;
     cudaStreamCaptureStatus state = cudaStreamCaptureStatusNone;
@@ -608,7 +609,9 @@ int32_t* claim_counters(rgg_handle* h, cudaStream_t stream) {
         if (cudaStreamGetId(stream, &id) != cudaSuccess) return nullptr;
         capture = 0;
     } else {
-        id = reinterpret_cast<uintptr_t>(stream);  // cudaStreamGetId would end the capture
+        // cudaStreamGetId would end the capture; one handle stands for every thread's own default stream
+        if (stream == cudaStreamPerThread) return nullptr;
+        id = reinterpret_cast<uintptr_t>(stream);
     }
     const int set = h->sets.set_of(id, capture);
     return set < 0 ? nullptr : h->d_status + kCountersAt / 4 + set * rgg::kCounterSetWords;

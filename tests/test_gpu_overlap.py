@@ -2,6 +2,7 @@
 handle: each has tile counters of its own, so every tile of every call is computed once, as in calls that follow each
 other.  And a handle whose counters are all taken."""
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -162,3 +163,43 @@ def test_calls_beside_a_capture():
     assert torch.equal(got[0], want[0][0])
     for o in eager:
         assert torch.equal(o[0], want[1][0])
+
+
+def test_per_thread_default_streams():
+    # one handle stands for the default stream of each thread: its calls run beside those of other threads
+    per_thread = torch.cuda.ExternalStream(2)
+    cases = [_case(0), _case(1)]
+    want = [_outs("dgrad", c) for c in cases]
+    for c, w in zip(cases, want):
+        _call("dgrad", c, w, check=True)
+    got = [[_outs("dgrad", c) for _ in range(20)] for c in cases]
+    torch.cuda.synchronize()
+    failures = []
+
+    def work(i):
+        try:
+            torch.cuda.set_device(0)
+            for outs in got[i]:
+                _call("dgrad", cases[i], outs, stream=per_thread)
+            per_thread.synchronize()
+        except Exception as e:  # shown by the test's own thread
+            failures.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures
+    assert rgg.rgg_query_status(0) == rgg.RGG_OK
+    for side, w in zip(got, want):
+        for outs in side:
+            assert torch.equal(outs[0], w[0])
+    # and captured
+    out, graph = _outs("dgrad", cases[0]), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=per_thread):
+        _call("dgrad", cases[0], out)
+    out[0].fill_(7)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want[0][0])

@@ -575,6 +575,134 @@ rgg_status rgg_grouped_gemm_swiglu_mxfp4(rgg_handle* h, const void* x_codes, con
                                          void* H, int E, int64_t M_tot, int K, int N, void* stream,
                                          const rgg_options* opt);
 
+/*
+ * The router of a mixture of experts: for each of T tokens the k largest of its E
+ * logits, largest first, ties to the lower expert, and their weights.  With l the
+ * logits and C the choices,
+ *     s_i = exp(l_i) / sum over all experts of exp(l_j),  or 1 / (1 + exp(-l_i)) with RGG_ROUTE_SIGMOID,
+ *     w_i = scale * s_i,  or scale * s_i / (sum over C of s_j + 1e-20) with RGG_ROUTE_RENORMALIZE.
+ * A logit of -inf is a masked expert, never chosen: choices that a token has too few
+ * experts for are expert -1 with weight 0.  NaN is ordered above Inf, so that it shows
+ * in the weights.
+ *
+ * logits: [T, E] of type `dtype` (RGG_BF16, RGG_FP32, RGG_FP16); experts: int32
+ * [T, k]; weights: fp32 [T, k].  1 <= k <= E; k <= 32 and E <= 4096, else
+ * RGG_ERR_UNSUPPORTED.  Sums in fp32, in an order that the sizes alone decide.
+ *
+ * rgg_route_topk_backward: the gradient by the logits, dlogits [T, E] of their type
+ * (every element is written), from dweights, fp32 [T, k]; s and w are computed again
+ * from the logits.  Choices of a negative expert have no gradient; one of E or above
+ * is treated so too and recorded as RGG_ERR_BAD_ROW_INDEX.  An expert that a row
+ * names twice gets both gradients.
+ *
+ * T may be 0.  Asynchronous on `stream`; nothing is allocated; can be captured in a
+ * graph.
+ */
+#define RGG_ROUTE_SIGMOID 1
+#define RGG_ROUTE_RENORMALIZE 2
+rgg_status rgg_route_topk(rgg_handle* h, const void* logits, int dtype, int64_t T, int E, int k, int flags, float scale,
+                          int32_t* experts, float* weights, void* stream);
+rgg_status rgg_route_topk_backward(rgg_handle* h, const void* logits, int dtype, const int32_t* experts,
+                                   const float* dweights, void* dlogits, int64_t T, int E, int k, int flags, float scale,
+                                   void* stream);
+
+/*
+ * rgg_sort_by_expert -- the choices of T tokens sorted by expert, stably: an expert's
+ * rows are in the order of the tokens, and of a token's choices.
+ *
+ * experts: int32 [T, k], -1 (or any negative number) for a choice that goes nowhere;
+ * numbers of E or above are treated so too and recorded as RGG_ERR_BAD_ROW_INDEX.
+ * group_offsets: int32 [E + 1], what the grouped products read.  row_index: int32
+ * [T k], the token of each sorted row, as the gather products read it, and -1
+ * behind the last row.  position: int32 [T, k], the row of each choice, -1 for those
+ * that go nowhere.  T k < 2^31, E <= 4096 (else RGG_ERR_UNSUPPORTED).
+ *
+ * workspace: device memory of at least rgg_sort_by_expert_workspace(T k, E) bytes,
+ * 4-byte aligned, not shared by calls that may overlap; NULL where that is 0.  T may be 0.
+ */
+int64_t rgg_sort_by_expert_workspace(int64_t n, int E);
+rgg_status rgg_sort_by_expert(rgg_handle* h, const int32_t* experts, int64_t T, int k, int E, int32_t* group_offsets,
+                              int32_t* row_index, int32_t* position, void* workspace, int64_t workspace_bytes,
+                              void* stream);
+
+/*
+ * Rows of tokens to rows of experts and back, by rgg_sort_by_expert's positions:
+ *     rgg_dispatch           out[position[t, j]] = X[t]
+ *     rgg_combine            out[t] = sum over j of weights[t, j] * Y[position[t, j]]
+ *     rgg_combine_backward   dY[position[t, j]] = weights[t, j] * dout[t]
+ *                            dweights[t, j] = sum over columns of dout[t] * Y[position[t, j]]
+ *
+ * The gradient of rgg_dispatch is rgg_combine without weights (NULL: all 1).
+ * X: [T] rows of row_bytes bytes of any type; Y and dY: bf16 [rows, N]; out of
+ * rgg_combine and dout: bf16 [T, N]; weights and dweights: fp32 [T, k].  Sums in
+ * fp32, over a token's choices in their order, rounded once to bf16; equal calls
+ * give equal bits.  A choice at position -1 (or any negative number) adds nothing and
+ * its dweight is 0; positions of `rows` or above are treated so too and recorded as
+ * RGG_ERR_BAD_ROW_INDEX.  Rows of no choice are left as they were.  Two choices must
+ * not share a row of what a call writes.  dY or dweights may be NULL.
+ *
+ * T, rows, T k and N below 2^31; T and rows may be 0.  Pointers aligned to their
+ * elements (wider loads are used where 16, 8 or 4 bytes divide them and the rows).
+ * What is written must not overlap what is read.
+ */
+rgg_status rgg_dispatch(rgg_handle* h, const void* X, const int32_t* position, int64_t T, int k, int64_t rows,
+                        int64_t row_bytes, void* out, void* stream);
+rgg_status rgg_combine(rgg_handle* h, const void* Y, const int32_t* position, const float* weights, int64_t T, int k,
+                       int64_t rows, int64_t N, void* out, void* stream);
+rgg_status rgg_combine_backward(rgg_handle* h, const void* dout, const void* Y, const int32_t* position,
+                                const float* weights, int64_t T, int k, int64_t rows, int64_t N, void* dY,
+                                float* dweights, void* stream);
+
+/*
+ * 8-bit operands with a scale per block of 128: E4M3 codes ("E4M3FN"), K contiguous,
+ * and fp32 scales; a value is code * scale.
+ *   activations  codes [rows, K], scales [rows, ceil(K / 128)]: one per row and 128 of K
+ *   weights      codes [E, N, K], scales [E, ceil(N / 128), ceil(K / 128)]: one per 128 x 128
+ * The quantisers (bf16 in): with a = max(max |x|, 2^-100) of a block, the scale is
+ * a / 448 and a code is 448 x / a rounded to nearest even.  A block that holds Inf or
+ * NaN comes back as NaN, and so do the products of its rows.
+ *
+ * rgg_fp8_block_quantize with `position` (int32 [T, k], from rgg_sort_by_expert) writes
+ * a token's codes and scales to the rows of its choices, [rows, K]: rgg_dispatch on the
+ * way, with its rules.  With NULL, row t goes to row t, and rows must be T.  Weights come in as bf16
+ * [E, K, N], as the bf16 products have them.  The dequantisers give bf16 values,
+ * rounded once: [rows, K], [E, N, K].
+ *
+ * K a multiple of 16, N of 8; pointers 16-byte aligned (scales and position 4).
+ * Asynchronous on `stream`; nothing is allocated.
+ */
+rgg_status rgg_fp8_block_quantize(rgg_handle* h, const void* X, const int32_t* position, int64_t T, int k, int64_t rows,
+                                  int K, void* codes, float* scales, void* stream);
+rgg_status rgg_fp8_block_dequantize(rgg_handle* h, const void* codes, const float* scales, void* X, int64_t rows, int K,
+                                    void* stream);
+rgg_status rgg_fp8_block_quantize_weights(rgg_handle* h, const void* W, void* codes, float* scales, int E, int K, int N,
+                                          void* stream);
+rgg_status rgg_fp8_block_dequantize_weights(rgg_handle* h, const void* codes, const float* scales, void* W, int E, int K,
+                                            int N, void* stream);
+
+/*
+ * rgg_grouped_gemm_fp8_block -- the grouped product of such operands:
+ *     Y[i, n] = sum over k of x[i, k] * w[e, n, k]      for every row i of expert e,
+ * the products of a block of 128 of K summed on the tensor core, the blocks in fp32, each
+ * times its two scales, the result rounded once to bf16: Y [M_tot, N].
+ * rgg_grouped_gemm_swiglu_fp8_block is the gate-up projection: the weight has 2N
+ * columns, gate first, and H = silu(g) * u leaves as activations of this form, codes
+ * [M_tot, N] and scales [M_tot, N / 128], quantised from fp32 by the rule above; N
+ * must be a multiple of 128 (fill other widths up with zero columns of gate and up).
+ *
+ * Rows of no expert are never written.  Of `opt` they read bm (256: CTA pairs, 128:
+ * single CTAs, 0: by the sizes), stages, max_ctas (at least 2 for pairs), timeout_ns
+ * and debug_flags.  K a multiple of 16, N of 8; pointers 16-byte aligned (scales 4).
+ * Other arguments, errors and the stream contract as for rgg_grouped_gemm.
+ */
+rgg_status rgg_grouped_gemm_fp8_block(rgg_handle* h, const void* x_codes, const float* x_scales, const void* w_codes,
+                                      const float* w_scales, const int32_t* group_offsets, void* Y, int E,
+                                      int64_t M_tot, int K, int N, void* stream, const rgg_options* opt);
+rgg_status rgg_grouped_gemm_swiglu_fp8_block(rgg_handle* h, const void* x_codes, const float* x_scales,
+                                             const void* w13_codes, const float* w13_scales,
+                                             const int32_t* group_offsets, void* h_codes, float* h_scales, int E,
+                                             int64_t M_tot, int K, int N, void* stream, const rgg_options* opt);
+
 #ifdef __cplusplus
 }
 #endif

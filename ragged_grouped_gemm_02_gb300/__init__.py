@@ -21,7 +21,11 @@ __all__ = [
     "rgg_grouped_gemm_swiglu_gather", "rgg_grouped_gemm_dgrad", "rgg_grouped_gemm_wgrad",
     "rgg_grouped_gemm_swiglu_backward", "rgg_clip_grad_norm",
     "rgg_mxfp4_quantize", "rgg_mxfp4_dequantize", "rgg_mxfp4_quantize_weights", "rgg_mxfp4_dequantize_weights",
-    "rgg_grouped_gemm_mxfp4", "rgg_grouped_gemm_swiglu_mxfp4", "rgg_grouped_gemm_noalloc", "rgg_export_tiles", "rgg_export_walk",
+    "rgg_grouped_gemm_mxfp4", "rgg_grouped_gemm_swiglu_mxfp4",
+    "rgg_route_topk", "rgg_route_topk_backward", "rgg_sort_by_expert", "rgg_dispatch", "rgg_combine",
+    "rgg_combine_backward", "rgg_fp8_block_quantize", "rgg_fp8_block_dequantize", "rgg_fp8_block_quantize_weights",
+    "rgg_fp8_block_dequantize_weights", "rgg_grouped_gemm_fp8_block", "rgg_grouped_gemm_swiglu_fp8_block",
+    "rgg_grouped_gemm_noalloc", "rgg_export_tiles", "rgg_export_walk",
     "rgg_query_status",
     "rgg_plan", "rgg_status_string", "library_path", "load_library", "EXPORTED_SYMBOLS",
     "RGG_OK", "RGG_ERR_INVALID_ARG", "RGG_ERR_UNSUPPORTED", "RGG_ERR_CUDA", "RGG_ERR_BAD_OFFSETS",
@@ -54,6 +58,10 @@ EXPORTED_SYMBOLS = (
     "rgg_clip_grad_norm", "rgg_clip_grad_norm_workspace", "rgg_mxfp4_scale_bytes", "rgg_mxfp4_quantize",
     "rgg_mxfp4_dequantize", "rgg_mxfp4_quantize_weights", "rgg_mxfp4_dequantize_weights", "rgg_grouped_gemm_mxfp4",
     "rgg_grouped_gemm_swiglu_mxfp4",
+    "rgg_route_topk", "rgg_route_topk_backward", "rgg_sort_by_expert", "rgg_sort_by_expert_workspace", "rgg_dispatch",
+    "rgg_combine", "rgg_combine_backward", "rgg_fp8_block_quantize", "rgg_fp8_block_dequantize",
+    "rgg_fp8_block_quantize_weights", "rgg_fp8_block_dequantize_weights", "rgg_grouped_gemm_fp8_block",
+    "rgg_grouped_gemm_swiglu_fp8_block",
 )
 
 
@@ -160,6 +168,26 @@ def open_library(path: str) -> ctypes.CDLL:
         getattr(lib, name).restype = I
     lib.rgg_grouped_gemm_swiglu_backward.argtypes = [P, P, P, P, P, P, P, I, I64, I, I, P, ctypes.POINTER(_Options)]
     lib.rgg_grouped_gemm_swiglu_backward.restype = I
+    F = ctypes.c_float
+    lib.rgg_route_topk.argtypes = [P, P, I, I64, I, I, I, F, P, P, P]
+    lib.rgg_route_topk_backward.argtypes = [P, P, I, P, P, P, I64, I, I, I, F, P]
+    lib.rgg_sort_by_expert_workspace.argtypes = [I64, I]
+    lib.rgg_sort_by_expert_workspace.restype = I64
+    lib.rgg_sort_by_expert.argtypes = [P, P, I64, I, I, P, P, P, P, I64, P]
+    lib.rgg_dispatch.argtypes = [P, P, P, I64, I, I64, I64, P, P]
+    lib.rgg_combine.argtypes = [P, P, P, P, I64, I, I64, I64, P, P]
+    lib.rgg_combine_backward.argtypes = [P, P, P, P, P, I64, I, I64, I64, P, P, P]
+    lib.rgg_fp8_block_quantize.argtypes = [P, P, P, I64, I, I64, I, P, P, P]
+    lib.rgg_fp8_block_dequantize.argtypes = [P, P, P, P, I64, I, P]
+    for name in ("rgg_fp8_block_quantize_weights", "rgg_fp8_block_dequantize_weights"):
+        getattr(lib, name).argtypes = [P, P, P, P, I, I, I, P]
+    lib.rgg_grouped_gemm_fp8_block.argtypes = [P, P, P, P, P, P, P, I, I64, I, I, P, ctypes.POINTER(_Options)]
+    lib.rgg_grouped_gemm_swiglu_fp8_block.argtypes = [P, P, P, P, P, P, P, P, I, I64, I, I, P, ctypes.POINTER(_Options)]
+    for name in ("rgg_route_topk", "rgg_route_topk_backward", "rgg_sort_by_expert", "rgg_dispatch", "rgg_combine",
+                 "rgg_combine_backward", "rgg_fp8_block_quantize", "rgg_fp8_block_dequantize",
+                 "rgg_fp8_block_quantize_weights", "rgg_fp8_block_dequantize_weights", "rgg_grouped_gemm_fp8_block",
+                 "rgg_grouped_gemm_swiglu_fp8_block"):
+        getattr(lib, name).restype = I
     lib.rgg_grouped_gemm_noalloc.argtypes = [P, P, P, P, I, I64, I, I, P, P]
     lib.rgg_grouped_gemm_noalloc.restype = I
     return lib
@@ -836,6 +864,410 @@ def rgg_grouped_gemm_swiglu_mxfp4(x_codes, x_scales, w13_codes, w13_scales, grou
     CUDA [M_tot, N]."""
     return _mxfp4_call("rgg_grouped_gemm_swiglu_mxfp4", x_codes, x_scales, w13_codes, w13_scales, group_offsets, H,
                        True, bn, stages, max_ctas, timeout_ns, debug_flags, stream, check)
+
+
+_ROUTE_FLAGS = {("softmax", False): 0, ("sigmoid", False): 1, ("softmax", True): 2, ("sigmoid", True): 3}
+
+
+def _route_flags(score, renormalize):
+    flags = _ROUTE_FLAGS.get((score, bool(renormalize)))
+    if flags is None:
+        raise ValueError('score must be "softmax" or "sigmoid", not %r' % (score,))
+    return flags
+
+
+def _logits(logits):
+    """Refuses anything but contiguous CUDA logits [T, E] of a type the router takes; returns the type's code."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    dtype = logits.dtype
+    code = 1 if dtype is torch.float32 else 0 if dtype is torch.bfloat16 else 2 if dtype is torch.float16 else None
+    if code is None:
+        raise TypeError("logits must be bf16, fp16 or fp32, not %s" % dtype)
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if not logits.is_contiguous():
+        raise ValueError("logits must be contiguous")
+    return code
+
+
+def rgg_route_topk(logits, k, experts=None, weights=None, *, score="softmax", renormalize=True, scale=1.0, stream=None):
+    """The k largest of each token's E logits, largest first (ties to the lower
+    expert), and the choices' weights.
+
+    logits: bf16, fp16 or fp32 CUDA [T, E]; -inf masks an expert, and choices
+    that a token has too few experts for are expert -1 with weight 0.  score:
+    "softmax" over all experts or "sigmoid" of each logit; ``renormalize``
+    divides a token's weights by their sum (+ 1e-20); ``scale`` multiplies them.
+    Returns ``(experts, weights)``: int32 [T, k] and fp32 [T, k].  k <= 32,
+    E <= 4096."""
+    import torch
+    code = _logits(logits)
+    flags = _route_flags(score, renormalize)
+    T, E = logits.shape
+    k = int(k)
+    if not 1 <= k <= E:
+        raise ValueError("k must be between 1 and E = %d, not %d" % (E, k))
+    dev = logits.device
+    if experts is None:
+        experts = _empty((T, k), torch.int32, dev, stream)
+    else:
+        _operand("experts", experts, torch.int32, (T, k), dev)
+    if weights is None:
+        weights = _empty((T, k), torch.float32, dev, stream)
+    else:
+        _operand("weights", weights, torch.float32, (T, k), dev)
+    device = dev.index
+    s = load_library().rgg_route_topk(_handle(device), logits.data_ptr(), code, T, E, k, flags, scale, experts.data_ptr(),
+                                      weights.data_ptr(), _raw_stream(stream, device))
+    if s != RGG_OK:
+        _raise(s, "rgg_route_topk")
+    return experts, weights
+
+
+def rgg_route_topk_backward(logits, experts, dweights, dlogits=None, *, score="softmax", renormalize=True, scale=1.0,
+                            stream=None, check=False):
+    """The gradient of ``rgg_route_topk``'s weights by the logits (of their type,
+    [T, E]), from dweights, fp32 CUDA [T, k]; the other arguments as that call
+    had them, experts as it returned them."""
+    import torch
+    code = _logits(logits)
+    flags = _route_flags(score, renormalize)
+    T, E = logits.shape
+    if experts.dim() != 2 or not 1 <= experts.shape[1] <= E:
+        raise ValueError("experts must be [T, k] with k between 1 and E = %d" % E)
+    k = experts.shape[1]
+    dev = logits.device
+    _operand("experts", experts, torch.int32, (T, k), dev)
+    _operand("dweights", dweights, torch.float32, (T, k), dev)
+    if dlogits is None:
+        dlogits = _empty((T, E), logits.dtype, dev, stream)
+    else:
+        _operand("dlogits", dlogits, logits.dtype, (T, E), dev)
+    device = dev.index
+    st = _raw_stream(stream, device)
+    s = load_library().rgg_route_topk_backward(_handle(device), logits.data_ptr(), code, experts.data_ptr(),
+                                               dweights.data_ptr(), dlogits.data_ptr(), T, E, k, flags, scale, st)
+    _finish("rgg_route_topk_backward", s, device, st, check)
+    return dlogits
+
+
+def rgg_sort_by_expert(experts, E, *, stream=None, check=False):
+    """The choices sorted by expert, stably.
+
+    experts: int32 CUDA [T, k], negative for a choice that goes nowhere.  Returns
+    ``(group_offsets, row_index, position)``: int32 [E+1], the offsets that the
+    grouped products read; int32 [T * k], the token of each sorted row (what
+    the gather products read; -1 behind the last row); int32 [T, k], the row of
+    each choice (-1: none).  Numbers of E or above go nowhere and are reported
+    through the device status (``check=True`` raises)."""
+    import torch
+    if experts.dim() != 2 or experts.shape[1] < 1:
+        raise ValueError("experts must be [T, k]")
+    T, k = experts.shape
+    E = int(E)
+    dev = experts.device
+    _operand("experts", experts, torch.int32, (T, k), dev)
+    n = T * k
+    lib = load_library()
+    offsets = _empty((E + 1 if E > 0 else 0,), torch.int32, dev, stream)
+    row_index = _empty((n,), torch.int32, dev, stream)
+    position = _empty((T, k), torch.int32, dev, stream)
+    bytes_ = lib.rgg_sort_by_expert_workspace(n, E)
+    workspace = _empty((bytes_ // 4,), torch.int32, dev, stream) if bytes_ > 0 else None
+    device = dev.index
+    st = _raw_stream(stream, device)
+    s = lib.rgg_sort_by_expert(_handle(device), experts.data_ptr(), T, k, E, offsets.data_ptr(), row_index.data_ptr(),
+                               position.data_ptr(), workspace.data_ptr() if workspace is not None else None, bytes_, st)
+    _finish("rgg_sort_by_expert", s, device, st, check)
+    return offsets, row_index, position
+
+
+def _positions(position, T, dev):
+    import torch
+    if position.dim() != 2 or position.shape[1] < 1:
+        raise ValueError("position must be [T, k]")
+    _operand("position", position, torch.int32, (T, position.shape[1]), dev)
+    return position.shape[1]
+
+
+def rgg_dispatch(X, position, out=None, *, stream=None, check=False):
+    """Tokens' rows in the order of the experts: out[position[t, j]] = X[t].
+
+    X: CUDA [T, K] of any type; position: int32 CUDA [T, k] from
+    ``rgg_sort_by_expert``; out: optional, [rows, K] of X's type ([T * k, K] when
+    omitted, uninitialised: rows of no choice are never written)."""
+    if X.dim() != 2 or X.shape[1] < 1:
+        raise ValueError("X must be [T, K]")
+    T, K = X.shape
+    dev = X.device
+    _operand("X", X, X.dtype, (T, K), dev)
+    k = _positions(position, T, dev)
+    if out is None:
+        out = _empty((T * k, K), X.dtype, dev, stream)
+    else:
+        if out.dim() != 2:
+            raise ValueError("out must be [rows, K]")
+        _operand("out", out, X.dtype, (out.shape[0], K), dev)
+    device = dev.index
+    st = _raw_stream(stream, device)
+    s = load_library().rgg_dispatch(_handle(device), X.data_ptr(), position.data_ptr(), T, k, out.shape[0],
+                                    K * X.element_size(), out.data_ptr(), st)
+    _finish("rgg_dispatch", s, device, st, check)
+    return out
+
+
+def rgg_combine(Y, position, weights=None, out=None, *, stream=None, check=False):
+    """Experts' rows back to the tokens: out[t] = sum_j weights[t, j] * Y[position[t, j]].
+
+    Y: bf16 CUDA [rows, N]; position: int32 CUDA [T, k]; weights: fp32 CUDA
+    [T, k], or None for all 1 (the gradient of ``rgg_dispatch``); out: optional
+    bf16 [T, N].  Choices without a row (position -1) add nothing."""
+    import torch
+    if Y.dim() != 2 or Y.shape[1] < 1 or position.dim() != 2:
+        raise ValueError("Y must be [rows, N] and position [T, k]")
+    rows, N = Y.shape
+    T = position.shape[0]
+    dev = Y.device
+    _operand("Y", Y, torch.bfloat16, (rows, N), dev)
+    k = _positions(position, T, dev)
+    if weights is not None:
+        _operand("weights", weights, torch.float32, (T, k), dev)
+    if out is None:
+        out = _empty((T, N), torch.bfloat16, dev, stream)
+    else:
+        _operand("out", out, torch.bfloat16, (T, N), dev)
+    device = dev.index
+    st = _raw_stream(stream, device)
+    s = load_library().rgg_combine(_handle(device), Y.data_ptr(), position.data_ptr(),
+                                   weights.data_ptr() if weights is not None else None, T, k, rows, N, out.data_ptr(), st)
+    _finish("rgg_combine", s, device, st, check)
+    return out
+
+
+def rgg_combine_backward(dout, Y, position, weights, dY=None, dweights=None, *, stream=None, check=False):
+    """The gradients of ``rgg_combine`` with weights: ``(dY, dweights)``,
+    dY[position[t, j]] = weights[t, j] * dout[t], bf16 [rows, N] (rows of no
+    choice are never written), and dweights[t, j] = dout[t] . Y[position[t, j]],
+    fp32 [T, k].  Both optional arguments; ``False`` leaves one out (None comes
+    back in its place)."""
+    import torch
+    if Y.dim() != 2 or Y.shape[1] < 1 or dout.dim() != 2:
+        raise ValueError("dout must be [T, N] and Y [rows, N]")
+    rows, N = Y.shape
+    T = dout.shape[0]
+    dev = Y.device
+    _operand("dout", dout, torch.bfloat16, (T, N), dev)
+    _operand("Y", Y, torch.bfloat16, (rows, N), dev)
+    k = _positions(position, T, dev)
+    _operand("weights", weights, torch.float32, (T, k), dev)
+    if dY is None:
+        dY = _empty((rows, N), torch.bfloat16, dev, stream)
+    elif dY is False:
+        dY = None
+    else:
+        _operand("dY", dY, torch.bfloat16, (rows, N), dev)
+    if dweights is None:
+        dweights = _empty((T, k), torch.float32, dev, stream)
+    elif dweights is False:
+        dweights = None
+    else:
+        _operand("dweights", dweights, torch.float32, (T, k), dev)
+    device = dev.index
+    st = _raw_stream(stream, device)
+    s = load_library().rgg_combine_backward(
+        _handle(device), dout.data_ptr(), Y.data_ptr(), position.data_ptr(), weights.data_ptr(), T, k, rows, N,
+        dY.data_ptr() if dY is not None else None, dweights.data_ptr() if dweights is not None else None, st)
+    _finish("rgg_combine_backward", s, device, st, check)
+    return dY, dweights
+
+
+def rgg_fp8_block_quantize(X, position=None, codes=None, scales=None, *, stream=None, check=False):
+    """8-bit form of activations: E4M3 codes with one fp32 scale per 128 values of a row.
+
+    X: bf16 CUDA [T, K], K a multiple of 16.  Returns ``(codes, scales)``:
+    float8_e4m3fn [rows, K] and fp32 [rows, ceil(K / 128)].  With ``position``
+    (int32 CUDA [T, k], from ``rgg_sort_by_expert``) a token is written to the
+    rows of its choices, T * k rows when the results are omitted; rows of no
+    choice are never written.  Without, row t goes to row t."""
+    import torch
+    if X.dim() != 2:
+        raise ValueError("X must be [T, K]")
+    T, K = X.shape
+    dev = X.device
+    _operand("X", X, torch.bfloat16, (T, K), dev)
+    if K < 16 or K % 16:
+        raise ValueError("K must be a multiple of 16, not %d" % K)
+    k = 1 if position is None else _positions(position, T, dev)
+    rows = T * k
+    given = codes if codes is not None else scales
+    if given is not None:
+        if given.dim() != 2:
+            raise ValueError("codes must be [rows, K] and scales [rows, ceil(K / 128)]")
+        rows = given.shape[0]
+        if position is None and rows != T:
+            raise ValueError("codes and scales must have T = %d rows, not %d" % (T, rows))
+    blocks = -(-K // 128)
+    if codes is None:
+        codes = _empty((rows, K), torch.float8_e4m3fn, dev, stream)
+    else:
+        _operand("codes", codes, torch.float8_e4m3fn, (rows, K), dev)
+    if scales is None:
+        scales = _empty((rows, blocks), torch.float32, dev, stream)
+    else:
+        _operand("scales", scales, torch.float32, (rows, blocks), dev)
+    device = dev.index
+    st = _raw_stream(stream, device)
+    s = load_library().rgg_fp8_block_quantize(_handle(device), X.data_ptr(),
+                                              position.data_ptr() if position is not None else None, T, k, rows, K,
+                                              codes.data_ptr(), scales.data_ptr(), st)
+    _finish("rgg_fp8_block_quantize", s, device, st, check)
+    return codes, scales
+
+
+def rgg_fp8_block_dequantize(codes, scales, X=None, *, stream=None):
+    """The values of ``rgg_fp8_block_quantize``'s result, bf16 [rows, K], each rounded once."""
+    import torch
+    if codes.dim() != 2:
+        raise ValueError("codes must be [rows, K]")
+    rows, K = codes.shape
+    dev = codes.device
+    _operand("codes", codes, torch.float8_e4m3fn, (rows, K), dev)
+    _operand("scales", scales, torch.float32, (rows, -(-K // 128)), dev)
+    if X is None:
+        X = _empty((rows, K), torch.bfloat16, dev, stream)
+    else:
+        _operand("X", X, torch.bfloat16, (rows, K), dev)
+    device = dev.index
+    s = load_library().rgg_fp8_block_dequantize(_handle(device), codes.data_ptr(), scales.data_ptr(), X.data_ptr(), rows,
+                                                K, _raw_stream(stream, device))
+    if s != RGG_OK:
+        _raise(s, "rgg_fp8_block_dequantize")
+    return X
+
+
+def _fp_weight_scale_shape(E, N, K):
+    return (E, -(-N // 128), -(-K // 128))
+
+
+def rgg_fp8_block_quantize_weights(W, codes=None, scales=None, *, stream=None):
+    """8-bit form of expert weights, laid out once: W bf16 CUDA [E, K, N], one scale
+    per 128 x 128 values.  Returns ``(codes, scales)``: float8_e4m3fn [E, N, K] and
+    fp32 [E, ceil(N / 128), ceil(K / 128)]."""
+    import torch
+    if W.dim() != 3:
+        raise ValueError("W must be [E, K, N]")
+    E, K, N = W.shape
+    dev = W.device
+    _operand("W", W, torch.bfloat16, (E, K, N), dev)
+    if codes is None:
+        codes = _empty((E, N, K), torch.float8_e4m3fn, dev, stream)
+    else:
+        _operand("codes", codes, torch.float8_e4m3fn, (E, N, K), dev)
+    if scales is None:
+        scales = _empty(_fp_weight_scale_shape(E, N, K), torch.float32, dev, stream)
+    else:
+        _operand("scales", scales, torch.float32, _fp_weight_scale_shape(E, N, K), dev)
+    device = dev.index
+    s = load_library().rgg_fp8_block_quantize_weights(_handle(device), W.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                                      E, K, N, _raw_stream(stream, device))
+    if s != RGG_OK:
+        _raise(s, "rgg_fp8_block_quantize_weights")
+    return codes, scales
+
+
+def rgg_fp8_block_dequantize_weights(codes, scales, W=None, *, stream=None):
+    """The values of ``rgg_fp8_block_quantize_weights``'s result, bf16 [E, N, K], each rounded once."""
+    import torch
+    if codes.dim() != 3:
+        raise ValueError("codes must be [E, N, K]")
+    E, N, K = codes.shape
+    dev = codes.device
+    _operand("codes", codes, torch.float8_e4m3fn, (E, N, K), dev)
+    _operand("scales", scales, torch.float32, _fp_weight_scale_shape(E, N, K), dev)
+    if W is None:
+        W = _empty((E, N, K), torch.bfloat16, dev, stream)
+    else:
+        _operand("W", W, torch.bfloat16, (E, N, K), dev)
+    device = dev.index
+    s = load_library().rgg_fp8_block_dequantize_weights(_handle(device), codes.data_ptr(), scales.data_ptr(),
+                                                        W.data_ptr(), E, K, N, _raw_stream(stream, device))
+    if s != RGG_OK:
+        _raise(s, "rgg_fp8_block_dequantize_weights")
+    return W
+
+
+def _fp8_block_operands(x_codes, x_scales, w_codes, w_scales, group_offsets):
+    import torch
+    if x_codes.dim() != 2 or w_codes.dim() != 3:
+        raise ValueError("codes must be [M_tot, K] for the activations and [E, N, K] for the weights")
+    M_tot, K = x_codes.shape
+    E, cols = w_codes.shape[:2]
+    dev = x_codes.device
+    fp8, fp32 = torch.float8_e4m3fn, torch.float32
+    _operand("x_codes", x_codes, fp8, (M_tot, K), dev)
+    _operand("x_scales", x_scales, fp32, (M_tot, -(-K // 128)), dev)
+    _operand("w_codes", w_codes, fp8, (E, cols, K), dev)
+    _operand("w_scales", w_scales, fp32, _fp_weight_scale_shape(E, cols, K), dev)
+    _operand("group_offsets", group_offsets, torch.int32, (E + 1,), dev)
+    return M_tot, K, E, cols, dev
+
+
+def rgg_grouped_gemm_fp8_block(x_codes, x_scales, w_codes, w_scales, group_offsets, Y=None, *, bm=0, stages=0, max_ctas=0,
+                               timeout_ns=0, debug_flags=0, stream=None, check=False):
+    """Y_e = X_e . W_e for every expert with 8-bit operands and a scale per block of
+    128, as ``rgg_fp8_block_quantize`` and ``rgg_fp8_block_quantize_weights`` leave
+    them; Y: optional bf16 CUDA [M_tot, N].  bm: 256 (256 x 256 tiles on CTA
+    pairs), 128 (single CTAs) or 0, by the sizes."""
+    import torch
+    M_tot, K, E, N, dev = _fp8_block_operands(x_codes, x_scales, w_codes, w_scales, group_offsets)
+    if Y is None:
+        Y = _empty((M_tot, N), torch.bfloat16, dev, stream)
+    else:
+        _operand("Y", Y, torch.bfloat16, (M_tot, N), dev)
+    device = dev.index
+    opt = None
+    if bm or stages or max_ctas or timeout_ns or debug_flags:
+        opt, _ = _options(bm, 0, stages, max_ctas, timeout_ns, None, debug_flags)
+    st = _raw_stream(stream, device)
+    s = load_library().rgg_grouped_gemm_fp8_block(
+        _handle(device), x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+        group_offsets.data_ptr(), Y.data_ptr(), E, M_tot, K, N, st, opt)
+    _finish("rgg_grouped_gemm_fp8_block", s, device, st, check)
+    return Y
+
+
+def rgg_grouped_gemm_swiglu_fp8_block(x_codes, x_scales, w13_codes, w13_scales, group_offsets, h_codes=None, h_scales=None,
+                                      *, bm=0, stages=0, max_ctas=0, timeout_ns=0, debug_flags=0, stream=None,
+                                      check=False):
+    """H = silu(gate) * up for every expert with 8-bit operands, itself in 8 bits:
+    ``(h_codes, h_scales)``, float8_e4m3fn [M_tot, N] and fp32 [M_tot, N / 128], what
+    the down product reads.  w13_codes hold the 2N columns of W13 (gate first), N a
+    multiple of 128 (``expert_layer`` fills other widths up with zero columns)."""
+    import torch
+    M_tot, K, E, cols, dev = _fp8_block_operands(x_codes, x_scales, w13_codes, w13_scales, group_offsets)
+    if cols % 256:
+        raise ValueError("w13_codes must have 2N columns, N a multiple of 128, not %d" % cols)
+    N = cols // 2
+    if h_codes is None:
+        h_codes = _empty((M_tot, N), torch.float8_e4m3fn, dev, stream)
+    else:
+        _operand("h_codes", h_codes, torch.float8_e4m3fn, (M_tot, N), dev)
+    if h_scales is None:
+        h_scales = _empty((M_tot, N // 128), torch.float32, dev, stream)
+    else:
+        _operand("h_scales", h_scales, torch.float32, (M_tot, N // 128), dev)
+    device = dev.index
+    opt = None
+    if bm or stages or max_ctas or timeout_ns or debug_flags:
+        opt, _ = _options(bm, 0, stages, max_ctas, timeout_ns, None, debug_flags)
+    st = _raw_stream(stream, device)
+    s = load_library().rgg_grouped_gemm_swiglu_fp8_block(
+        _handle(device), x_codes.data_ptr(), x_scales.data_ptr(), w13_codes.data_ptr(), w13_scales.data_ptr(),
+        group_offsets.data_ptr(), h_codes.data_ptr(), h_scales.data_ptr(), E, M_tot, K, N, st, opt)
+    _finish("rgg_grouped_gemm_swiglu_fp8_block", s, device, st, check)
+    return h_codes, h_scales
 
 
 def rgg_export_tiles(group_offsets, M_tot: int, N: int, bm: int, bn: int, cap: int | None = None, stream=None):

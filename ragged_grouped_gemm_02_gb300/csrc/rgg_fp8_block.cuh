@@ -1,0 +1,470 @@
+// rgg_fp8_block.cuh -- the grouped product of 8-bit operands with a scale per
+// block of 128: for every row i of expert e and every column n,
+//
+//     Y[i, n] = sum over blocks b of  sx[i, b] sw[e, n / 128, b] sum over k in b of x[i, k] w[e, n, k],
+//
+// x and w E4M3 codes, the inner sums in fp32 on the tensor core (tcgen05.mma
+// kind::f8f6f4, K = 32 an instruction), the outer one in fp32 registers; Y bf16,
+// rounded once.  For the gate-up projection H = silu(g) u leaves as 8-bit codes with
+// a scale per row and 128 columns, which the down product reads.
+//
+// The scales are arbitrary fp32 numbers, so the tensor core cannot apply them: each
+// stage of 128 of K is a product of its own, into one of two accumulators in TMEM,
+// and the epilogue warps add it, times its two scales, to the sums that they hold in
+// registers while the next stage is multiplied into the other.
+//
+// Two tile shapes, one kernel.  A CTA pair (cta_group::2) computes 256 x 256: each CTA
+// holds 128 rows of x and half of the W rows.  A single CTA computes 128 x 128, or for
+// gate-up 128 x 256 (128 columns of H, whose scale needs them all).
+//
+// Persistent over the flat tile list; warp 0 copies, warp 1 issues, warps 2-17 add up
+// and write: four for each 32 TMEM lanes, with a quarter of the columns each, so
+// that a thread holds at most 64 sums, and each warp's waits run under the others' work.
+// A stage holds 128 bytes a row, one swizzle row, K-major on both sides.
+#pragma once
+
+#include "rgg_fp8_block.h"
+#include "rgg_gemm_2cta.cuh"
+
+namespace rgg {
+
+struct FpArgs {
+    const int32_t* offsets;
+    const float* sx;       // [M_tot, K blocks]
+    const float* sw;       // [E, row blocks of W, K blocks]
+    __nv_bfloat16* Y;      // plain
+    uint8_t* codes;        // gate-up: H's codes and scales
+    float* scales;
+    int32_t* status;
+    int64_t M_tot;
+    int32_t E, K, N;       // N: output columns
+    int32_t n_tiles_n;
+    int32_t stages;
+    int32_t y_vec32;
+    int32_t n_major;       // walk an expert's tiles N tile by N tile
+    int32_t debug_flags;
+    uint64_t timeout_ns;
+};
+
+// Tensor maps: codes in boxes of 128 bytes by the named number of rows.
+struct FpMaps {
+    CUtensorMap x128, x32, w128, w64;
+};
+
+constexpr int kFpEpiWarps = 16;
+constexpr int kFpThreads = 64 + 32 * kFpEpiWarps;
+constexpr uint32_t kFpTile = 128u * 128u;  // bytes of 128 rows of a stage
+
+// Columns that a tile multiplies.
+template <bool kPair, bool kGateUp>
+__host__ __device__ constexpr int fp_tile_cols() { return (kPair || kGateUp) ? 256 : 128; }
+// Bytes of W in a stage of a CTA.
+template <bool kPair, bool kGateUp>
+__host__ __device__ constexpr uint32_t fp_w_bytes() { return (!kPair && kGateUp) ? 2 * kFpTile : kFpTile; }
+
+struct FpSmem {
+    uint32_t b_off, top_off, bar_off, misc_off, off_off, pre_off, total;
+};
+
+__host__ __device__ inline FpSmem fp_smem(int stages, int E, uint32_t w_bytes, bool gate_up) {
+    FpSmem p;
+    const uint32_t ex = 4u * static_cast<uint32_t>(E + 1);
+    p.b_off = stages * kFpTile;
+    p.top_off = p.b_off + stages * w_bytes;               // gate-up: [2][4][128] magnitudes
+    p.bar_off = p.top_off + (gate_up ? 4096u : 0u);       // full[S], empty[S], acc_full[2], acc_empty[2], top[4], drain
+    p.misc_off = p.bar_off + 8u * (2u * stages + 9u);
+    p.misc_off = (p.misc_off + 15u) & ~15u;
+    p.off_off = p.misc_off + 16u;
+    p.pre_off = p.off_off + ex;
+    p.total = p.pre_off + ex;
+    return p;
+}
+
+template <bool kPair>
+__device__ __forceinline__ void mma_e4m3_if(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+            : "memory");
+    else
+        mma_single_if<true>(lead, d_tmem, a_desc, b_desc, idesc, accumulate);
+}
+
+// Each thread reads its TMEM lane's 16 columns from taddr's on.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+template <bool kPair, bool kGateUp>
+__device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs& args) {
+    constexpr int BM = kPair ? 256 : 128;
+    constexpr int BN = fp_tile_cols<kPair, kGateUp>();
+    constexpr int kOutN = kGateUp ? BN / 2 : BN;
+    constexpr uint32_t kWBytes = fp_w_bytes<kPair, kGateUp>();
+    constexpr int kCols = BN / 4;  // columns whose sums a thread holds; gate-up: half gate, half up
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+
+    const int warp = uniform_warp();
+    const int lane = threadIdx.x & 31;
+    const int E = args.E;
+    const int S = args.stages;
+    const int N = args.N;
+    const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+    const int32_t unit = kPair ? static_cast<int32_t>(cluster_id_x()) : static_cast<int32_t>(blockIdx.x);
+    const int32_t units = kPair ? static_cast<int32_t>(cluster_count_x()) : static_cast<int32_t>(gridDim.x);
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const FpSmem sp = fp_smem(S, E, kWBytes, kGateUp);
+    const uint32_t a0 = base;
+    const uint32_t b0 = base + sp.b_off;
+    const uint32_t bars = base + sp.bar_off;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+    auto accf_bar = [&](int a) { return bars + 8u * (2 * S + a); };
+    auto acce_bar = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
+    auto top_bar = [&](int q) { return bars + 8u * (2 * S + 4 + q); };
+    const uint32_t drain_bar = bars + 8u * (2 * S + 8);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(gbase + sp.misc_off);
+    int32_t* s_off = reinterpret_cast<int32_t*>(gbase + sp.off_off);
+    int32_t* s_pre = reinterpret_cast<int32_t*>(gbase + sp.pre_off);
+
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
+
+    if (!load_and_check_offsets(args.offsets, s_off, E, args.M_tot)) {
+        if (threadIdx.x == 0 && rank == 0) atomicCAS(args.status, 0, kStatusBadOffsets);
+        return;
+    }
+    if (warp == 0) build_tile_prefix_warp(s_off, s_pre, E, BM, args.n_tiles_n);
+    __syncthreads();
+    const int32_t T = s_pre[E];
+    if (unit >= T) return;  // both CTAs of a pair alike
+
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(accf_bar(a), 1);
+            mbar_init(acce_bar(a), (kPair ? 2 : 1) * kFpEpiWarps);
+        }
+        for (int q = 0; q < 4; ++q) mbar_init(top_bar(q), 4);
+        mbar_init(drain_bar, 1);
+        misc[1] = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&maps.x128);
+        tma_prefetch_map(&maps.x32);
+        tma_prefetch_map(&maps.w128);
+    }
+    if (warp == 1) {
+        if constexpr (kPair) {
+            tmem_alloc_pair(smem_addr(&misc[0]), 2 * BN);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_addr(&misc[0]), 2 * BN);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before_sync();
+    if constexpr (kPair) cluster_sync_all();
+    else __syncthreads();
+    tc_fence_after_sync();
+
+    const uint32_t tmem_base = misc[0];
+    volatile uint32_t* abort_flag = &misc[1];
+    const uint32_t peer_flag = kPair ? map_to_rank(smem_addr(&misc[1]), rank ^ 1u) : 0u;
+    // of a whole warp, the same answer in every lane
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        return warp_wait<kPair>(bar, parity, abort_flag, peer_flag, args.status, args.timeout_ns);
+    };
+    const int KB = (args.K + kFpBlock - 1) / kFpBlock;
+    const int64_t cols_w = kGateUp ? 2 * static_cast<int64_t>(N) : N;
+    auto tile_at = [&](int32_t t) {
+        return decode_tile(s_off, s_pre, E, BM, kOutN, args.n_tiles_n, t, args.n_major != 0);
+    };
+    // A pair's plain tile with no columns past its first 128 multiplies those alone, 64 in each CTA.
+    auto narrow = [&](const TileCoord& c) -> bool { return kPair && !kGateUp && N - c.col0 <= 128; };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- producer
+        if ((args.debug_flags & kDebugProducerStall) == 0) {
+            const uint32_t lead = elect_one();
+            int st = 0;
+            uint32_t ph = 0, issued = 0;
+            const uint32_t full0 = kPair ? map_to_rank(full_bar(0), 0) : full_bar(0);
+            bool ok = true;
+            for (int32_t t = unit; ok && t < T; t += units) {
+                const TileCoord c = tile_at(t);
+                const bool thin = narrow(c);
+                // rows of x in each CTA, and the boxes that bring them: one of
+                // 128 rows, or as many of 32 as hold rows of the expert
+                auto boxes_of = [&](int32_t rows) { return rows > 96 ? 4 : (rows + 31) / 32; };
+                const int32_t rows = c.rows - 128 * static_cast<int32_t>(rank);
+                const int boxes = rows > 0 ? boxes_of(rows) : 0;
+                const int32_t x_row = c.row0 + 128 * static_cast<int32_t>(rank);
+                // first row of W in this CTA (gate-up on a single CTA: and of its up rows)
+                const int32_t w_row = kGateUp ? c.col0 + (kPair && rank ? N : 0)
+                                              : c.col0 + (thin ? 64 : 128) * static_cast<int32_t>(rank);
+                uint32_t bytes = 0;
+                if (rank == 0) {
+                    const int more = kPair && c.rows > 128 ? boxes_of(c.rows - 128) : 0;  // the peer's
+                    bytes = (boxes + more) * 4096u + (kPair ? 2u : 1u) * (thin ? kFpTile / 2 : kWBytes);
+                }
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!wait(empty_bar(st), ph ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = full0 + 8u * st;
+                    if (rank == 0) expect_tx_if(lead, full_bar(st), bytes);
+                    const uint32_t a = a0 + st * kFpTile, b = b0 + st * kWBytes;
+                    const int32_t kx = kb * kFpBlock;
+                    auto x_ok = [&](int32_t row) {
+                        return RGG_BOUNDS_OK(x_box_ok(kx, row, args.K, args.M_tot, 1), args.status);
+                    };
+                    // a tile's second CTA may start past the last column: the copy zero-fills its rows
+                    auto w_ok = [&](int32_t row) {
+                        return RGG_BOUNDS_OK(w_box_ok(kx, row, c.expert, args.K, cols_w + 64, E, 1), args.status);
+                    };
+                    if (boxes == 4) {
+                        if (x_ok(x_row)) load_3d_if<kPair>(lead, a, &maps.x128, bar, kx, x_row, 0);
+                    } else {
+                        for (int i = 0; i < boxes; ++i)
+                            if (x_ok(x_row + 32 * i))
+                                load_3d_if<kPair>(lead, a + 4096u * i, &maps.x32, bar, kx, x_row + 32 * i, 0);
+                    }
+                    if (w_ok(w_row)) load_3d_if<kPair>(lead, b, thin ? &maps.w64 : &maps.w128, bar, kx, w_row, c.expert);
+                    if constexpr (!kPair && kGateUp)
+                        if (w_ok(N + w_row))
+                            load_3d_if<kPair>(lead, b + kFpTile, &maps.w128, bar, kx, N + w_row, c.expert);
+                    ++issued;
+                    if (++st == S) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                // copies are counted on the (leader's) full barriers, which a pair's second CTA does not watch
+                const uint32_t n = issued < static_cast<uint32_t>(S) ? issued : static_cast<uint32_t>(S);
+                if (rank == 0)
+                    for (uint32_t i = issued - n; i < issued; ++i)
+                        wait_bounded(full_bar(static_cast<int>(i % S)), (i / S) & 1u, kDrainLimitNs);
+                else
+                    spin_ns(200000ull);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ----------------------------------------------- MMA issuer (leader)
+        if (rank == 0) {
+            const uint32_t lead = elect_one();
+            int st = 0;
+            uint32_t ph = 0, n = 0;  // stages multiplied
+            const uint64_t a_desc = sw128_desc(a0, 16u, 1024u), b_desc = sw128_desc(b0, 16u, 1024u);
+            bool ok = true;
+            for (int32_t t = unit; ok && t < T; t += units) {
+                const uint32_t idesc = idesc_e4m3_f32(BM, narrow(tile_at(t)) ? 128 : BN, false);
+                for (int kb = 0; kb < KB; ++kb, ++n) {
+                    // the accumulator's last stage has been added up, and this one's operands are here
+                    if ((n >= 2 && !wait(acce_bar(n & 1), ((n >> 1) - 1) & 1u)) || !wait(full_bar(st), ph)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint64_t ad = a_desc + st * (kFpTile >> 4);
+                    const uint64_t bd = b_desc + st * (kWBytes >> 4);
+                    const uint32_t d_tmem = tmem_base + (n & 1) * BN;
+                    const int left = args.K - kb * kFpBlock;
+                    const int steps = left >= kFpBlock ? 4 : (left + 31) / 32;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (j >= steps) break;
+                        mma_e4m3_if<kPair>(lead, d_tmem, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u);
+                    }
+                    commit_if<kPair>(lead, empty_bar(st));
+                    commit_if<kPair>(lead, accf_bar(n & 1));
+                    if (++st == S) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                commit_if<kPair>(lead, drain_bar);
+                wait_bounded(drain_bar, 0u, kDrainLimitNs);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- epilogue
+        const int q = warp & 3;           // TMEM lanes 32 q to 32 q + 31
+        const int part = (warp - 2) >> 2; // its quarter of the columns
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        const int r_local = 128 * static_cast<int>(rank) + 32 * q + lane;
+        const int nblocks = static_cast<int>(fp_blocks(cols_w));
+        uint32_t n = 0, tiles = 0;
+        bool ok = true;
+        for (int32_t t = unit; ok && t < T; t += units, ++tiles) {
+            const TileCoord c = tile_at(t);
+            const bool row_ok = r_local < c.rows;
+            const int64_t row = static_cast<int64_t>(c.row0) + r_local;
+            // first column of the thread's sums; columns past N are not computed
+            const int col = kGateUp ? part * (kCols / 2) : part * kCols;
+            const bool work = kGateUp || c.col0 + col < N;
+            const float* sx = args.sx + (row_ok ? row : c.row0) * KB;
+            const float* sw = args.sw + (static_cast<int64_t>(c.expert) * nblocks + (c.col0 + (work ? col : 0)) / kFpBlock) * KB;
+            const float* su = sw + static_cast<int64_t>(N / kFpBlock) * KB;  // gate-up: of the up columns
+            float sum[kCols];
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
+            // scales two stages ahead
+            float fx0 = sx[0], fw0 = sw[0], fu0 = kGateUp ? su[0] : 0.0f;
+            float fx1 = KB > 1 ? sx[1] : 0.0f, fw1 = KB > 1 ? sw[1] : 0.0f, fu1 = kGateUp && KB > 1 ? su[1] : 0.0f;
+            for (int kb = 0; kb < KB; ++kb, ++n) {
+                const float f = fx0 * fw0, fu = kGateUp ? fx0 * fu0 : f;
+                fx0 = fx1;
+                fw0 = fw1;
+                fu0 = fu1;
+                if (kb + 2 < KB) {
+                    fx1 = sx[kb + 2];
+                    fw1 = sw[kb + 2];
+                    if (kGateUp) fu1 = su[kb + 2];
+                }
+                const uint32_t acc = n & 1;
+                if (!wait(accf_bar(acc), (n >> 1) & 1u)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                if (work) {
+                    const uint32_t col_acc = acc * BN + col;
+                    if (RGG_BOUNDS_OK(tmem_cols_ok(col_acc, kGateUp ? 128 + kCols / 2 : kCols, 2 * BN), args.status)) {
+#pragma unroll
+                        for (int i = 0; i < kCols / 16; ++i) {
+                            // gate-up: the second half of the sums is the up columns
+                            const int at = kGateUp && i >= kCols / 32 ? 128 + 16 * i - kCols / 2 : 16 * i;
+                            uint32_t v[16];
+                            tmem_ld_32x32b_x16(t_row + col_acc + at, v);
+                            tmem_ld_wait();
+                            const float s = kGateUp && i >= kCols / 32 ? fu : f;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                asm volatile("" : "+r"(v[j]));  // not before the wait
+                                sum[16 * i + j] = fmaf(__uint_as_float(v[j]), s, sum[16 * i + j]);
+                            }
+                        }
+                    }
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (kPair) mbar_arrive_cluster(map_to_rank(acce_bar(acc), 0));
+                    else mbar_arrive(acce_bar(acc));
+                }
+            }
+            if (!ok) break;
+            const int32_t row_lo = s_off[c.expert], row_hi = s_off[c.expert + 1];
+            if constexpr (!kGateUp) {
+                if (!work) continue;
+#pragma unroll
+                for (int i = 0; i < kCols / 32; ++i) {
+                    const int cc = c.col0 + col + 32 * i;
+                    if (cc >= N) continue;
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        w[j] = pack_bf16x2(__float_as_uint(sum[32 * i + 2 * j]), __float_as_uint(sum[32 * i + 2 * j + 1]));
+                    if (!args.y_vec32) {
+                        store_rows_turned(args.Y, N, row, row_ok, cc, N, w, lane, row_lo, row_hi, args.status);
+                        continue;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // whole 16 columns: N is a multiple of 16
+                        if (!row_ok || cc + 16 * h >= N ||
+                            !RGG_BOUNDS_OK(store_ok(row, cc + 16 * h, 16, row_lo, row_hi, N), args.status))
+                            continue;
+                        const uint32_t x[8] = {w[8 * h],     w[8 * h + 1], w[8 * h + 2], w[8 * h + 3],
+                                               w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]};
+                        st_global_v8(args.Y + row * N + cc + 16 * h, x);
+                    }
+                }
+            } else {
+                // H, its largest magnitude over the 128 columns (four warps', through
+                // shared memory, two buffers by turns: a warp is in the next but one
+                // tile's only when all have left this one's), codes and scale
+                constexpr int kH = kCols / 2;
+                float top = kFpLeast;
+#pragma unroll
+                for (int i = 0; i < kH; ++i) {
+                    const float g = sum[i];
+                    sum[i] = __fdividef(g, 1.0f + __expf(-g)) * sum[kH + i];
+                    top = fmaxf(top, fabsf(sum[i]));
+                }
+                float* s_top = reinterpret_cast<float*>(gbase + sp.top_off) + (tiles & 1) * 512;
+                s_top[part * 128 + 32 * q + lane] = top;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(top_bar(q));
+                if (!wait(top_bar(q), tiles & 1)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, s_top[i * 128 + 32 * q + lane]);
+                const float inv = kFpMax / top;
+                uint32_t w[kH / 4];
+#pragma unroll
+                for (int i = 0; i < kH / 4; ++i) {
+                    uint16_t lo, hi;
+                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(sum[4 * i + 1] * inv), "f"(sum[4 * i] * inv));
+                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(sum[4 * i + 3] * inv), "f"(sum[4 * i + 2] * inv));
+                    w[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+                }
+                if (row_ok && RGG_BOUNDS_OK(store_ok(row, c.col0 + col, kH, row_lo, row_hi, N), args.status)) {
+                    uint8_t* out = args.codes + row * N + c.col0 + col;
+#pragma unroll
+                    for (int i = 0; i < kH / 16; ++i)
+                        st_global_v4(out + 16 * i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    if (part == 0) args.scales[row * (N / kFpBlock) + c.col0 / kFpBlock] = top / kFpMax;
+                }
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    if constexpr (kPair) cluster_sync_all();  // neither CTA leaves while the pair's MMAs or arrivals may touch it
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        if constexpr (kPair) tmem_dealloc_pair(tmem_base, 2 * BN);
+        else tmem_dealloc(tmem_base, 2 * BN);
+    }
+}
+
+template <bool kGateUp>
+__global__ void __launch_bounds__(kFpThreads, 1)
+    grouped_fp8_block_kernel(const __grid_constant__ FpMaps maps, const __grid_constant__ FpArgs args) {
+    fp8_block_tiles<false, kGateUp>(maps, args);
+}
+
+template <bool kGateUp>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFpThreads, 1)
+    grouped_fp8_block_pair_kernel(const __grid_constant__ FpMaps maps, const __grid_constant__ FpArgs args) {
+    fp8_block_tiles<true, kGateUp>(maps, args);
+}
+
+}  // namespace rgg

@@ -9,17 +9,18 @@
 // a scale per row and 128 columns, which the down product reads.
 //
 // The scales are arbitrary fp32 numbers, so the tensor core cannot apply them: each
-// stage of 128 of K is a product of its own, into one of two accumulators in TMEM,
-// and the epilogue warps add it, times its two scales, to the sums that they hold in
-// registers while the next stage is multiplied into the other.
+// stage of 128 of K by 128 columns is a product of its own, into one of four
+// accumulators in TMEM in turn, and the epilogue warps add it, times its two scales, to
+// the sums that they hold in registers while the next ones are multiplied.
 //
 // Two tile shapes, one kernel.  A CTA pair (cta_group::2) computes 256 x 256: each CTA
 // holds 128 rows of x and half of the W rows.  A single CTA computes 128 x 128, or for
 // gate-up 128 x 256 (128 columns of H, whose scale needs them all).
 //
-// Persistent over the flat tile list; warp 0 copies, warp 1 issues, warps 2-17 add up
-// and write: four for each 32 TMEM lanes, with a quarter of the columns each, so
-// that a thread holds at most 64 sums, and each warp's waits run under the others' work.
+// Persistent over the flat tile list; warp 0 copies, warp 1 issues, warps 4-11 add up
+// and write: two for each 32 TMEM lanes, with half of the columns each.  A thread holds up to
+// 128 sums and 32 values on their way from TMEM, so the epilogue's warps take over registers
+// that the others do not need.
 // A stage holds 128 bytes a row, one swizzle row, K-major on both sides.
 #pragma once
 
@@ -51,16 +52,23 @@ struct FpMaps {
     CUtensorMap x128, x32, w128, w64;
 };
 
-constexpr int kFpEpiWarps = 16;
-constexpr int kFpThreads = 64 + 32 * kFpEpiWarps;
+constexpr int kFpParts = 2;  // parts of 128 columns, each added up by a warp of every 32 TMEM lanes
+constexpr int kFpCols = 128 / kFpParts;
+constexpr int kFpMostSlots = 4;  // accumulators, at most
+constexpr int kFpEpiWarps = 4 * kFpParts;
+constexpr int kFpThreads = 128 + 32 * kFpEpiWarps;
+// Registers a thread: at launch, and how the four warps that copy and issue and the
+// epilogue's share them out.  (An increase waits until the block has as many left,
+// so the shares must add up to the launch's, which the host checks.)
+constexpr int kFpRegsLaunch = 168, kFpRegsIssue = 40, kFpRegsEpi = 232;
+static_assert(128 * kFpRegsIssue + 32 * kFpEpiWarps * kFpRegsEpi == kFpThreads * kFpRegsLaunch, "");
 constexpr uint32_t kFpTile = 128u * 128u;  // bytes of 128 rows of a stage
 
-// Columns that a tile multiplies.
+// Halves of 128 columns that a whole tile multiplies, and bytes of W in a stage of a CTA.
 template <bool kPair, bool kGateUp>
-__host__ __device__ constexpr int fp_tile_cols() { return (kPair || kGateUp) ? 256 : 128; }
-// Bytes of W in a stage of a CTA.
+__host__ __device__ constexpr int fp_halves() { return (kPair || kGateUp) ? 2 : 1; }
 template <bool kPair, bool kGateUp>
-__host__ __device__ constexpr uint32_t fp_w_bytes() { return (!kPair && kGateUp) ? 2 * kFpTile : kFpTile; }
+__host__ __device__ constexpr uint32_t fp_w_bytes() { return fp_halves<kPair, kGateUp>() * kFpTile / (kPair ? 2 : 1); }
 
 struct FpSmem {
     uint32_t b_off, top_off, bar_off, misc_off, off_off, pre_off, total;
@@ -70,9 +78,9 @@ __host__ __device__ inline FpSmem fp_smem(int stages, int E, uint32_t w_bytes, b
     FpSmem p;
     const uint32_t ex = 4u * static_cast<uint32_t>(E + 1);
     p.b_off = stages * kFpTile;
-    p.top_off = p.b_off + stages * w_bytes;               // gate-up: [2][4][128] magnitudes
-    p.bar_off = p.top_off + (gate_up ? 4096u : 0u);       // full[S], empty[S], acc_full[2], acc_empty[2], top[4], drain
-    p.misc_off = p.bar_off + 8u * (2u * stages + 9u);
+    p.top_off = p.b_off + stages * w_bytes;               // gate-up: [2][kFpParts][128] magnitudes
+    p.bar_off = p.top_off + (gate_up ? 1024u * kFpParts : 0u);  // full[S], empty[S], acc_full[4], acc_empty[4], top[4], drain
+    p.misc_off = p.bar_off + 8u * (2u * stages + 2u * kFpMostSlots + 5u);
     p.misc_off = (p.misc_off + 15u) & ~15u;
     p.off_off = p.misc_off + 16u;
     p.pre_off = p.off_off + ex;
@@ -95,16 +103,6 @@ __device__ __forceinline__ void mma_e4m3_if(uint32_t lead, uint32_t d_tmem, uint
         mma_single_if<true>(lead, d_tmem, a_desc, b_desc, idesc, accumulate);
 }
 
-// Each thread reads its TMEM lane's 16 columns from taddr's on.
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
 // Arrives on `bar` (kPair: at that offset in the pair's first CTA) behind the warp's loads from TMEM.  Relaxed: nothing
 // that was written to memory is handed over, and a release at cluster scope waits for the
 // scales' loads as well (32,768 rows, 6144 x 4096, on pairs: 1 402 us with it).
@@ -116,13 +114,59 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
         asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Each thread reads its TMEM lane's 16 columns from taddr's on.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Two fp32 sums in a register pair: sum += v * f, each rounded once, in one instruction.
+__device__ __forceinline__ void add_scaled2(uint64_t& sum, uint32_t v0, uint32_t v1, uint64_t f) {
+    asm("{\n\t.reg .b64 v;\n\t"
+        "mov.b64 v, {%1, %2};\n\t"
+        "fma.rn.f32x2 %0, v, %3, %0;\n\t}"
+        : "+l"(sum)
+        : "r"(v0), "r"(v1), "l"(f));
+}
+__device__ __forceinline__ uint64_t twice(float f) {
+    const uint64_t b = __float_as_uint(f);
+    return b | (b << 32);
+}
+__device__ __forceinline__ float half_of(uint64_t s, int i) {
+    return __uint_as_float(static_cast<uint32_t>(i ? s >> 32 : s));
+}
+
+// warp_wait without a call, which the sums in registers would have to be saved for.
+template <bool kPair>
+__device__ __forceinline__ bool warp_wait_inline(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                                 uint32_t peer_flag, int32_t* status, uint64_t timeout_ns) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *abort_flag != 0u)) return false;
+        if (__any_sync(0xffffffffu, global_timer_ns() - t0 > timeout_ns)) {
+            *abort_flag = 1u;
+            if constexpr (kPair) st_shared_cluster_u32(peer_flag, 1u);
+            atomicCAS(status, 0, kStatusTimeout);
+            return false;
+        }
+    }
+}
+
 template <bool kPair, bool kGateUp>
 __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs& args) {
     constexpr int BM = kPair ? 256 : 128;
-    constexpr int BN = fp_tile_cols<kPair, kGateUp>();
-    constexpr int kOutN = kGateUp ? BN / 2 : BN;
+    constexpr int kHalves = fp_halves<kPair, kGateUp>();
+    constexpr int kOutN = kGateUp ? 128 : 128 * kHalves;
     constexpr uint32_t kWBytes = fp_w_bytes<kPair, kGateUp>();
-    constexpr int kCols = BN / 4;  // columns whose sums a thread holds; gate-up: half gate, half up
+    constexpr uint32_t kHalfBytes = kFpTile;       // single CTAs: 128 rows of W
+    constexpr uint32_t kSlotCols = 128 * kHalves;  // an accumulator; all of TMEM's 512 columns are in use
+    constexpr uint32_t kSlots = 512 / kSlotCols;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
 
     const int warp = uniform_warp();
@@ -143,9 +187,9 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
     auto accf_bar = [&](int a) { return bars + 8u * (2 * S + a); };
-    auto acce_bar = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
-    auto top_bar = [&](int q) { return bars + 8u * (2 * S + 4 + q); };
-    const uint32_t drain_bar = bars + 8u * (2 * S + 8);
+    auto acce_bar = [&](int a) { return bars + 8u * (2 * S + kFpMostSlots + a); };
+    auto top_bar = [&](int q) { return bars + 8u * (2 * S + 2 * kFpMostSlots + q); };
+    const uint32_t drain_bar = bars + 8u * (2 * S + 2 * kFpMostSlots + 4);
     uint32_t* misc = reinterpret_cast<uint32_t*>(gbase + sp.misc_off);
     int32_t* s_off = reinterpret_cast<int32_t*>(gbase + sp.off_off);
     int32_t* s_pre = reinterpret_cast<int32_t*>(gbase + sp.pre_off);
@@ -167,11 +211,11 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < static_cast<int>(kSlots); ++a) {
             mbar_init(accf_bar(a), 1);
             mbar_init(acce_bar(a), (kPair ? 2 : 1) * kFpEpiWarps);
         }
-        for (int q = 0; q < 4; ++q) mbar_init(top_bar(q), 4);
+        for (int q = 0; q < 4; ++q) mbar_init(top_bar(q), kFpParts);
         mbar_init(drain_bar, 1);
         misc[1] = 0u;
         fence_mbar_init();
@@ -179,14 +223,14 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
     if (warp == 0 && lane == 0) {
         tma_prefetch_map(&maps.x128);
         tma_prefetch_map(&maps.x32);
-        tma_prefetch_map(&maps.w128);
+        tma_prefetch_map(kPair ? &maps.w64 : &maps.w128);
     }
     if (warp == 1) {
         if constexpr (kPair) {
-            tmem_alloc_pair(smem_addr(&misc[0]), 2 * BN);
+            tmem_alloc_pair(smem_addr(&misc[0]), 512);
             tmem_relinquish_pair();
         } else {
-            tmem_alloc(smem_addr(&misc[0]), 2 * BN);
+            tmem_alloc(smem_addr(&misc[0]), 512);
             tmem_relinquish();
         }
     }
@@ -207,9 +251,11 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
     auto tile_at = [&](int32_t t) {
         return decode_tile(s_off, s_pre, E, BM, kOutN, args.n_tiles_n, t, args.n_major != 0);
     };
-    // A pair's plain tile with no columns past its first 128 multiplies those alone, 64 in each CTA.
-    auto narrow = [&](const TileCoord& c) -> bool { return kPair && !kGateUp && N - c.col0 <= 128; };
+    // A plain tile with no columns past its first 128 multiplies those alone.
+    auto halves_of = [&](const TileCoord& c) -> int { return kHalves == 2 && (kGateUp || N - c.col0 > 128) ? 2 : 1; };
 
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFpRegsIssue));
     if (warp == 0) {
         // ---------------------------------------------------------- producer
         if ((args.debug_flags & kDebugProducerStall) == 0) {
@@ -220,20 +266,19 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
             bool ok = true;
             for (int32_t t = unit; ok && t < T; t += units) {
                 const TileCoord c = tile_at(t);
-                const bool thin = narrow(c);
+                const int halves = halves_of(c);
                 // rows of x in each CTA, and the boxes that bring them: one of
                 // 128 rows, or as many of 32 as hold rows of the expert
                 auto boxes_of = [&](int32_t rows) { return rows > 96 ? 4 : (rows + 31) / 32; };
                 const int32_t rows = c.rows - 128 * static_cast<int32_t>(rank);
                 const int boxes = rows > 0 ? boxes_of(rows) : 0;
                 const int32_t x_row = c.row0 + 128 * static_cast<int32_t>(rank);
-                // first row of W in this CTA (gate-up on a single CTA: and of its up rows)
-                const int32_t w_row = kGateUp ? c.col0 + (kPair && rank ? N : 0)
-                                              : c.col0 + (thin ? 64 : 128) * static_cast<int32_t>(rank);
+                // first row of W in this CTA: a pair's second one has the second half, or half of the only one
+                const int32_t w_row = c.col0 + (kPair && rank ? (kGateUp ? N : 64 * halves) : 0);
                 uint32_t bytes = 0;
                 if (rank == 0) {
                     const int more = kPair && c.rows > 128 ? boxes_of(c.rows - 128) : 0;  // the peer's
-                    bytes = (boxes + more) * 4096u + (kPair ? 2u : 1u) * (thin ? kFpTile / 2 : kWBytes);
+                    bytes = (boxes + more) * 4096u + halves * kFpTile;  // of W: a pair's halves are shared out
                 }
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!wait(empty_bar(st), ph ^ 1u)) {
@@ -247,7 +292,7 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                     auto x_ok = [&](int32_t row) {
                         return RGG_BOUNDS_OK(x_box_ok(kx, row, args.K, args.M_tot, 1), args.status);
                     };
-                    // a tile's second CTA may start past the last column: the copy zero-fills its rows
+                    // a pair's second CTA may start past the last column: the copy zero-fills its rows
                     auto w_ok = [&](int32_t row) {
                         return RGG_BOUNDS_OK(w_box_ok(kx, row, c.expert, args.K, cols_w + 64, E, 1), args.status);
                     };
@@ -258,10 +303,13 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                             if (x_ok(x_row + 32 * i))
                                 load_3d_if<kPair>(lead, a + 4096u * i, &maps.x32, bar, kx, x_row + 32 * i, 0);
                     }
-                    if (w_ok(w_row)) load_3d_if<kPair>(lead, b, thin ? &maps.w64 : &maps.w128, bar, kx, w_row, c.expert);
-                    if constexpr (!kPair && kGateUp)
-                        if (w_ok(N + w_row))
-                            load_3d_if<kPair>(lead, b + kFpTile, &maps.w128, bar, kx, N + w_row, c.expert);
+                    if constexpr (kPair) {
+                        if (w_ok(w_row)) load_3d_if<kPair>(lead, b, halves == 1 ? &maps.w64 : &maps.w128, bar, kx, w_row, c.expert);
+                    } else {
+                        if (w_ok(w_row)) load_3d_if<kPair>(lead, b, &maps.w128, bar, kx, w_row, c.expert);
+                        if (kGateUp && w_ok(N + w_row))
+                            load_3d_if<kPair>(lead, b + kHalfBytes, &maps.w128, bar, kx, N + w_row, c.expert);
+                    }
                     ++issued;
                     if (++st == S) {
                         st = 0;
@@ -289,26 +337,26 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
             const uint64_t a_desc = sw128_desc(a0, 16u, 1024u), b_desc = sw128_desc(b0, 16u, 1024u);
             bool ok = true;
             for (int32_t t = unit; ok && t < T; t += units) {
-                const uint32_t idesc = idesc_e4m3_f32(BM, narrow(tile_at(t)) ? 128 : BN, false);
+                const uint32_t idesc = idesc_e4m3_f32(BM, 128 * halves_of(tile_at(t)), false);
                 for (int kb = 0; kb < KB; ++kb, ++n) {
-                    // the accumulator's last stage has been added up, and this one's operands are here
-                    if ((n >= 2 && !wait(acce_bar(n & 1), ((n >> 1) - 1) & 1u)) || !wait(full_bar(st), ph)) {
+                    // the slot's last sums have been read, and the stage's operands are here
+                    const uint32_t slot = n % kSlots;
+                    if ((n >= kSlots && !wait(acce_bar(slot), (n / kSlots - 1) & 1u)) || !wait(full_bar(st), ph)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
                     const uint64_t ad = a_desc + st * (kFpTile >> 4);
                     const uint64_t bd = b_desc + st * (kWBytes >> 4);
-                    const uint32_t d_tmem = tmem_base + (n & 1) * BN;
                     const int left = args.K - kb * kFpBlock;
                     const int steps = left >= kFpBlock ? 4 : (left + 31) / 32;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (j >= steps) break;
-                        mma_e4m3_if<kPair>(lead, d_tmem, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u);
+                        mma_e4m3_if<kPair>(lead, tmem_base + slot * kSlotCols, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u);
                     }
+                    commit_if<kPair>(lead, accf_bar(slot));
                     commit_if<kPair>(lead, empty_bar(st));
-                    commit_if<kPair>(lead, accf_bar(n & 1));
                     if (++st == S) {
                         st = 0;
                         ph ^= 1u;
@@ -321,10 +369,15 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
             }
         }
         __syncwarp();
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFpRegsEpi));
         // ---------------------------------------------------------- epilogue
-        const int q = warp & 3;           // TMEM lanes 32 q to 32 q + 31
-        const int part = (warp - 2) >> 2; // its quarter of the columns
+        auto epi_wait = [&](uint32_t bar, uint32_t parity) -> bool {
+            return warp_wait_inline<kPair>(bar, parity, abort_flag, peer_flag, args.status, args.timeout_ns);
+        };
+        const int q = warp & 3;            // TMEM lanes 32 q to 32 q + 31
+        const int part = (warp - 4) >> 2;  // its part of the columns
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         const int r_local = 128 * static_cast<int>(rank) + 32 * q + lane;
         const int nblocks = static_cast<int>(fp_blocks(cols_w));
@@ -334,64 +387,72 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
             const TileCoord c = tile_at(t);
             const bool row_ok = r_local < c.rows;
             const int64_t row = static_cast<int64_t>(c.row0) + r_local;
-            // first column of the thread's sums; columns past N are not computed
-            const int col = kGateUp ? part * (kCols / 2) : part * kCols;
-            const bool work = kGateUp || c.col0 + col < N;
+            const int halves = halves_of(c);
+            const int col = part * kFpCols;  // first column of the thread's sums, in each half
+            // scales: of the row, and of the first and second half's 128 columns
             const float* sx = args.sx + (row_ok ? row : c.row0) * KB;
-            const float* sw = args.sw + (static_cast<int64_t>(c.expert) * nblocks + (c.col0 + (work ? col : 0)) / kFpBlock) * KB;
-            const float* su = sw + static_cast<int64_t>(N / kFpBlock) * KB;  // gate-up: of the up columns
-            float sum[kCols];
+            const float* sw = args.sw + (static_cast<int64_t>(c.expert) * nblocks + c.col0 / kFpBlock) * KB;
+            const float* su = halves == 2 ? sw + static_cast<int64_t>(kGateUp ? N / kFpBlock : 1) * KB : sw;
+            uint64_t sums[kHalves * kFpCols / 2];
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
-            // scales two stages ahead
-            float fx0 = sx[0], fw0 = sw[0], fu0 = kGateUp ? su[0] : 0.0f;
-            float fx1 = KB > 1 ? sx[1] : 0.0f, fw1 = KB > 1 ? sw[1] : 0.0f, fu1 = kGateUp && KB > 1 ? su[1] : 0.0f;
-            for (int kb = 0; kb < KB; ++kb, ++n) {
-                const float f = fx0 * fw0, fu = kGateUp ? fx0 * fu0 : f;
+            for (int i = 0; i < kHalves * kFpCols / 2; ++i) sums[i] = 0u;
+            // two stages ahead
+            float fx0 = sx[0], fw0 = sw[0], fu0 = su[0];
+            float fx1 = KB > 1 ? sx[1] : 0.0f, fw1 = KB > 1 ? sw[1] : 0.0f, fu1 = KB > 1 ? su[1] : 0.0f;
+            for (int kb = 0; ok && kb < KB; ++kb) {
+                const float f[2] = {fx0 * fw0, fx0 * fu0};
                 fx0 = fx1;
                 fw0 = fw1;
                 fu0 = fu1;
                 if (kb + 2 < KB) {
                     fx1 = sx[kb + 2];
                     fw1 = sw[kb + 2];
-                    if (kGateUp) fu1 = su[kb + 2];
+                    if (kHalves == 2) fu1 = su[kb + 2];
                 }
-                const uint32_t acc = n & 1;
-                if (!wait(accf_bar(acc), (n >> 1) & 1u)) {
+                const uint32_t slot = n % kSlots;
+                if (!epi_wait(accf_bar(slot), (n / kSlots) & 1u)) {
                     ok = false;
                     break;
                 }
+                ++n;
                 tc_fence_after_sync();
-                if (work) {
-                    const uint32_t col_acc = acc * BN + col;
-                    if (RGG_BOUNDS_OK(tmem_cols_ok(col_acc, kGateUp ? 128 + kCols / 2 : kCols, 2 * BN), args.status)) {
+                // 32 columns at a time, two of them on their way; columns past N hold nothing that is read
+                constexpr int kChunks = kHalves * kFpCols / 32, kPerHalf = kFpCols / 32;
+                uint32_t v[2][32];
+                const uint32_t at = slot * kSlotCols + col;
+                auto load = [&](int i) {
+                    const uint32_t c0 = at + 128 * (i / kPerHalf) + 32 * (i % kPerHalf);
+                    if (RGG_BOUNDS_OK(tmem_cols_ok(c0, 32, 512), args.status)) tmem_ld_32x32b_x32(t_row + c0, v[i & 1]);
+                };
+                load(0);
+                load(1);
 #pragma unroll
-                        for (int i = 0; i < kCols / 16; ++i) {
-                            // gate-up: the second half of the sums is the up columns
-                            const int at = kGateUp && i >= kCols / 32 ? 128 + 16 * i - kCols / 2 : 16 * i;
-                            uint32_t v[16];
-                            tmem_ld_32x32b_x16(t_row + col_acc + at, v);
-                            tmem_ld_wait();
-                            const float s = kGateUp && i >= kCols / 32 ? fu : f;
+                for (int i = 0; i < kChunks; ++i) {
+                    if ((i & 1) == 0) {
+                        tmem_ld_wait();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                asm volatile("" : "+r"(v[j]));  // not before the wait
-                                sum[16 * i + j] = fmaf(__uint_as_float(v[j]), s, sum[16 * i + j]);
-                            }
+                        for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[0][j]), "+r"(v[1][j]));  // not before the wait
+                        if (i + 2 == kChunks) {
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) arrive_relaxed<kPair>(acce_bar(slot));
                         }
                     }
+                    const uint64_t ff = twice(f[i / kPerHalf]);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) add_scaled2(sums[16 * i + j], v[i & 1][2 * j], v[i & 1][2 * j + 1], ff);
+                    if (i + 2 < kChunks) load(i + 2);
                 }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) arrive_relaxed<kPair>(acce_bar(acc));
             }
             if (!ok) break;
+            float sum[kHalves * kFpCols];
+#pragma unroll
+            for (int i = 0; i < kHalves * kFpCols; ++i) sum[i] = half_of(sums[i / 2], i & 1);
             const int32_t row_lo = s_off[c.expert], row_hi = s_off[c.expert + 1];
             if constexpr (!kGateUp) {
-                if (!work) continue;
 #pragma unroll
-                for (int i = 0; i < kCols / 32; ++i) {
-                    const int cc = c.col0 + col + 32 * i;
+                for (int i = 0; i < kHalves * kFpCols / 32; ++i) {
+                    const int cc = c.col0 + 128 * (32 * i / kFpCols) + col + 32 * i % kFpCols;
                     if (cc >= N) continue;
                     uint32_t w[16];
 #pragma unroll
@@ -412,10 +473,10 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                     }
                 }
             } else {
-                // H, its largest magnitude over the 128 columns (four warps', through
+                // H, its largest magnitude over the 128 columns (two warps', through
                 // shared memory, two buffers by turns: a warp is in the next but one
                 // tile's only when all have left this one's), codes and scale
-                constexpr int kH = kCols / 2;
+                constexpr int kH = kFpCols;
                 float top = kFpLeast;
 #pragma unroll
                 for (int i = 0; i < kH; ++i) {
@@ -423,16 +484,16 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                     sum[i] = __fdividef(g, 1.0f + __expf(-g)) * sum[kH + i];
                     top = fmaxf(top, fabsf(sum[i]));
                 }
-                float* s_top = reinterpret_cast<float*>(gbase + sp.top_off) + (tiles & 1) * 512;
+                float* s_top = reinterpret_cast<float*>(gbase + sp.top_off) + (tiles & 1) * (128 * kFpParts);
                 s_top[part * 128 + 32 * q + lane] = top;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(top_bar(q));
-                if (!wait(top_bar(q), tiles & 1)) {
+                if (!epi_wait(top_bar(q), tiles & 1)) {
                     ok = false;
                     break;
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, s_top[i * 128 + 32 * q + lane]);
+                for (int i = 0; i < kFpParts; ++i) top = fmaxf(top, s_top[i * 128 + 32 * q + lane]);
                 const float inv = kFpMax / top;
                 uint32_t w[kH / 4];
 #pragma unroll
@@ -458,8 +519,8 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
     else __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
-        if constexpr (kPair) tmem_dealloc_pair(tmem_base, 2 * BN);
-        else tmem_dealloc(tmem_base, 2 * BN);
+        if constexpr (kPair) tmem_dealloc_pair(tmem_base, 512);
+        else tmem_dealloc(tmem_base, 512);
     }
 }
 

@@ -16,6 +16,12 @@ static cudaError_t launch_fp8_block(Kernel kernel, int grid, size_t smem, cudaSt
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(smem));
     if (err != cudaSuccess) return err;
+    // the kernel's warps share out the registers that it was launched with: other code than
+    // was planned for would wait for ever
+    cudaFuncAttributes attr;
+    err = cudaFuncGetAttributes(&attr, kernel);
+    if (err != cudaSuccess) return err;
+    if (attr.numRegs != kFpRegsLaunch) return cudaErrorInvalidKernelImage;
     return launch_chained(kernel, grid, kFpThreads, smem, stream, maps, args);
 }
 

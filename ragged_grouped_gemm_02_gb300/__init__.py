@@ -1214,12 +1214,13 @@ def _fp8_block_operands(x_codes, x_scales, w_codes, w_scales, group_offsets):
     return M_tot, K, E, cols, dev
 
 
-def rgg_grouped_gemm_fp8_block(x_codes, x_scales, w_codes, w_scales, group_offsets, Y=None, *, bm=0, stages=0, max_ctas=0,
-                               timeout_ns=0, debug_flags=0, stream=None, check=False):
+def rgg_grouped_gemm_fp8_block(x_codes, x_scales, w_codes, w_scales, group_offsets, Y=None, *, bm=0, bn=0, stages=0,
+                               max_ctas=0, timeout_ns=0, debug_flags=0, stream=None, check=False):
     """Y_e = X_e . W_e for every expert with 8-bit operands and a scale per block of
     128, as ``rgg_fp8_block_quantize`` and ``rgg_fp8_block_quantize_weights`` leave
     them; Y: optional bf16 CUDA [M_tot, N].  bm: 256 (256 x 256 tiles on CTA
-    pairs), 128 (single CTAs) or 0, by the sizes."""
+    pairs), 128 (single CTAs, with bn 128 or 256 columns a tile) or 0, by the
+    sizes."""
     import torch
     M_tot, K, E, N, dev = _fp8_block_operands(x_codes, x_scales, w_codes, w_scales, group_offsets)
     if Y is None:
@@ -1228,8 +1229,8 @@ def rgg_grouped_gemm_fp8_block(x_codes, x_scales, w_codes, w_scales, group_offse
         _operand("Y", Y, torch.bfloat16, (M_tot, N), dev)
     device = dev.index
     opt = None
-    if bm or stages or max_ctas or timeout_ns or debug_flags:
-        opt, _ = _options(bm, 0, stages, max_ctas, timeout_ns, None, debug_flags)
+    if bm or bn or stages or max_ctas or timeout_ns or debug_flags:
+        opt, _ = _options(bm, bn, stages, max_ctas, timeout_ns, None, debug_flags)
     st = _raw_stream(stream, device)
     s = load_library().rgg_grouped_gemm_fp8_block(
         _handle(device), x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),

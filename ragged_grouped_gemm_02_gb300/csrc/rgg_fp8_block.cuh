@@ -55,6 +55,7 @@ struct FpMaps {
 constexpr int kFpParts = 2;  // parts of 128 columns, each added up by a warp of every 32 TMEM lanes
 constexpr int kFpCols = 128 / kFpParts;
 constexpr int kFpMostSlots = 4;  // accumulators, at most
+constexpr int kFpFactors = 8;    // stages whose scales' products are held, at most
 constexpr int kFpEpiWarps = 4 * kFpParts;
 constexpr int kFpThreads = 128 + 32 * kFpEpiWarps;
 // Registers a thread: at launch, and how the four warps that copy and issue and the
@@ -64,21 +65,26 @@ constexpr int kFpRegsLaunch = 168, kFpRegsIssue = 40, kFpRegsEpi = 232;
 static_assert(128 * kFpRegsIssue + 32 * kFpEpiWarps * kFpRegsEpi == kFpThreads * kFpRegsLaunch, "");
 constexpr uint32_t kFpTile = 128u * 128u;  // bytes of 128 rows of a stage
 
+// The tiles: rows by columns of W.
+constexpr int kFpPair = 0;      // 256 x 256 on a CTA pair
+constexpr int kFpWide = 1;      // 128 x 256 on a single CTA
+constexpr int kFpNarrow = 2;    // 128 x 128 on a single CTA (not for gate-up)
 // Halves of 128 columns that a whole tile multiplies, and bytes of W in a stage of a CTA.
-template <bool kPair, bool kGateUp>
-__host__ __device__ constexpr int fp_halves() { return (kPair || kGateUp) ? 2 : 1; }
-template <bool kPair, bool kGateUp>
-__host__ __device__ constexpr uint32_t fp_w_bytes() { return fp_halves<kPair, kGateUp>() * kFpTile / (kPair ? 2 : 1); }
+__host__ __device__ constexpr int fp_halves(int shape) { return shape == kFpNarrow ? 1 : 2; }
+__host__ __device__ constexpr uint32_t fp_w_bytes(int shape) {
+    return fp_halves(shape) * kFpTile / (shape == kFpPair ? 2 : 1);
+}
 
 struct FpSmem {
-    uint32_t b_off, top_off, bar_off, misc_off, off_off, pre_off, total;
+    uint32_t b_off, factor_off, top_off, bar_off, misc_off, off_off, pre_off, total;
 };
 
 __host__ __device__ inline FpSmem fp_smem(int stages, int E, uint32_t w_bytes, bool gate_up) {
     FpSmem p;
     const uint32_t ex = 4u * static_cast<uint32_t>(E + 1);
     p.b_off = stages * kFpTile;
-    p.top_off = p.b_off + stages * w_bytes;               // gate-up: [2][kFpParts][128] magnitudes
+    p.factor_off = p.b_off + stages * w_bytes;            // [kFpFactors][128][2] products of a row's and the columns' scales
+    p.top_off = p.factor_off + 1024u * kFpFactors;        // gate-up: [2][kFpParts][128] magnitudes
     p.bar_off = p.top_off + (gate_up ? 1024u * kFpParts : 0u);  // full[S], empty[S], acc_full[4], acc_empty[4], top[4], drain
     p.misc_off = p.bar_off + 8u * (2u * stages + 2u * kFpMostSlots + 5u);
     p.misc_off = (p.misc_off + 15u) & ~15u;
@@ -103,13 +109,13 @@ __device__ __forceinline__ void mma_e4m3_if(uint32_t lead, uint32_t d_tmem, uint
         mma_single_if<true>(lead, d_tmem, a_desc, b_desc, idesc, accumulate);
 }
 
-// Arrives on `bar` (kPair: at that offset in the pair's first CTA) behind the warp's loads from TMEM.  Relaxed: nothing
+// Arrives on `bar` (kPair: a cluster address) behind the warp's loads from TMEM.  Relaxed: nothing
 // that was written to memory is handed over, and a release at cluster scope waits for the
 // scales' loads as well (32,768 rows, 6144 x 4096, on pairs: 1 402 us with it).
 template <bool kPair>
 __device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
     if constexpr (kPair)
-        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, 0)) : "memory");
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
     else
         asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -158,15 +164,19 @@ __device__ __forceinline__ bool warp_wait_inline(uint32_t bar, uint32_t parity, 
     }
 }
 
-template <bool kPair, bool kGateUp>
+template <int kShape, bool kGateUp>
 __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs& args) {
+    static_assert(!(kGateUp && kShape == kFpNarrow), "a scale of H needs 128 of its columns");
+    constexpr bool kPair = kShape == kFpPair;
     constexpr int BM = kPair ? 256 : 128;
-    constexpr int kHalves = fp_halves<kPair, kGateUp>();
+    constexpr int kHalves = fp_halves(kShape);
     constexpr int kOutN = kGateUp ? 128 : 128 * kHalves;
-    constexpr uint32_t kWBytes = fp_w_bytes<kPair, kGateUp>();
+    constexpr uint32_t kWBytes = fp_w_bytes(kShape);
     constexpr uint32_t kHalfBytes = kFpTile;       // single CTAs: 128 rows of W
     constexpr uint32_t kSlotCols = 128 * kHalves;  // an accumulator; all of TMEM's 512 columns are in use
     constexpr uint32_t kSlots = 512 / kSlotCols;
+    constexpr uint32_t kRing = 2 * kSlots;         // stages whose scales' products are held
+    static_assert(kRing <= kFpFactors && kRing >= kSlots + 2 && kRing <= 2 * kSlots + 1, "");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
 
     const int warp = uniform_warp();
@@ -212,7 +222,7 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
             mbar_init(empty_bar(s), 1);
         }
         for (int a = 0; a < static_cast<int>(kSlots); ++a) {
-            mbar_init(accf_bar(a), 1);
+            mbar_init(accf_bar(a), 1 + 2);  // the MMAs' commit, and two warps with the scales
             mbar_init(acce_bar(a), (kPair ? 2 : 1) * kFpEpiWarps);
         }
         for (int q = 0; q < 4; ++q) mbar_init(top_bar(q), kFpParts);
@@ -307,8 +317,8 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                         if (w_ok(w_row)) load_3d_if<kPair>(lead, b, halves == 1 ? &maps.w64 : &maps.w128, bar, kx, w_row, c.expert);
                     } else {
                         if (w_ok(w_row)) load_3d_if<kPair>(lead, b, &maps.w128, bar, kx, w_row, c.expert);
-                        if (kGateUp && w_ok(N + w_row))
-                            load_3d_if<kPair>(lead, b + kHalfBytes, &maps.w128, bar, kx, N + w_row, c.expert);
+                        if (halves == 2 && w_ok(w_row + (kGateUp ? N : 128)))
+                            load_3d_if<kPair>(lead, b + kHalfBytes, &maps.w128, bar, kx, w_row + (kGateUp ? N : 128), c.expert);
                     }
                     ++issued;
                     if (++st == S) {
@@ -369,6 +379,46 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
             }
         }
         __syncwarp();
+    } else {
+        // ------------------------------------------------------------ scales
+        // Products of the scales of this CTA's rows (64 a warp) and of the columns, a stage at
+        // a time; the epilogue's wait for a stage is for these too.  Stage n takes the place of
+        // stage n - kRing.  Its sums were made before the epilogue gave back the accumulator of
+        // stage n - kRing + 1, and that before stage n - kRing + 1 + kSlots was multiplied:
+        // so this waits for that product.  (A phase on would need stage n's scales.)
+        constexpr uint32_t kBehind = kRing - 1 - kSlots;
+        const int row0 = 64 * (warp - 2) + lane;
+        float2* out = reinterpret_cast<float2*>(gbase + sp.factor_off) + row0;
+        const int nblocks = static_cast<int>(fp_blocks(cols_w));
+        uint32_t n = 0;
+        bool ok = true;
+        for (int32_t t = unit; ok && t < T; t += units) {
+            const TileCoord c = tile_at(t);
+            const int r0 = 128 * static_cast<int>(rank) + row0;
+            const float* x0 = args.sx + static_cast<int64_t>(c.row0 + (r0 < c.rows ? r0 : 0)) * KB;
+            const float* x1 = args.sx + static_cast<int64_t>(c.row0 + (r0 + 32 < c.rows ? r0 + 32 : 0)) * KB;
+            const float* w0 = args.sw + (static_cast<int64_t>(c.expert) * nblocks + c.col0 / kFpBlock) * KB;
+            const float* w1 = halves_of(c) == 2 ? w0 + static_cast<int64_t>(kGateUp ? N / kFpBlock : 1) * KB : w0;
+            float a0 = x0[0], a1 = x1[0], b0 = w0[0], b1 = w1[0];
+            for (int kb = 0; kb < KB; ++kb, ++n) {
+                const float2 f0 = make_float2(a0 * b0, a0 * b1), f1 = make_float2(a1 * b0, a1 * b1);
+                if (kb + 1 < KB) {
+                    a0 = x0[kb + 1];
+                    a1 = x1[kb + 1];
+                    b0 = w0[kb + 1];
+                    b1 = w1[kb + 1];
+                }
+                if (n >= kBehind && !wait(accf_bar((n - kBehind) % kSlots), ((n - kBehind) / kSlots) & 1u)) {
+                    ok = false;
+                    break;
+                }
+                out[(n % kRing) * 128] = f0;
+                out[(n % kRing) * 128 + 32] = f1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(accf_bar(n % kSlots));
+            }
+        }
+        __syncwarp();
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFpRegsEpi));
@@ -380,69 +430,65 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
         const int part = (warp - 4) >> 2;  // its part of the columns
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         const int r_local = 128 * static_cast<int>(rank) + 32 * q + lane;
-        const int nblocks = static_cast<int>(fp_blocks(cols_w));
+        const float2* factors = reinterpret_cast<const float2*>(gbase + sp.factor_off) + 32 * q + lane;
+        const uint32_t acce0 = kPair ? map_to_rank(acce_bar(0), 0) : acce_bar(0);
         uint32_t n = 0, tiles = 0;
         bool ok = true;
         for (int32_t t = unit; ok && t < T; t += units, ++tiles) {
             const TileCoord c = tile_at(t);
             const bool row_ok = r_local < c.rows;
             const int64_t row = static_cast<int64_t>(c.row0) + r_local;
-            const int halves = halves_of(c);
             const int col = part * kFpCols;  // first column of the thread's sums, in each half
-            // scales: of the row, and of the first and second half's 128 columns
-            const float* sx = args.sx + (row_ok ? row : c.row0) * KB;
-            const float* sw = args.sw + (static_cast<int64_t>(c.expert) * nblocks + c.col0 / kFpBlock) * KB;
-            const float* su = halves == 2 ? sw + static_cast<int64_t>(kGateUp ? N / kFpBlock : 1) * KB : sw;
             uint64_t sums[kHalves * kFpCols / 2];
 #pragma unroll
             for (int i = 0; i < kHalves * kFpCols / 2; ++i) sums[i] = 0u;
-            // two stages ahead
-            float fx0 = sx[0], fw0 = sw[0], fu0 = su[0];
-            float fx1 = KB > 1 ? sx[1] : 0.0f, fw1 = KB > 1 ? sw[1] : 0.0f, fu1 = KB > 1 ? su[1] : 0.0f;
-            for (int kb = 0; ok && kb < KB; ++kb) {
-                const float f[2] = {fx0 * fw0, fx0 * fu0};
-                fx0 = fx1;
-                fw0 = fw1;
-                fu0 = fu1;
-                if (kb + 2 < KB) {
-                    fx1 = sx[kb + 2];
-                    fw1 = sw[kb + 2];
-                    if (kHalves == 2) fu1 = su[kb + 2];
-                }
-                const uint32_t slot = n % kSlots;
-                if (!epi_wait(accf_bar(slot), (n / kSlots) & 1u)) {
-                    ok = false;
-                    break;
-                }
-                ++n;
+            constexpr int kChunks = kHalves * kFpCols / 32, kPerHalf = kFpCols / 32;
+            uint32_t v[2][32];
+            auto load = [&](uint32_t slot, int i) {
+                const uint32_t c0 = slot * kSlotCols + col + 128 * (i / kPerHalf) + 32 * (i % kPerHalf);
+                if (RGG_BOUNDS_OK(tmem_cols_ok(c0, 32, 512), args.status)) tmem_ld_32x32b_x32(t_row + c0, v[i & 1]);
+            };
+            auto full = [&]() -> bool {  // the n-th stage's products are there
+                ok = epi_wait(accf_bar(n % kSlots), (n / kSlots) & 1u);
                 tc_fence_after_sync();
-                // 32 columns at a time, two of them on their way; columns past N hold nothing that is read
-                constexpr int kChunks = kHalves * kFpCols / 32, kPerHalf = kFpCols / 32;
-                uint32_t v[2][32];
-                const uint32_t at = slot * kSlotCols + col;
-                auto load = [&](int i) {
-                    const uint32_t c0 = at + 128 * (i / kPerHalf) + 32 * (i % kPerHalf);
-                    if (RGG_BOUNDS_OK(tmem_cols_ok(c0, 32, 512), args.status)) tmem_ld_32x32b_x32(t_row + c0, v[i & 1]);
-                };
-                load(0);
-                load(1);
+                return ok;
+            };
+            if (!full()) break;
+            load(n % kSlots, 0);
+            load(n % kSlots, 1);
+            float2 factor = factors[(n % kRing) * 128];
+#pragma unroll 1
+            for (int kb = 0; kb < KB; ++kb) {
+                const uint32_t slot = n % kSlots;
+                ++n;
+                float2 next = factor;
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
                     if ((i & 1) == 0) {
                         tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[0][j]), "+r"(v[1][j]));  // not before the wait
-                        if (i + 2 == kChunks) {
+                        if (i + 2 == kChunks) {  // all of the slot has been read
                             tc_fence_before_sync();
                             __syncwarp();
-                            if (lane == 0) arrive_relaxed<kPair>(acce_bar(slot));
+                            if (lane == 0) arrive_relaxed<kPair>(acce0 + 8u * slot);
                         }
                     }
-                    const uint64_t ff = twice(f[i / kPerHalf]);
+                    const uint64_t ff = twice(i / kPerHalf ? factor.y : factor.x);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) add_scaled2(sums[16 * i + j], v[i & 1][2 * j], v[i & 1][2 * j + 1], ff);
-                    if (i + 2 < kChunks) load(i + 2);
+                    if (i + 2 < kChunks) {
+                        load(slot, i + 2);
+                    } else if (kb + 1 < KB) {
+                        if (i + 2 == kChunks) {
+                            if (!full()) break;
+                            next = factors[(n % kRing) * 128];
+                        }
+                        load(n % kSlots, i + 2 - kChunks);
+                    }
                 }
+                if (!ok) break;
+                factor = next;
             }
             if (!ok) break;
             float sum[kHalves * kFpCols];
@@ -524,16 +570,16 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
     }
 }
 
-template <bool kGateUp>
+template <int kShape, bool kGateUp>
 __global__ void __launch_bounds__(kFpThreads, 1)
     grouped_fp8_block_kernel(const __grid_constant__ FpMaps maps, const __grid_constant__ FpArgs args) {
-    fp8_block_tiles<false, kGateUp>(maps, args);
+    fp8_block_tiles<kShape, kGateUp>(maps, args);
 }
 
 template <bool kGateUp>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFpThreads, 1)
     grouped_fp8_block_pair_kernel(const __grid_constant__ FpMaps maps, const __grid_constant__ FpArgs args) {
-    fp8_block_tiles<true, kGateUp>(maps, args);
+    fp8_block_tiles<kFpPair, kGateUp>(maps, args);
 }
 
 }  // namespace rgg

@@ -4,6 +4,7 @@
 #include "rgg_fp8_block.cuh"
 
 #include <algorithm>
+#include <cmath>
 
 #include "rgg_host.h"
 #include "rgg_internal.h"
@@ -39,6 +40,8 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
         return RGG_ERR_INVALID_ARG;
     const int want_bm = opt ? opt->bm : 0, want_stages = opt ? opt->stages : 0, max_ctas = opt ? opt->max_ctas : 0;
     if ((want_bm != 0 && want_bm != 128 && want_bm != 256) || max_ctas < 0) return RGG_ERR_INVALID_ARG;
+    if (opt && opt->bn != 0 && opt->bn != 128 && opt->bn != 256) return RGG_ERR_INVALID_ARG;
+    if (opt && opt->bn == 128 && (want_bm == 256 || gate_up)) return RGG_ERR_INVALID_ARG;
     if (want_stages != 0 && (want_stages < 2 || want_stages > kMaxStages)) return RGG_ERR_INVALID_ARG;
     const HostDevice dev = host_device(h);
     HostDeviceScope scope(dev.device);
@@ -50,15 +53,51 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
     }
 
     const int cap = max_ctas > 0 ? std::min(max_ctas, dev.num_sms) : dev.num_sms;
-    const int64_t avg = (M_tot + E - 1) / E;
-    auto tile_n = [&](int bm) { return gate_up ? 128 : bm; };
-    auto tiles_n = [&](int bm) { return (N + tile_n(bm) - 1) / tile_n(bm); };
-    const int bm = want_bm ? want_bm : (avg > 128 && cap >= 2 ? 256 : 128);
-    const bool pair = bm == 256;
+    const double avg = static_cast<double>(M_tot) / E;
+    auto tile_n = [&](int shape) { return gate_up || shape == kFpNarrow ? 128 : 256; };
+    auto tiles_n = [&](int shape) { return (N + tile_n(shape) - 1) / tile_n(shape); };
+    const int want_bn = opt ? opt->bn : 0;
+    int shape;
+    if (want_bm == 256) {
+        shape = kFpPair;
+    } else if (want_bn == 128 && !gate_up) {
+        shape = kFpNarrow;
+    } else if (want_bn == 256 && want_bm == 128) {
+        shape = kFpWide;
+    } else if (avg <= 128) {
+        // The weights' bytes bound the product, and more, smaller tiles keep all SMs reading (32 experts x 16 rows, 6144 x
+        // 4096: 126 us; wide tiles 129, pairs 150).
+        shape = gate_up ? kFpWide : kFpNarrow;
+    } else {
+        // The shape with the shorter waves.  A tile costs a fixed part and a part per stage, fitted in us to 32 experts x
+        // 1,024 rows of K = 1024 and 6144.  Experts are taken to spread around their mean as choices at random do.  Pairs
+        // move the least bytes a stage; narrow tiles make the most of few; wide ones lose least to experts' last
+        // tiles (32 experts x about 300 rows, 6144 x 4096: 274 us, narrow tiles 314, pairs 335).
+        const double kb = static_cast<double>(fp_blocks(K));
+        const double fixed[3] = {2.6, 1.9, 0.7}, stage[3] = {0.45, 0.468, 0.283};
+        const double spread = std::sqrt(avg);
+        auto tiles_m = [&](double bm) {
+            return (std::ceil((avg - spread) / bm) + std::ceil((avg + spread) / bm)) / 2;
+        };
+        double best = 1e300;
+        shape = kFpWide;
+        for (int s2 = kFpPair; s2 <= kFpNarrow; ++s2) {
+            if ((s2 == kFpPair && (cap < 2 || want_bm == 128)) || (s2 == kFpNarrow && gate_up)) continue;
+            const int units = s2 == kFpPair ? cap / 2 : cap;
+            const double tiles = E * tiles_m(s2 == kFpPair ? 256 : 128) * tiles_n(s2);
+            const double cost = std::max(1.0, std::ceil(tiles / units)) * (fixed[s2] + stage[s2] * kb);
+            if (cost < best) {
+                best = cost;
+                shape = s2;
+            }
+        }
+    }
+    const bool pair = shape == kFpPair;
+    const int bm = pair ? 256 : 128;
     if (pair && cap < 2) return RGG_ERR_INVALID_ARG;
-    const int64_t most = (M_tot / bm + E) * tiles_n(bm);
+    const int64_t most = (M_tot / bm + E) * tiles_n(shape);
     if (most >= (int64_t(1) << 30)) return RGG_ERR_UNSUPPORTED;
-    const uint32_t w_bytes = pair ? fp_w_bytes<true, false>() : gate_up ? fp_w_bytes<false, true>() : fp_w_bytes<false, false>();
+    const uint32_t w_bytes = fp_w_bytes(shape);
     const int64_t fixed = fp_smem(0, E, w_bytes, gate_up).total;
     const int64_t per_stage = static_cast<int64_t>(kFpTile) + w_bytes + 16;
     const int64_t room = static_cast<int64_t>(dev.smem_optin) - 1024 - 16 - fixed;
@@ -88,7 +127,7 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
     a.E = E;
     a.K = K;
     a.N = N;
-    a.n_tiles_n = tiles_n(bm);
+    a.n_tiles_n = tiles_n(shape);
     a.stages = stages;
     a.y_vec32 = (N % 16 == 0 && host_aligned(Y, 32)) ? 1 : 0;
     a.n_major = avg >= 3 * bm ? 1 : 0;  // as the bf16 plan: the tiles that read one weight panel side by side
@@ -96,11 +135,10 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
     a.timeout_ns = (opt && opt->timeout_ns) ? opt->timeout_ns : kHostDefaultTimeoutNs;
     const int grid = static_cast<int>(pair ? 2 * std::max<int64_t>(1, std::min<int64_t>(cap / 2, most))
                                            : std::max<int64_t>(1, std::min<int64_t>(cap, most)));
-    cudaError_t err =
-        pair ? launch_fp8_block(gate_up ? grouped_fp8_block_pair_kernel<true> : grouped_fp8_block_pair_kernel<false>,
-                                grid, smem, st, m, a)
-             : launch_fp8_block(gate_up ? grouped_fp8_block_kernel<true> : grouped_fp8_block_kernel<false>, grid, smem,
-                                st, m, a);
+    auto kernel = pair ? (gate_up ? grouped_fp8_block_pair_kernel<true> : grouped_fp8_block_pair_kernel<false>)
+                  : gate_up ? grouped_fp8_block_kernel<kFpWide, true>
+                  : shape == kFpWide ? grouped_fp8_block_kernel<kFpWide, false> : grouped_fp8_block_kernel<kFpNarrow, false>;
+    cudaError_t err = launch_fp8_block(kernel, grid, smem, st, m, a);
     return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, "grouped_gemm_fp8_block launch");
 }
 

@@ -193,6 +193,15 @@ def test_gate_up(K, N, bm):
     assert bool((scales[:a] == 77).all()) and bool((scales[b:] == 77).all())
 
 
+@pytest.mark.parametrize("K,N", [(16, 8), (144, 264), (528, 392), (1040, 200), (256, 512)])
+@pytest.mark.parametrize("bn", [128, 256])
+def test_single_cta_tiles(K, N, bn):
+    x, w, off, offg = _product_case(COUNTS, K, N, seed=K + N)
+    Y = _canary(len(x[0]), N)
+    rgg.rgg_grouped_gemm_fp8_block(*x, *w, offg, Y, bm=128, bn=bn, check=True)
+    _check(Y, *_reference(x, w, off), off, K)
+
+
 @pytest.mark.parametrize("gate_up", [False, True])
 @pytest.mark.parametrize("counts", [[1], [0, 0, 5], [1] * 70, [600], [256] * 4, [3, 1500, 2, 90]])
 def test_routings(counts, gate_up):

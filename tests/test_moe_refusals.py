@@ -173,5 +173,5 @@ def test_product_arguments(lib, gate_up):
     assert call(E=4097) == UNSUPPORTED
     if gate_up:
         assert call(N=64) == call(hs=None) == call(hs=P + 2) == call(N=2 ** 30) == INVALID
-    for kw in ({"bm": 64}, {"bm": 192}, {"max_ctas": -1}, {"stages": 1}, {"stages": 17}):
+    for kw in ({"bn": 64}, {"bm": 256, "bn": 128}, {"bm": 64}, {"bm": 192}, {"max_ctas": -1}, {"stages": 1}, {"stages": 17}):
         assert call(opt=ctypes.byref(rgg._options(**kw)[0])) == INVALID, kw

@@ -10,11 +10,15 @@
 // of the choices: no atomics, equal calls give equal bits.  Choices without a row
 // (position -1) add nothing; rows of no choice are left alone.  Bound by memory.
 //
-// A warp takes a token and a part of its row; the widest loads and stores that the
-// row's size and the pointers' alignment allow.
+// Rows move in blocks of 16 bytes, aligned where they are written.  Where rows are not
+// whole 16 bytes (an odd width), a block that is read starts anywhere: two aligned
+// loads and a funnel shift, the same for a whole row, give it; the first and last
+// blocks of a written row are stored element by element.  (2693 columns, 8,192 tokens
+// x 6, forward and backward: element-wise loads and stores took 308 us.)
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "rgg_host.h"
 #include "rgg_internal.h"
@@ -23,102 +27,195 @@
 namespace rgg {
 
 constexpr int kDispatchLoads = 4;  // in flight a lane
-constexpr int kCombineCols = 8;    // columns a lane
-constexpr int kCombineSeg = 32 * kCombineCols;
-constexpr int kGradThreads = 128;
-constexpr int kGradChoices = 8;    // choices whose sums a thread holds at a time
+constexpr int kFlight = 4;         // choices whose loads are in flight together
+// Blocks that a lane combines at a time: shifted ones take twice the registers.
+__host__ __device__ constexpr int combine_steps(bool whole) { return whole ? 2 : 1; }
 
-// V: uint4, uint2, uint32_t, uint16_t or uint8_t; row_v: a row in those.
-template <typename V>
+// A tensor's bytes, for loads that may not leave them.
+struct Span {
+    uintptr_t begin, end;
+};
+
+// The 16 bytes at `at`, those outside the span 0.  For the few rows at a tensor's ends: a call, so that the
+// other rows' code has the registers to itself.
+__device__ __noinline__ uint4 load_edge(uintptr_t at, uintptr_t begin, uintptr_t end) {
+    uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+    for (int i = 15; i >= 0; --i) {
+        hi = (hi << 8) | (lo >> 56);
+        lo <<= 8;
+        if (at + i >= begin && at + i < end) lo |= *reinterpret_cast<const uint8_t*>(at + i);
+    }
+    return make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                      static_cast<uint32_t>(hi >> 32));
+}
+
+// How a block of 16 bytes is read: aligned; from two aligned neighbours; byte by byte, where the
+// neighbours may be outside the tensor.
+constexpr int kAligned = 0, kShifted = 1, kEdge = 2;
+
+// The block, or (kShifted) the two aligned ones that it is in.
+struct Block16 {
+    uint4 lo, hi;
+};
+template <int kMode>
+__device__ __forceinline__ Block16 load_block(uintptr_t at, Span in) {
+    Block16 b;
+    if constexpr (kMode == kEdge) {
+        b.lo = load_edge(at, in.begin, in.end);
+    } else if constexpr (kMode == kShifted) {
+        const uint4* first = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+        b.lo = __ldg(first);
+        b.hi = __ldg(first + 1);
+    } else {
+        b.lo = __ldg(reinterpret_cast<const uint4*>(at));
+    }
+    return b;
+}
+// Whether all blocks that overlap a row, the one before it and the two behind it are inside the tensor.
+__device__ __forceinline__ bool row_inside(uintptr_t row, int64_t bytes, Span in) {
+    return row >= in.begin + 32 && row + bytes + 48 <= in.end;
+}
+template <int kMode>
+__device__ __forceinline__ uint4 shift_block(const Block16& b, uint32_t shift) {
+    if constexpr (kMode != kShifted) return b.lo;
+    const uint32_t bits = 8 * (shift & 3);
+    auto take = [&](uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t w4) {
+        return make_uint4(__funnelshift_r(w0, w1, bits), __funnelshift_r(w1, w2, bits), __funnelshift_r(w2, w3, bits),
+                          __funnelshift_r(w3, w4, bits));
+    };
+    switch (shift >> 2) {  // the same in all lanes of a row
+        case 0: return take(b.lo.x, b.lo.y, b.lo.z, b.lo.w, b.hi.x);  // by 0 bits: the first itself
+        case 1: return take(b.lo.y, b.lo.z, b.lo.w, b.hi.x, b.hi.y);
+        case 2: return take(b.lo.z, b.lo.w, b.hi.x, b.hi.y, b.hi.z);
+        default: return take(b.lo.w, b.hi.x, b.hi.y, b.hi.z, b.hi.w);
+    }
+}
+
+// The aligned blocks of a row [row, row + bytes): the b-th starts `at(b)` bytes into it (the first may be before it).
+struct RowBlocks {
+    int64_t bytes, lead;
+    __device__ __forceinline__ RowBlocks(uintptr_t row, int64_t bytes_) : bytes(bytes_), lead(row & 15) {}
+    __device__ __forceinline__ int64_t count() const { return (bytes + lead + 15) / 16; }
+    __device__ __forceinline__ int64_t at(int64_t b) const { return 16 * b - lead; }
+    __device__ __forceinline__ bool whole(int64_t off) const { return off >= 0 && off + 16 <= bytes; }
+};
+inline __host__ __device__ int64_t most_blocks(int64_t bytes, bool aligned) { return aligned ? bytes / 16 : (bytes + 15) / 16 + 1; }
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// Eight values, rounded, to the block `off` bytes into a row; a block that is not whole element by element.
+template <int kMode>
+__device__ __forceinline__ void store8(uintptr_t row, int64_t off, const RowBlocks& blocks, const float (&x)[8]) {
+    const uint32_t w[4] = {pack_bf16x2(__float_as_uint(x[0]), __float_as_uint(x[1])),
+                           pack_bf16x2(__float_as_uint(x[2]), __float_as_uint(x[3])),
+                           pack_bf16x2(__float_as_uint(x[4]), __float_as_uint(x[5])),
+                           pack_bf16x2(__float_as_uint(x[6]), __float_as_uint(x[7]))};
+    if (kMode == kAligned || blocks.whole(off)) {
+        *reinterpret_cast<uint4*>(row + off) = make_uint4(w[0], w[1], w[2], w[3]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (off + 2 * i >= 0 && off + 2 * i < blocks.bytes)
+            *reinterpret_cast<uint16_t*>(row + off + 2 * i) = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+}
+
+template <bool kWhole>
 __global__ void __launch_bounds__(kRowThreads)
-    dispatch_kernel(const V* __restrict__ X, const int32_t* __restrict__ position, int64_t T, int k, int64_t row_v,
-                    int64_t rows, V* __restrict__ out, int32_t* status) {
+    dispatch_kernel(uintptr_t X, const int32_t* __restrict__ position, int64_t T, int k, int64_t row_bytes, int64_t rows,
+                    uintptr_t out, int32_t* status) {
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int32_t segs = static_cast<int32_t>((row_v + 32 * kDispatchLoads - 1) / (32 * kDispatchLoads));
+    const int64_t most = most_blocks(row_bytes, kWhole);
+    const int32_t segs = static_cast<int32_t>((most + 32 * kDispatchLoads - 1) / (32 * kDispatchLoads));
+    const Span span{X, X + T * row_bytes};
     for (RowItems it(T, segs); it.left(); it.next()) {
         const int64_t t = it.token();
-        const int64_t c = (it.item - t * segs) * (32 * kDispatchLoads) + lane;
-        V v[kDispatchLoads];
-#pragma unroll
-        for (int u = 0; u < kDispatchLoads; ++u)
-            if (c + 32 * u < row_v) v[u] = X[t * row_v + c + 32 * u];
-        for (int j = 0; j < k; ++j) {
-            const int32_t p = checked_row(position[t * k + j], rows, status);
-            if (p < 0) continue;
+        const int64_t b0 = (it.item - t * segs) * (32 * kDispatchLoads) + lane;
+        const uintptr_t from = X + t * row_bytes;
+        if constexpr (kWhole) {
+            uint4 v[kDispatchLoads];
 #pragma unroll
             for (int u = 0; u < kDispatchLoads; ++u)
-                if (c + 32 * u < row_v) out[p * row_v + c + 32 * u] = v[u];
+                if (b0 + 32 * u < most) v[u] = __ldg(reinterpret_cast<const uint4*>(from) + b0 + 32 * u);
+            for (int j = 0; j < k; ++j) {
+                const int32_t p = checked_row(position[t * k + j], rows, status);
+                if (p < 0) continue;
+                uint4* to = reinterpret_cast<uint4*>(out + p * row_bytes) + b0;
+#pragma unroll
+                for (int u = 0; u < kDispatchLoads; ++u)
+                    if (b0 + 32 * u < most) to[32 * u] = v[u];
+            }
+        } else {
+            auto copy = [&](auto mode, int32_t p) {
+                constexpr int kMode = decltype(mode)::value;
+                const uintptr_t to = out + p * row_bytes;
+                const RowBlocks blocks(to, row_bytes);
+                const uint32_t shift = static_cast<uint32_t>(from - blocks.lead) & 15u;
+                const int64_t count = blocks.count();
+                Block16 v[kDispatchLoads];
+#pragma unroll
+                for (int u = 0; u < kDispatchLoads; ++u)
+                    if (b0 + 32 * u < count) v[u] = load_block<kMode>(from + blocks.at(b0 + 32 * u), span);
+#pragma unroll
+                for (int u = 0; u < kDispatchLoads; ++u) {
+                    const int64_t off = blocks.at(b0 + 32 * u);
+                    if (b0 + 32 * u >= count) continue;
+                    const uint4 x = shift_block<kMode>(v[u], shift);
+                    if (blocks.whole(off)) {
+                        *reinterpret_cast<uint4*>(to + off) = x;
+                    } else {
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (off + i >= 0 && off + i < row_bytes)
+                                *reinterpret_cast<uint8_t*>(to + off + i) = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+                    }
+                }
+            };
+            const bool inside = row_inside(from, row_bytes, span);
+            for (int j = 0; j < k; ++j) {
+                const int32_t p = checked_row(position[t * k + j], rows, status);
+                if (p < 0) continue;
+                if (inside) copy(std::integral_constant<int, kShifted>(), p);
+                else copy(std::integral_constant<int, kEdge>(), p);
+            }
         }
     }
 }
 
-// kVec bf16 values in a load or store.
-template <int kVec>
-struct Bf16Vec;
-template <>
-struct Bf16Vec<8> {
-    using type = uint4;
-};
-template <>
-struct Bf16Vec<4> {
-    using type = uint2;
-};
-template <>
-struct Bf16Vec<2> {
-    using type = uint32_t;
-};
-template <>
-struct Bf16Vec<1> {
-    using type = uint16_t;
-};
-
-template <int kVec>
-__device__ __forceinline__ void bf16_values(const typename Bf16Vec<kVec>::type& v, float* x) {
-    if constexpr (kVec == 1) {
-        x[0] = __uint_as_float(static_cast<uint32_t>(v) << 16);
-    } else {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-#pragma unroll
-        for (int i = 0; i < kVec / 2; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-}
-
-template <int kVec>
-__device__ __forceinline__ typename Bf16Vec<kVec>::type bf16_pack(const float* x) {
-    typename Bf16Vec<kVec>::type v;
-    if constexpr (kVec == 1) {
-        v = __bfloat16_as_ushort(__float2bfloat16_rn(x[0]));
-    } else {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-        for (int i = 0; i < kVec / 2; ++i) w[i] = pack_bf16x2(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]));
-    }
-    return v;
-}
-
-template <int kVec>
-__global__ void __launch_bounds__(kRowThreads)
-    combine_kernel(const __nv_bfloat16* __restrict__ Y, const int32_t* __restrict__ position,
-                   const float* __restrict__ weights, int64_t T, int k, int64_t rows, int64_t N,
-                   __nv_bfloat16* __restrict__ out, int32_t* status) {
-    using V = typename Bf16Vec<kVec>::type;
-    constexpr int kLoads = kCombineCols / kVec;
-    constexpr int kFlight = 4;  // choices whose loads are in flight together
+// A warp takes kSteps times 32 blocks of a token's row.
+template <bool kWhole>
+__global__ void __launch_bounds__(kRowThreads, 3)
+    combine_kernel(uintptr_t Y, const int32_t* __restrict__ position, const float* __restrict__ weights, int64_t T, int k,
+                   int64_t rows, int64_t N, uintptr_t out, int32_t* status) {
+    constexpr int kSteps = combine_steps(kWhole);
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int32_t segs = static_cast<int32_t>((N + kCombineSeg - 1) / kCombineSeg);
+    const int64_t bytes = 2 * N;
+    const int32_t segs = static_cast<int32_t>((most_blocks(bytes, kWhole) + 32 * kSteps - 1) / (32 * kSteps));
+    const Span span{Y, Y + rows * bytes};
     for (RowItems it(T, segs); it.left(); it.next()) {
         const int64_t t = it.token();
-        const int64_t c = (it.item - t * segs) * kCombineSeg + lane * kVec;
-        float acc[kCombineCols];
+        const uintptr_t to = out + t * bytes;
+        const RowBlocks blocks(to, bytes);
+        const int64_t count = blocks.count();
+        const int64_t b0 = (it.item - t * segs) * (32 * kSteps) + lane;
+        float acc[kSteps][8];
 #pragma unroll
-        for (int i = 0; i < kCombineCols; ++i) acc[i] = 0.0f;
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[s][i] = 0.0f;
         for (int k0 = 0; k0 < k; k0 += 32) {
             int32_t p = -1;  // lane j: choice k0 + j
             float w = 0.0f;
@@ -127,118 +224,126 @@ __global__ void __launch_bounds__(kRowThreads)
                 w = weights ? weights[t * k + k0 + lane] : 1.0f;
             }
             const int here = min(32, k - k0);
-            for (int j0 = 0; j0 < here; j0 += kFlight) {
-                V v[kFlight][kLoads];
-                int32_t pj[kFlight];
+            bool inside = true;
+            if constexpr (!kWhole) inside = __all_sync(0xffffffffu, p < 0 || row_inside(Y + p * bytes, bytes, span));
+            auto add = [&](auto mode) {
+                constexpr int kMode = decltype(mode)::value;
+                for (int j0 = 0; j0 < here; j0 += kFlight) {
+                    Block16 v[kFlight][kSteps];
+                    int32_t pj[kFlight];
 #pragma unroll
-                for (int j = 0; j < kFlight; ++j) {
-                    pj[j] = __shfl_sync(0xffffffffu, p, (j0 + j) & 31);
-                    if (j0 + j >= here) pj[j] = -1;
-                    if (pj[j] < 0) continue;
-                    const __nv_bfloat16* row = Y + pj[j] * N;
+                    for (int j = 0; j < kFlight; ++j) {
+                        pj[j] = __shfl_sync(0xffffffffu, p, (j0 + j) & 31);
+                        if (j0 + j >= here) pj[j] = -1;
+                        if (pj[j] < 0) continue;
 #pragma unroll
-                    for (int u = 0; u < kLoads; ++u)
-                        if (c + 32 * kVec * u < N) v[j][u] = *reinterpret_cast<const V*>(row + c + 32 * kVec * u);
-                }
+                        for (int s = 0; s < kSteps; ++s)
+                            if (b0 + 32 * s < count) v[j][s] = load_block<kMode>(Y + pj[j] * bytes + blocks.at(b0 + 32 * s), span);
+                    }
 #pragma unroll
-                for (int j = 0; j < kFlight; ++j) {
-                    const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
-                    if (pj[j] < 0) continue;
+                    for (int j = 0; j < kFlight; ++j) {
+                        const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+                        if (pj[j] < 0) continue;
+                        const uint32_t shift = static_cast<uint32_t>(Y + pj[j] * bytes - blocks.lead) & 15u;
 #pragma unroll
-                    for (int u = 0; u < kLoads; ++u) {
-                        if (c + 32 * kVec * u >= N) continue;
-                        float x[kVec];
-                        bf16_values<kVec>(v[j][u], x);
+                        for (int s = 0; s < kSteps; ++s) {
+                            float x[8];
+                            unpack8(shift_block<kMode>(v[j][s], shift), x);
 #pragma unroll
-                        for (int i = 0; i < kVec; ++i) acc[u * kVec + i] += wj * x[i];
+                            for (int i = 0; i < 8; ++i) acc[s][i] += wj * x[i];
+                        }
                     }
                 }
-            }
+            };
+            if constexpr (kWhole) add(std::integral_constant<int, kAligned>());
+            else if (inside) add(std::integral_constant<int, kShifted>());
+            else add(std::integral_constant<int, kEdge>());
         }
 #pragma unroll
-        for (int u = 0; u < kLoads; ++u)
-            if (c + 32 * kVec * u < N)
-                *reinterpret_cast<V*>(out + t * N + c + 32 * kVec * u) = bf16_pack<kVec>(acc + u * kVec);
+        for (int s = 0; s < kSteps; ++s)
+            if (b0 + 32 * s < count) store8<kWhole ? kAligned : kShifted>(to, blocks.at(b0 + 32 * s), blocks, acc[s]);
     }
 }
 
-// A block takes a token: its threads walk the columns and hold their parts of the
-// choices' sums, which the block then adds in a fixed order.
-template <int kVec>
-__global__ void __launch_bounds__(kGradThreads)
-    combine_backward_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* __restrict__ Y,
-                            const int32_t* __restrict__ position, const float* __restrict__ weights, int64_t T, int k,
-                            int64_t rows, int64_t N, __nv_bfloat16* __restrict__ dY, float* __restrict__ dweights,
-                            int32_t* status) {
-    using V = typename Bf16Vec<kVec>::type;
-    __shared__ float s_part[kGradThreads / 32][kGradChoices];
+// A warp takes a choice and walks its row: the dot product in its lanes, added in a
+// fixed order, and the scaled gradient.  The warps of a token's choices are neighbours, so
+// its gradient comes from memory once.
+template <bool kWhole>
+__global__ void __launch_bounds__(kRowThreads, 3)
+    combine_backward_kernel(uintptr_t dout, uintptr_t Y, const int32_t* __restrict__ position,
+                            const float* __restrict__ weights, int64_t T, int k, int64_t rows, int64_t N, uintptr_t dY,
+                            float* __restrict__ dweights, int32_t* status) {
+    constexpr int kLoads = 2;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-        for (int k0 = 0; k0 < k; k0 += kGradChoices) {
-            int32_t p[kGradChoices];
-            float w[kGradChoices], sum[kGradChoices];
+    const int lane = threadIdx.x & 31;
+    const int64_t bytes = 2 * N;
+    const Span d_span{dout, dout + T * bytes}, y_span{Y, Y + rows * bytes};
+    for (RowItems it(T, k); it.left(); it.next()) {
+        const int64_t t = it.token();
+        const int32_t p = checked_row(position[it.item], rows, status);
+        float sum = 0.0f;
+        if (p >= 0) {
+            const float w = weights[it.item];
+            const uintptr_t d_row = dout + t * bytes, y_row = Y + p * bytes, to = dY + p * bytes;
+            const RowBlocks blocks(dY ? to : y_row, bytes);
+            const uint32_t d_shift = static_cast<uint32_t>(d_row - blocks.lead) & 15u;
+            const uint32_t y_shift = static_cast<uint32_t>(y_row - blocks.lead) & 15u;
+            const int64_t count = blocks.count();
+            auto walk = [&](auto d_mode, auto y_mode) {
+                constexpr int kD = decltype(d_mode)::value, kY = decltype(y_mode)::value;
+                for (int64_t b0 = lane; b0 < count; b0 += 32 * kLoads) {
+                    Block16 dv[kLoads], yv[kLoads];
 #pragma unroll
-            for (int j = 0; j < kGradChoices; ++j) {
-                p[j] = k0 + j < k ? checked_row(position[t * k + k0 + j], rows, status) : -1;
-                w[j] = p[j] >= 0 ? weights[t * k + k0 + j] : 0.0f;
-                sum[j] = 0.0f;
-            }
-            for (int64_t c = static_cast<int64_t>(threadIdx.x) * kVec; c < N; c += kGradThreads * kVec) {
-                float d[kVec];
-                bf16_values<kVec>(*reinterpret_cast<const V*>(dout + t * N + c), d);
-                V v[kGradChoices];
-#pragma unroll
-                for (int j = 0; j < kGradChoices; ++j)
-                    if (p[j] >= 0) v[j] = *reinterpret_cast<const V*>(Y + p[j] * N + c);
-#pragma unroll
-                for (int j = 0; j < kGradChoices; ++j) {
-                    if (p[j] < 0) continue;
-                    float y[kVec], g[kVec];
-                    bf16_values<kVec>(v[j], y);
-#pragma unroll
-                    for (int i = 0; i < kVec; ++i) {
-                        sum[j] += d[i] * y[i];
-                        g[i] = w[j] * d[i];
+                    for (int u = 0; u < kLoads; ++u) {
+                        const int64_t off = blocks.at(b0 + 32 * u);
+                        if (b0 + 32 * u >= count) continue;
+                        yv[u] = load_block<kY>(y_row + off, y_span);
+                        dv[u] = load_block<kD>(d_row + off, d_span);
                     }
-                    if (dY) *reinterpret_cast<V*>(dY + p[j] * N + c) = bf16_pack<kVec>(g);
+#pragma unroll
+                    for (int u = 0; u < kLoads; ++u) {
+                        const int64_t off = blocks.at(b0 + 32 * u);
+                        if (b0 + 32 * u >= count) continue;
+                        float d[8], y[8];
+                        unpack8(shift_block<kD>(dv[u], d_shift), d);
+                        unpack8(shift_block<kY>(yv[u], y_shift), y);
+                        if (!kWhole && !blocks.whole(off)) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (off + 2 * i < 0 || off + 2 * i >= bytes) d[i] = y[i] = 0.0f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            sum += d[i] * y[i];
+                            d[i] *= w;
+                        }
+                        if (dY) store8<kWhole ? kAligned : kShifted>(to, off, blocks, d);
+                    }
                 }
-            }
-            if (!dweights) continue;
-#pragma unroll
-            for (int j = 0; j < kGradChoices; ++j) {
-#pragma unroll
-                for (int s = 16; s > 0; s >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], s);
-                if (lane == 0) s_part[warp][j] = sum[j];
-            }
-            __syncthreads();
-            if (threadIdx.x < kGradChoices && k0 + static_cast<int>(threadIdx.x) < k) {
-                float all = 0.0f;
-#pragma unroll
-                for (int i = 0; i < kGradThreads / 32; ++i) all += s_part[i][threadIdx.x];
-                dweights[t * k + k0 + threadIdx.x] = all;
-            }
-            __syncthreads();
+            };
+            using Shifted = std::integral_constant<int, kShifted>;
+            using Aligned = std::integral_constant<int, kAligned>;
+            using Edge = std::integral_constant<int, kEdge>;
+            if constexpr (kWhole) walk(Aligned(), Aligned());
+            else if (!row_inside(d_row, bytes, d_span) || !row_inside(y_row, bytes, y_span)) walk(Edge(), Edge());
+            else if (y_shift == 0) walk(Shifted(), Aligned());  // dY and Y alike: its blocks are Y's own
+            else walk(Shifted(), Shifted());
         }
+        if (!dweights) continue;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        if (lane == 0) dweights[it.item] = sum;
     }
 }
 
-template <typename V>
-static cudaError_t launch_dispatch(const void* X, const int32_t* position, int64_t T, int k, int64_t row_bytes,
-                                   int64_t rows, void* out, int32_t* status, cudaStream_t st) {
-    const int64_t row_v = row_bytes / static_cast<int64_t>(sizeof(V));
-    const int64_t segs = (row_v + 32 * kDispatchLoads - 1) / (32 * kDispatchLoads);
-    return launch_chained(dispatch_kernel<V>, row_grid(T * segs, kRowThreads), kRowThreads, 0, st,
-                          static_cast<const V*>(X), position, T, k, row_v, rows, static_cast<V*>(out), status);
-}
-
-// The widest of 16, 8, 4, 2 and 1 bytes that divides a row and all addresses.
-static int common_width(int64_t row_bytes, std::initializer_list<const void*> p) {
-    uintptr_t all = static_cast<uintptr_t>(row_bytes) | 16u;
+// Whether rows of that size at these addresses are whole, aligned 16 bytes.
+static bool rows_aligned(int64_t row_bytes, std::initializer_list<const void*> p) {
+    uintptr_t all = static_cast<uintptr_t>(row_bytes);
     for (const void* q : p) all |= reinterpret_cast<uintptr_t>(q);
-    return static_cast<int>(all & (~all + 1));
+    return (all & 15u) == 0;
 }
+static uintptr_t address(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
 // 0 <= T, rows < 2^31, 1 <= k, 1 <= row < 2^31.
 static bool rows_ok(int64_t T, int k, int64_t rows, int64_t row) {
@@ -259,14 +364,11 @@ extern "C" rgg_status rgg_dispatch(rgg_handle* h, const void* X, const int32_t* 
     HostDeviceScope scope(dev.device);
     if (scope.error() != cudaSuccess) return host_cuda_failure(scope.error(), "cudaSetDevice");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t err;
-    switch (common_width(row_bytes, {X, out})) {
-        case 16: err = launch_dispatch<uint4>(X, position, T, k, row_bytes, rows, out, dev.status, st); break;
-        case 8: err = launch_dispatch<uint2>(X, position, T, k, row_bytes, rows, out, dev.status, st); break;
-        case 4: err = launch_dispatch<uint32_t>(X, position, T, k, row_bytes, rows, out, dev.status, st); break;
-        case 2: err = launch_dispatch<uint16_t>(X, position, T, k, row_bytes, rows, out, dev.status, st); break;
-        default: err = launch_dispatch<uint8_t>(X, position, T, k, row_bytes, rows, out, dev.status, st); break;
-    }
+    const bool aligned = rows_aligned(row_bytes, {X, out});
+    const int64_t segs = (most_blocks(row_bytes, aligned) + 32 * kDispatchLoads - 1) / (32 * kDispatchLoads);
+    cudaError_t err = launch_chained(aligned ? dispatch_kernel<true> : dispatch_kernel<false>,
+                                     row_grid(T * segs, kRowThreads), kRowThreads, 0, st, address(X), position, T, k,
+                                     row_bytes, rows, address(out), dev.status);
     return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, "dispatch launch");
 }
 
@@ -281,12 +383,11 @@ extern "C" rgg_status rgg_combine(rgg_handle* h, const void* Y, const int32_t* p
     HostDeviceScope scope(dev.device);
     if (scope.error() != cudaSuccess) return host_cuda_failure(scope.error(), "cudaSetDevice");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int width = common_width(2 * N, {Y, out});
-    const int grid = row_grid(T * ((N + kCombineSeg - 1) / kCombineSeg), kRowThreads);
-    auto kernel = width == 16 ? combine_kernel<8> : width == 8 ? combine_kernel<4>
-                  : width == 4 ? combine_kernel<2> : combine_kernel<1>;
-    cudaError_t err = launch_chained(kernel, grid, kRowThreads, 0, st, static_cast<const __nv_bfloat16*>(Y), position,
-                                     weights, T, k, rows, N, static_cast<__nv_bfloat16*>(out), dev.status);
+    const bool aligned = rows_aligned(2 * N, {Y, out});
+    const int64_t segs = (most_blocks(2 * N, aligned) + 32 * combine_steps(aligned) - 1) / (32 * combine_steps(aligned));
+    cudaError_t err = launch_chained(aligned ? combine_kernel<true> : combine_kernel<false>, row_grid(T * segs, kRowThreads),
+                                     kRowThreads, 0, st, address(Y), position, weights, T, k, rows, N, address(out),
+                                     dev.status);
     return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, "combine launch");
 }
 
@@ -302,11 +403,9 @@ extern "C" rgg_status rgg_combine_backward(rgg_handle* h, const void* dout, cons
     HostDeviceScope scope(dev.device);
     if (scope.error() != cudaSuccess) return host_cuda_failure(scope.error(), "cudaSetDevice");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int width = common_width(2 * N, {dout, Y, dY});
-    auto kernel = width == 16 ? combine_backward_kernel<8> : width == 8 ? combine_backward_kernel<4>
-                  : width == 4 ? combine_backward_kernel<2> : combine_backward_kernel<1>;
-    cudaError_t err = launch_chained(kernel, static_cast<int>(T), kGradThreads, 0, st,
-                                     static_cast<const __nv_bfloat16*>(dout), static_cast<const __nv_bfloat16*>(Y),
-                                     position, weights, T, k, rows, N, static_cast<__nv_bfloat16*>(dY), dweights, dev.status);
+    const bool aligned = rows_aligned(2 * N, {dout, Y, dY});
+    cudaError_t err = launch_chained(aligned ? combine_backward_kernel<true> : combine_backward_kernel<false>,
+                                     row_grid(T * k, kRowThreads), kRowThreads, 0, st, address(dout), address(Y), position,
+                                     weights, T, k, rows, N, address(dY), dweights, dev.status);
     return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, "combine_backward launch");
 }

@@ -80,13 +80,18 @@ __global__ void __launch_bounds__(1024)
     }
     if (bad) atomicCAS(status, 0, kRowStatusBadIndex);
     if (counts) {
-        const int64_t all = static_cast<int64_t>(gridDim.x) * E, before = static_cast<int64_t>(blockIdx.x) * E;
-        for (int64_t i = threadIdx.x; i < all; i += blockDim.x) {
-            const int32_t c = counts[i];
-            if (c == 0) continue;
-            const int e = static_cast<int>(i % E);
-            atomicAdd(&s_start[e], c);
-            if (i < before) atomicAdd(&s_before[e], c);
+        // as many rows of the counts at a time as the block has threads for
+        const int at_once = max(1, static_cast<int>(blockDim.x) / E);
+        for (int i = threadIdx.x; i < at_once * E; i += blockDim.x) {
+            const int row = i / E, e = i - row * E;
+            int32_t all = 0, before = 0;
+            for (int b = row; b < static_cast<int>(gridDim.x); b += at_once) {
+                const int32_t c = counts[b * E + e];
+                all += c;
+                if (b < static_cast<int>(blockIdx.x)) before += c;
+            }
+            if (all) atomicAdd(&s_start[e], all);
+            if (before) atomicAdd(&s_before[e], before);
         }
     }
     __syncthreads();

@@ -11,9 +11,10 @@
 // (position -1) add nothing; rows of no choice are left alone.  Bound by memory.
 //
 // Rows move in blocks of 16 bytes, aligned where they are written.  Where rows are not
-// whole 16 bytes (an odd width), a block that is read starts anywhere: two aligned
-// loads and a funnel shift, the same for a whole row, give it; the first and last
-// blocks of a written row are stored element by element.  (2693 columns, 8,192 tokens
+// whole 16 bytes (an odd width), a block that is read starts anywhere: it is put together
+// from an aligned one and the next lane's, by a funnel shift that is the same for a whole
+// row (so 32 lanes give 31 blocks); the first and last blocks of a written row are stored
+// element by element.  (2693 columns, 8,192 tokens
 // x 6, forward and backward: element-wise loads and stores took 308 us.)
 #include <cuda_bf16.h>
 
@@ -28,8 +29,7 @@ namespace rgg {
 
 constexpr int kDispatchLoads = 4;  // in flight a lane
 constexpr int kFlight = 4;         // choices whose loads are in flight together
-// Blocks that a lane combines at a time: shifted ones take twice the registers.
-__host__ __device__ constexpr int combine_steps(bool whole) { return whole ? 2 : 1; }
+constexpr int kCombineSteps = 2;   // blocks that a lane combines at a time
 
 // A tensor's bytes, for loads that may not leave them.
 struct Span {
@@ -50,47 +50,38 @@ __device__ __noinline__ uint4 load_edge(uintptr_t at, uintptr_t begin, uintptr_t
                       static_cast<uint32_t>(hi >> 32));
 }
 
-// How a block of 16 bytes is read: aligned; from two aligned neighbours; byte by byte, where the
-// neighbours may be outside the tensor.
+// How a block of 16 bytes is read: aligned; from an aligned one and the next lane's; byte by
+// byte, where those may be outside the tensor.
 constexpr int kAligned = 0, kShifted = 1, kEdge = 2;
 
-// The block, or (kShifted) the two aligned ones that it is in.
-struct Block16 {
-    uint4 lo, hi;
-};
 template <int kMode>
-__device__ __forceinline__ Block16 load_block(uintptr_t at, Span in) {
-    Block16 b;
-    if constexpr (kMode == kEdge) {
-        b.lo = load_edge(at, in.begin, in.end);
-    } else if constexpr (kMode == kShifted) {
-        const uint4* first = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
-        b.lo = __ldg(first);
-        b.hi = __ldg(first + 1);
-    } else {
-        b.lo = __ldg(reinterpret_cast<const uint4*>(at));
-    }
-    return b;
+__device__ __forceinline__ uint4 load_block(uintptr_t at, Span in) {
+    if constexpr (kMode == kEdge) return load_edge(at, in.begin, in.end);
+    else return __ldg(reinterpret_cast<const uint4*>(kMode == kShifted ? at & ~static_cast<uintptr_t>(15) : at));
 }
-// Whether all blocks that overlap a row, the one before it and the two behind it are inside the tensor.
+// Whether the aligned blocks around a row are inside the tensor: all that a lane loads of it, or the lane before it needs.
 __device__ __forceinline__ bool row_inside(uintptr_t row, int64_t bytes, Span in) {
     return row >= in.begin + 32 && row + bytes + 48 <= in.end;
 }
+// kShifted: the 16 bytes that start `shift` bytes (the same in all lanes) into v, the next lane's v behind it.  Whole warp.
 template <int kMode>
-__device__ __forceinline__ uint4 shift_block(const Block16& b, uint32_t shift) {
-    if constexpr (kMode != kShifted) return b.lo;
+__device__ __forceinline__ uint4 shift_block(const uint4& v, uint32_t shift) {
+    if constexpr (kMode != kShifted) return v;
     const uint32_t bits = 8 * (shift & 3);
+    auto next = [](uint32_t w) { return __shfl_down_sync(0xffffffffu, w, 1); };
     auto take = [&](uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t w4) {
         return make_uint4(__funnelshift_r(w0, w1, bits), __funnelshift_r(w1, w2, bits), __funnelshift_r(w2, w3, bits),
                           __funnelshift_r(w3, w4, bits));
     };
-    switch (shift >> 2) {  // the same in all lanes of a row
-        case 0: return take(b.lo.x, b.lo.y, b.lo.z, b.lo.w, b.hi.x);  // by 0 bits: the first itself
-        case 1: return take(b.lo.y, b.lo.z, b.lo.w, b.hi.x, b.hi.y);
-        case 2: return take(b.lo.z, b.lo.w, b.hi.x, b.hi.y, b.hi.z);
-        default: return take(b.lo.w, b.hi.x, b.hi.y, b.hi.z, b.hi.w);
+    switch (shift >> 2) {
+        case 0: return shift == 0 ? v : take(v.x, v.y, v.z, v.w, next(v.x));
+        case 1: return take(v.y, v.z, v.w, next(v.x), next(v.y));
+        case 2: return take(v.z, v.w, next(v.x), next(v.y), next(v.z));
+        default: return take(v.w, next(v.x), next(v.y), next(v.z), next(v.w));
     }
 }
+// Blocks that a warp's lanes give.
+__host__ __device__ constexpr int block_lanes(bool whole) { return whole ? 32 : 31; }
 
 // The aligned blocks of a row [row, row + bytes): the b-th starts `at(b)` bytes into it (the first may be before it).
 struct RowBlocks {
@@ -135,12 +126,13 @@ __global__ void __launch_bounds__(kRowThreads)
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
+    constexpr int kLanes = block_lanes(kWhole);
     const int64_t most = most_blocks(row_bytes, kWhole);
-    const int32_t segs = static_cast<int32_t>((most + 32 * kDispatchLoads - 1) / (32 * kDispatchLoads));
+    const int32_t segs = static_cast<int32_t>((most + kLanes * kDispatchLoads - 1) / (kLanes * kDispatchLoads));
     const Span span{X, X + T * row_bytes};
     for (RowItems it(T, segs); it.left(); it.next()) {
         const int64_t t = it.token();
-        const int64_t b0 = (it.item - t * segs) * (32 * kDispatchLoads) + lane;
+        const int64_t b0 = (it.item - t * segs) * (kLanes * kDispatchLoads) + lane;
         const uintptr_t from = X + t * row_bytes;
         if constexpr (kWhole) {
             uint4 v[kDispatchLoads];
@@ -162,15 +154,17 @@ __global__ void __launch_bounds__(kRowThreads)
                 const RowBlocks blocks(to, row_bytes);
                 const uint32_t shift = static_cast<uint32_t>(from - blocks.lead) & 15u;
                 const int64_t count = blocks.count();
-                Block16 v[kDispatchLoads];
-#pragma unroll
-                for (int u = 0; u < kDispatchLoads; ++u)
-                    if (b0 + 32 * u < count) v[u] = load_block<kMode>(from + blocks.at(b0 + 32 * u), span);
+                uint4 v[kDispatchLoads];
 #pragma unroll
                 for (int u = 0; u < kDispatchLoads; ++u) {
-                    const int64_t off = blocks.at(b0 + 32 * u);
-                    if (b0 + 32 * u >= count) continue;
+                    v[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (b0 + kLanes * u <= count) v[u] = load_block<kMode>(from + blocks.at(b0 + kLanes * u), span);
+                }
+#pragma unroll
+                for (int u = 0; u < kDispatchLoads; ++u) {
+                    const int64_t off = blocks.at(b0 + kLanes * u);
                     const uint4 x = shift_block<kMode>(v[u], shift);
+                    if (lane == 31 || b0 + kLanes * u >= count) continue;
                     if (blocks.whole(off)) {
                         *reinterpret_cast<uint4*>(to + off) = x;
                     } else {
@@ -193,24 +187,24 @@ __global__ void __launch_bounds__(kRowThreads)
     }
 }
 
-// A warp takes kSteps times 32 blocks of a token's row.
+// A warp takes two blocks a lane of a token's row.
 template <bool kWhole>
 __global__ void __launch_bounds__(kRowThreads, 3)
     combine_kernel(uintptr_t Y, const int32_t* __restrict__ position, const float* __restrict__ weights, int64_t T, int k,
                    int64_t rows, int64_t N, uintptr_t out, int32_t* status) {
-    constexpr int kSteps = combine_steps(kWhole);
+    constexpr int kSteps = kCombineSteps, kLanes = block_lanes(kWhole);
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t bytes = 2 * N;
-    const int32_t segs = static_cast<int32_t>((most_blocks(bytes, kWhole) + 32 * kSteps - 1) / (32 * kSteps));
+    const int32_t segs = static_cast<int32_t>((most_blocks(bytes, kWhole) + kLanes * kSteps - 1) / (kLanes * kSteps));
     const Span span{Y, Y + rows * bytes};
     for (RowItems it(T, segs); it.left(); it.next()) {
         const int64_t t = it.token();
         const uintptr_t to = out + t * bytes;
         const RowBlocks blocks(to, bytes);
         const int64_t count = blocks.count();
-        const int64_t b0 = (it.item - t * segs) * (32 * kSteps) + lane;
+        const int64_t b0 = (it.item - t * segs) * (kLanes * kSteps) + lane;
         float acc[kSteps][8];
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
@@ -229,7 +223,7 @@ __global__ void __launch_bounds__(kRowThreads, 3)
             auto add = [&](auto mode) {
                 constexpr int kMode = decltype(mode)::value;
                 for (int j0 = 0; j0 < here; j0 += kFlight) {
-                    Block16 v[kFlight][kSteps];
+                    uint4 v[kFlight][kSteps];
                     int32_t pj[kFlight];
 #pragma unroll
                     for (int j = 0; j < kFlight; ++j) {
@@ -238,7 +232,7 @@ __global__ void __launch_bounds__(kRowThreads, 3)
                         if (pj[j] < 0) continue;
 #pragma unroll
                         for (int s = 0; s < kSteps; ++s)
-                            if (b0 + 32 * s < count) v[j][s] = load_block<kMode>(Y + pj[j] * bytes + blocks.at(b0 + 32 * s), span);
+                            if (b0 + kLanes * s < count + (kWhole ? 0 : 1)) v[j][s] = load_block<kMode>(Y + pj[j] * bytes + blocks.at(b0 + kLanes * s), span);
                     }
 #pragma unroll
                     for (int j = 0; j < kFlight; ++j) {
@@ -261,7 +255,7 @@ __global__ void __launch_bounds__(kRowThreads, 3)
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
-            if (b0 + 32 * s < count) store8<kWhole ? kAligned : kShifted>(to, blocks.at(b0 + 32 * s), blocks, acc[s]);
+            if ((kWhole || lane < 31) && b0 + kLanes * s < count) store8<kWhole ? kAligned : kShifted>(to, blocks.at(b0 + kLanes * s), blocks, acc[s]);
     }
 }
 
@@ -292,22 +286,25 @@ __global__ void __launch_bounds__(kRowThreads, 3)
             const int64_t count = blocks.count();
             auto walk = [&](auto d_mode, auto y_mode) {
                 constexpr int kD = decltype(d_mode)::value, kY = decltype(y_mode)::value;
-                for (int64_t b0 = lane; b0 < count; b0 += 32 * kLoads) {
-                    Block16 dv[kLoads], yv[kLoads];
+                constexpr int kLanes = block_lanes(kWhole);
+                for (int64_t first = 0; first < count; first += kLanes * kLoads) {
+                    const int64_t b0 = first + lane;
+                    uint4 dv[kLoads], yv[kLoads];
 #pragma unroll
                     for (int u = 0; u < kLoads; ++u) {
-                        const int64_t off = blocks.at(b0 + 32 * u);
-                        if (b0 + 32 * u >= count) continue;
+                        dv[u] = yv[u] = make_uint4(0u, 0u, 0u, 0u);
+                        const int64_t off = blocks.at(b0 + kLanes * u);
+                        if (b0 + kLanes * u >= count + (kWhole ? 0 : 1)) continue;
                         yv[u] = load_block<kY>(y_row + off, y_span);
                         dv[u] = load_block<kD>(d_row + off, d_span);
                     }
 #pragma unroll
                     for (int u = 0; u < kLoads; ++u) {
-                        const int64_t off = blocks.at(b0 + 32 * u);
-                        if (b0 + 32 * u >= count) continue;
+                        const int64_t off = blocks.at(b0 + kLanes * u);
                         float d[8], y[8];
                         unpack8(shift_block<kD>(dv[u], d_shift), d);
                         unpack8(shift_block<kY>(yv[u], y_shift), y);
+                        if ((!kWhole && lane == 31) || b0 + kLanes * u >= count) continue;
                         if (!kWhole && !blocks.whole(off)) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
@@ -365,7 +362,8 @@ extern "C" rgg_status rgg_dispatch(rgg_handle* h, const void* X, const int32_t* 
     if (scope.error() != cudaSuccess) return host_cuda_failure(scope.error(), "cudaSetDevice");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool aligned = rows_aligned(row_bytes, {X, out});
-    const int64_t segs = (most_blocks(row_bytes, aligned) + 32 * kDispatchLoads - 1) / (32 * kDispatchLoads);
+    const int64_t segs = (most_blocks(row_bytes, aligned) + block_lanes(aligned) * kDispatchLoads - 1) /
+                         (block_lanes(aligned) * kDispatchLoads);
     cudaError_t err = launch_chained(aligned ? dispatch_kernel<true> : dispatch_kernel<false>,
                                      row_grid(T * segs, kRowThreads), kRowThreads, 0, st, address(X), position, T, k,
                                      row_bytes, rows, address(out), dev.status);
@@ -384,7 +382,8 @@ extern "C" rgg_status rgg_combine(rgg_handle* h, const void* Y, const int32_t* p
     if (scope.error() != cudaSuccess) return host_cuda_failure(scope.error(), "cudaSetDevice");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool aligned = rows_aligned(2 * N, {Y, out});
-    const int64_t segs = (most_blocks(2 * N, aligned) + 32 * combine_steps(aligned) - 1) / (32 * combine_steps(aligned));
+    const int64_t segs = (most_blocks(2 * N, aligned) + block_lanes(aligned) * kCombineSteps - 1) /
+                         (block_lanes(aligned) * kCombineSteps);
     cudaError_t err = launch_chained(aligned ? combine_kernel<true> : combine_kernel<false>, row_grid(T * segs, kRowThreads),
                                      kRowThreads, 0, st, address(Y), position, weights, T, k, rows, N, address(out),
                                      dev.status);

@@ -28,7 +28,7 @@
 namespace rgg {
 
 constexpr int kDispatchLoads = 4;  // in flight a lane
-constexpr int kFlight = 4;         // choices whose loads are in flight together
+constexpr int kFlight = 2;         // choices whose loads are in flight together
 constexpr int kCombineSteps = 2;   // blocks that a lane combines at a time
 
 // A tensor's bytes, for loads that may not leave them.
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kRowThreads)
 
 // A warp takes two blocks a lane of a token's row.
 template <bool kWhole>
-__global__ void __launch_bounds__(kRowThreads, 3)
+__global__ void __launch_bounds__(kRowThreads, 4)
     combine_kernel(uintptr_t Y, const int32_t* __restrict__ position, const float* __restrict__ weights, int64_t T, int k,
                    int64_t rows, int64_t N, uintptr_t out, int32_t* status) {
     constexpr int kSteps = kCombineSteps, kLanes = block_lanes(kWhole);
@@ -263,11 +263,11 @@ __global__ void __launch_bounds__(kRowThreads, 3)
 // fixed order, and the scaled gradient.  The warps of a token's choices are neighbours, so
 // its gradient comes from memory once.
 template <bool kWhole>
-__global__ void __launch_bounds__(kRowThreads, 3)
+__global__ void __launch_bounds__(kRowThreads, kWhole ? 3 : 4)
     combine_backward_kernel(uintptr_t dout, uintptr_t Y, const int32_t* __restrict__ position,
                             const float* __restrict__ weights, int64_t T, int k, int64_t rows, int64_t N, uintptr_t dY,
                             float* __restrict__ dweights, int32_t* status) {
-    constexpr int kLoads = 2;
+    constexpr int kLoads = kWhole ? 3 : 2;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;

@@ -13,11 +13,14 @@
 //     sigmoid, divided    dl_i = scale (g_i - sum g_j w_j) / (sum s_j + 1e-20) s_i (1 - s_i)
 // with w before the scale.
 //
-// A warp takes a token; lane l holds the logits l, l + 32, ...  The order is by
-// value, ties to the lower expert, NaN first, so that it shows in the weights;
-// -inf is never chosen.  Values are compared as unsigned numbers of the same order;
-// 16-bit ones share a word with the expert's complement, so that one warp
-// reduction gives the largest and settles ties.
+// A warp takes a token, each lane up to 8 logits (kWide: neighbouring ones, read by one or
+// two 16-byte loads; else l, l + 32, ...; above 256 experts more).  The order is by value,
+// ties to the lower expert, NaN first, so that it shows in the weights; -inf is
+// never chosen.  Values are compared as unsigned numbers of the same order, joined with
+// the expert's complement, which settles ties: 16-bit values share a 32-bit word with it.
+// Each lane sorts its own by a network; then k times a warp reduction finds the largest of
+// the lanes' first, and its lane moves on to its next.  Bound by the instructions that
+// takes: 32,768 tokens x 256 experts, k = 8, bf16 (17 MB).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,54 +37,135 @@ constexpr int kRouteMaxExperts = 4096;
 constexpr int kRouteMaxChoices = 32;  // a lane each
 constexpr float kRouteEps = 1e-20f;
 
-template <typename T>
-struct RouteKey;  // order(x): the value's place in the order, unsigned; kNegInf: that of -inf, below all others
+// A logit's place in the order: the bits of an fp32 number as an unsigned one.  Adding 0 makes 0 of -0, and of any NaN the
+// positive one, which comes out on top.  16-bit values keep their bits in the upper half.
+__device__ __forceinline__ uint32_t route_order(float x) {
+    const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float route_value(uint32_t order) {
+    return __uint_as_float(order ^ ((order & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+}
+constexpr uint32_t kRouteNegInf = 0x007fffffu;  // route_order(-inf): nothing above it is masked
 
+template <typename T>
+struct RouteType;
 template <>
-struct RouteKey<float> {
-    static constexpr bool kPacked = false;
-    static constexpr uint32_t kNegInf = 0x007fffffu;
-    static __device__ __forceinline__ uint32_t order(float x) {
-        const uint32_t b = __float_as_uint(x + 0.0f);  // -0 as 0
-        return x != x ? 0xffffffffu : (b & 0x80000000u) ? ~b : b | 0x80000000u;
-    }
-    static __device__ __forceinline__ float value(uint32_t o) {
-        return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
-    }
+struct RouteType<float> {
+    using Key = uint64_t;
     static __device__ __forceinline__ float to_float(float x) { return x; }
     static __device__ __forceinline__ float from_float(float x) { return x; }
 };
-
-// 16-bit values with the sign in the top bit; bits of a value and its place in the order.
-__device__ __forceinline__ uint32_t order16(uint32_t b) {
-    return b == 0x8000u ? 0x8000u : (b & 0x8000u) ? (~b & 0xffffu) : (b | 0x8000u);  // -0 as 0
-}
-__device__ __forceinline__ uint16_t bits16(uint32_t o) {
-    return static_cast<uint16_t>((o & 0x8000u) ? o & 0x7fffu : ~o);
-}
-
 template <>
-struct RouteKey<__nv_bfloat16> {
-    static constexpr bool kPacked = true;
-    static constexpr uint32_t kNegInf = 0x007fu;
-    static __device__ __forceinline__ uint32_t order(__nv_bfloat16 x) {
-        return __hisnan(x) ? 0xffffu : order16(__bfloat16_as_ushort(x));
-    }
-    static __device__ __forceinline__ float value(uint32_t o) { return __bfloat162float(__ushort_as_bfloat16(bits16(o))); }
+struct RouteType<__nv_bfloat16> {
+    using Key = uint32_t;
     static __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
     static __device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
 };
-
 template <>
-struct RouteKey<__half> {
-    static constexpr bool kPacked = true;
-    static constexpr uint32_t kNegInf = 0x03ffu;
-    static __device__ __forceinline__ uint32_t order(__half x) {
-        return __hisnan(x) ? 0xffffu : order16(__half_as_ushort(x));
-    }
-    static __device__ __forceinline__ float value(uint32_t o) { return __half2float(__ushort_as_half(bits16(o))); }
+struct RouteType<__half> {  // 10 bits of mantissa do not fit beside an expert's number: as fp32
+    using Key = uint64_t;
     static __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
     static __device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
+};
+
+// Value and expert in one number: the larger value first, then the lower expert.  0 is below all of them.
+template <typename Key>
+__device__ __forceinline__ Key route_key(float x, uint32_t expert) {
+    if constexpr (sizeof(Key) == 4) return (route_order(x) & 0xffff0000u) | (0xffffu - expert);
+    else return (static_cast<uint64_t>(route_order(x)) << 32) | (0xffffu - expert);
+}
+template <typename Key>
+__device__ __forceinline__ uint32_t key_order(Key key) {  // of bf16 -inf, too, this is kRouteNegInf or less
+    if constexpr (sizeof(Key) == 4) return key & 0xffff0000u;
+    else return static_cast<uint32_t>(key >> 32);
+}
+template <typename Key>
+__device__ __forceinline__ float key_value(Key key) {
+    uint32_t order = key_order(key);
+    if (sizeof(Key) == 4 && !(order & 0x80000000u)) order |= 0xffffu;  // the lower half of a negative number's
+    return route_value(order);
+}
+template <typename Key>
+__device__ __forceinline__ int32_t key_expert(Key key) {
+    return static_cast<int32_t>(0xffffu - static_cast<uint32_t>(key & 0xffffu));
+}
+// The largest of the warp's, in every lane.
+__device__ __forceinline__ uint32_t warp_max_key(uint32_t key) { return __reduce_max_sync(0xffffffffu, key); }
+__device__ __forceinline__ uint64_t warp_max_key(uint64_t key) {
+    const uint32_t hi = static_cast<uint32_t>(key >> 32);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, hi);
+    return (static_cast<uint64_t>(top) << 32) | __reduce_max_sync(0xffffffffu, hi == top ? static_cast<uint32_t>(key) : 0u);
+}
+
+template <typename Key>
+__device__ __forceinline__ void order_pair(Key& a, Key& b) {
+    const Key lo = a < b ? a : b;
+    a = a < b ? b : a;
+    b = lo;
+}
+// Largest first: odd-even merge networks for 2, 4 and 8.
+template <typename Key, int V>
+__device__ __forceinline__ void sort_lane(Key (&k)[V]) {
+    static_assert(V <= 8, "");
+    if constexpr (V >= 2)
+#pragma unroll
+        for (int i = 0; i < V; i += 2) order_pair(k[i], k[i + 1]);
+    if constexpr (V >= 4)
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            order_pair(k[i], k[i + 2]);
+            order_pair(k[i + 1], k[i + 3]);
+            order_pair(k[i + 1], k[i + 2]);
+        }
+    if constexpr (V == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) order_pair(k[i], k[i + 4]);
+        order_pair(k[2], k[4]);
+        order_pair(k[3], k[5]);
+        order_pair(k[1], k[2]);
+        order_pair(k[3], k[4]);
+        order_pair(k[5], k[6]);
+    }
+}
+
+// A lane's logits of a row: kWide, V neighbouring ones in 16-byte loads (E = 32 V); else l, l + 32, ..., -inf past E.
+template <typename T, int V, bool kWide>
+struct RouteRow {
+    static __device__ __forceinline__ int expert(int i, int lane) { return kWide ? V * lane + i : 32 * i + lane; }
+    static __device__ __forceinline__ void load(const T* row, int E, int lane, float (&x)[V]) {
+        if constexpr (kWide) {
+            constexpr int kPer = 16 / sizeof(T);
+            static_assert(V % kPer == 0, "");
+#pragma unroll
+            for (int i = 0; i < V; i += kPer) {
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + V * lane + i));
+                const T* t = reinterpret_cast<const T*>(&w);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) x[i + j] = RouteType<T>::to_float(t[j]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = 32 * i + lane < E ? RouteType<T>::to_float(row[32 * i + lane]) : -INFINITY;
+        }
+    }
+    static __device__ __forceinline__ void store(T* row, int E, int lane, const float (&x)[V]) {
+        if constexpr (kWide) {
+            constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+            for (int i = 0; i < V; i += kPer) {
+                uint4 w;
+                T* t = reinterpret_cast<T*>(&w);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) t[j] = RouteType<T>::from_float(x[i + j]);
+                *reinterpret_cast<uint4*>(row + V * lane + i) = w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (32 * i + lane < E) row[32 * i + lane] = RouteType<T>::from_float(x[i]);
+        }
+    }
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -101,106 +185,85 @@ __device__ __forceinline__ float sigmoid_f32(float x) { return 1.0f / (1.0f + ex
 __device__ __forceinline__ float not_zero(float total) { return total == 0.0f ? 1.0f : total; }
 
 // V: logits a lane, E <= 32 V.
-template <typename T, int V>
+template <typename T, int V, bool kWide>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const T* __restrict__ logits, int64_t tokens, int E, int k,
                                                               int flags, float scale, int32_t* __restrict__ experts,
                                                               float* __restrict__ weights) {
-    using Key = RouteKey<T>;
+    using Key = typename RouteType<T>::Key;
+    using Row = RouteRow<T, V, kWide>;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const bool sigmoid = flags & RGG_ROUTE_SIGMOID, renormalize = flags & RGG_ROUTE_RENORMALIZE;
     for (RowItems it(tokens, 1); it.left(); it.next()) {
-        const T* row = logits + it.item * E;
-        uint32_t key[V];
+        float x[V];
+        Row::load(logits + it.item * E, E, lane, x);
+        Key key[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = 32 * i + lane;
-            uint32_t o = 0;  // below every logit
-            if (e < E) {
-                o = Key::order(row[e]);
-                if constexpr (Key::kPacked) o = (o << 16) | (0xffffu - e);
-            }
-            key[i] = o;
-        }
+        for (int i = 0; i < V; ++i) key[i] = route_key<Key>(x[i], Row::expert(i, lane));
+        Key head;  // the lane's largest that is left
         auto best = [&]() {
-            uint32_t m = key[0];
+            head = key[0];
 #pragma unroll
-            for (int i = 1; i < V; ++i) m = max(m, key[i]);
-            return m;
+            for (int i = 1; i < V; ++i) head = key[i] > head ? key[i] : head;
         };
-        uint32_t m = best();
-        float top = 0.0f, total = 0.0f;
-        if (!sigmoid && !renormalize) {
-            const uint32_t first = __reduce_max_sync(0xffffffffu, m);
-            top = Key::value(Key::kPacked ? first >> 16 : first);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const uint32_t o = Key::kPacked ? key[i] >> 16 : key[i];
-                if (o > Key::kNegInf) total += expf(Key::value(o) - top);
-            }
-            total = warp_sum(total);
+        if constexpr (V <= 8) {
+            sort_lane<Key, V>(key);
+            head = key[0];
+        } else {
+            best();
         }
-        uint32_t mine = 0;  // order of this lane's choice
-        int32_t expert = -1;
+        Key mine = 0;  // this lane's choice
         for (int j = 0; j < k; ++j) {
-            const uint32_t M = __reduce_max_sync(0xffffffffu, m);
-            if ((Key::kPacked ? M >> 16 : M) <= Key::kNegInf) break;
-            if constexpr (Key::kPacked) {
-                if (lane == j) {
-                    mine = M >> 16;
-                    expert = static_cast<int32_t>(0xffffu - (M & 0xffffu));
-                }
-                if (m == M) {
+            const Key top = warp_max_key(head);
+            if (key_order(top) <= kRouteNegInf) break;
+            if (lane == j) mine = top;
+            if (head == top) {
+                if constexpr (V <= 8) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) key[i] = key[i] == M ? 0u : key[i];
-                    m = best();
-                }
-            } else {
-                uint32_t e = 0xffffffffu;  // the lane's lowest expert of that value
-                if (m == M) {
+                    for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+                    key[V - 1] = 0;
+                    head = key[0];
+                } else {
 #pragma unroll
-                    for (int i = V - 1; i >= 0; --i)
-                        if (key[i] == M) e = 32 * i + lane;
-                }
-                const uint32_t first = __reduce_min_sync(0xffffffffu, e);
-                if (lane == j) {
-                    mine = M;
-                    expert = static_cast<int32_t>(first);
-                }
-                if (e == first) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (static_cast<uint32_t>(32 * i + lane) == first) key[i] = 0u;
-                    m = best();
+                    for (int i = 0; i < V; ++i) key[i] = key[i] == top ? 0 : key[i];
+                    best();
                 }
             }
         }
+        const bool chosen = mine != 0;
+        const float l = key_value(mine);
         float w = 0.0f;
-        const float l = Key::value(mine);
         if (sigmoid) {
-            if (expert >= 0) w = sigmoid_f32(l);
+            if (chosen) w = sigmoid_f32(l);
             if (renormalize) w = w / (warp_sum(w) + kRouteEps);
-        } else if (renormalize) {
-            top = __shfl_sync(0xffffffffu, l, 0);
-            if (expert >= 0) w = expf(l - top);
-            w = w / not_zero(warp_sum(w));
-        } else if (expert >= 0) {
-            w = expf(l - top) / total;
+        } else {
+            const float top = __shfl_sync(0xffffffffu, l, 0);
+            if (chosen) w = expf(l - top);
+            float total = w;
+            if (!renormalize) {
+                total = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) total += x[i] == -INFINITY ? 0.0f : expf(x[i] - top);
+            }
+            w = w / not_zero(warp_sum(total));
         }
         if (lane < k) {
-            experts[it.item * k + lane] = expert;
-            weights[it.item * k + lane] = w * scale;
+            experts[it.item * k + lane] = chosen ? key_expert(mine) : -1;
+            weights[it.item * k + lane] = chosen ? w * scale : 0.0f;
         }
     }
 }
 
-template <typename T>
+// The gradient by a row's logits.  Softmax over all experts reads the whole row (V logits a lane); the other rules have a
+// gradient at the choices alone: zeros, and the choices' values behind them.
+template <typename T, int V, bool kWide, bool kDense>
 __global__ void __launch_bounds__(kRouteThreads)
     route_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ experts,
                           const float* __restrict__ dweights, int64_t tokens, int E, int k, int flags, float scale,
                           int wide, T* __restrict__ dlogits, int32_t* status) {
-    using Key = RouteKey<T>;
+    using Type = RouteType<T>;
+    using Row = RouteRow<T, V, kWide>;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -208,90 +271,130 @@ __global__ void __launch_bounds__(kRouteThreads)
     for (RowItems it(tokens, 1); it.left(); it.next()) {
         const T* row = logits + it.item * E;
         T* out = dlogits + it.item * E;
+        float x[V];
+        if constexpr (kDense) Row::load(row, E, lane, x);
         int32_t e = -1;
         float g = 0.0f, l = 0.0f;
         if (lane < k) {
             e = checked_row(experts[it.item * k + lane], E, status);
             if (e >= 0) {
                 g = dweights[it.item * k + lane] * scale;
-                l = Key::to_float(row[e]);
+                l = Type::to_float(row[e]);
             }
         }
         const bool chosen = e >= 0;
-        float d = 0.0f;
-        if (!sigmoid && !renormalize) {
-            float top = -INFINITY, total = 0.0f;
-            for (int i = lane; i < E; i += 32) top = fmaxf(top, Key::to_float(row[i]));
-            top = warp_max(top);
-            if (top == -INFINITY) top = 0.0f;  // all masked: every weight is 0
-            for (int i = lane; i < E; i += 32) total += expf(Key::to_float(row[i]) - top);
-            total = not_zero(warp_sum(total));
-            const float s = chosen ? expf(l - top) / total : 0.0f;
-            const float sum = warp_sum(chosen ? g * s : 0.0f);
-            for (int i = lane; i < E; i += 32)
-                out[i] = Key::from_float(-sum * (expf(Key::to_float(row[i]) - top) / total));
-            // an expert chosen twice has both gradients; its value is then written by each of its lanes alike
+        // an expert that the row names twice has both gradients: each of its lanes then holds their sum
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        const bool twice = __any_sync(0xffffffffu, chosen && (same & (same - 1)) != 0);
+        auto joined = [&](float v) {
+            if (!twice) return v;
             float all = 0.0f;
             for (int j = 0; j < k; ++j) {
-                const int32_t oe = __shfl_sync(0xffffffffu, e, j);
-                const float og = __shfl_sync(0xffffffffu, g, j);
-                if (oe == e) all += og;
+                const float other = __shfl_sync(0xffffffffu, v, j);
+                if (same >> j & 1u) all += other;
             }
-            d = s * (all - sum);
+            return all;
+        };
+        float d;
+        if constexpr (kDense) {
+            float top = x[0];
+#pragma unroll
+            for (int i = 1; i < V; ++i) top = fmaxf(top, x[i]);
+            top = warp_max(top);
+            if (top == -INFINITY) top = 0.0f;  // all masked: every weight is 0
+            float total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[i] = expf(x[i] - top);
+                total += x[i];
+            }
+            const float inverse = 1.0f / not_zero(warp_sum(total));
+            const float s = chosen ? expf(l - top) * inverse : 0.0f;
+            const float sum = warp_sum(g * s);
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] *= -sum * inverse;
+            Row::store(out, E, lane, x);
+            d = s * (joined(g) - sum);
         } else {
             if (sigmoid) {
                 const float s = chosen ? sigmoid_f32(l) : 0.0f;
+                d = g * s * (1.0f - s);
                 if (renormalize) {
                     const float total = warp_sum(s) + kRouteEps;
-                    const float sum = warp_sum(chosen ? g * (s / total) : 0.0f);
-                    d = chosen ? (g - sum) / total * s * (1.0f - s) : 0.0f;
-                } else {
-                    d = chosen ? g * s * (1.0f - s) : 0.0f;
+                    d = (g - warp_sum(g * (s / total))) / total * s * (1.0f - s);
                 }
             } else {
                 float top = warp_max(chosen ? l : -INFINITY);
                 if (top == -INFINITY) top = 0.0f;
                 float w = chosen ? expf(l - top) : 0.0f;
                 w = w / not_zero(warp_sum(w));
-                const float sum = warp_sum(chosen ? g * w : 0.0f);
-                d = chosen ? w * (g - sum) : 0.0f;
+                d = w * (g - warp_sum(g * w));
             }
             if (wide) {  // rows of whole 16 bytes
                 const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
                 for (int i = lane; i < wide; i += 32) reinterpret_cast<uint4*>(out)[i] = zero;
             } else {
-                for (int i = lane; i < E; i += 32) out[i] = Key::from_float(0.0f);
+                for (int i = lane; i < E; i += 32) out[i] = Type::from_float(0.0f);
             }
-            float all = 0.0f;
-            for (int j = 0; j < k; ++j) {
-                const int32_t oe = __shfl_sync(0xffffffffu, e, j);
-                const float od = __shfl_sync(0xffffffffu, d, j);
-                if (oe == e) all += od;
-            }
-            d = all;
+            d = joined(chosen ? d : 0.0f);
         }
         __syncwarp();  // the row's other values are written before the choices'
-        if (chosen) out[e] = Key::from_float(d);
+        if (chosen) out[e] = Type::from_float(d);
     }
 }
 
-template <typename T, int V>
-static cudaError_t launch_route(const void* logits, int64_t tokens, int E, int k, int flags, float scale,
-                                int32_t* experts, float* weights, cudaStream_t st) {
-    return launch_chained(route_kernel<T, V>, row_grid(tokens, kRouteThreads), kRouteThreads, 0, st,
-                          static_cast<const T*>(logits), tokens, E, k, flags, scale, experts, weights);
+struct RouteCall {
+    const void* logits;
+    int64_t T;
+    int E, k, flags;
+    float scale;
+    int32_t* experts;  // the backward pass reads them
+    float* weights;
+    const float* dweights;
+    void* dlogits;
+    int32_t* status;
+    cudaStream_t st;
+};
+
+template <typename T, int V, bool kWide>
+static cudaError_t launch_route(const RouteCall& c) {
+    const int grid = row_grid(c.T, kRouteThreads);
+    if (!c.dlogits)
+        return launch_chained(route_kernel<T, V, kWide>, grid, kRouteThreads, 0, c.st, static_cast<const T*>(c.logits), c.T,
+                              c.E, c.k, c.flags, c.scale, c.experts, c.weights);
+    return launch_chained(route_backward_kernel<T, V, kWide, true>, grid, kRouteThreads, 0, c.st,
+                          static_cast<const T*>(c.logits), static_cast<const int32_t*>(c.experts), c.dweights, c.T, c.E,
+                          c.k, c.flags, c.scale, 0, static_cast<T*>(c.dlogits), c.status);
 }
 
 template <typename T>
-static cudaError_t launch_route_for(int E, const void* logits, int64_t tokens, int k, int flags, float scale,
-                                    int32_t* experts, float* weights, cudaStream_t st) {
-    if (E <= 32) return launch_route<T, 1>(logits, tokens, E, k, flags, scale, experts, weights, st);
-    if (E <= 64) return launch_route<T, 2>(logits, tokens, E, k, flags, scale, experts, weights, st);
-    if (E <= 128) return launch_route<T, 4>(logits, tokens, E, k, flags, scale, experts, weights, st);
-    if (E <= 256) return launch_route<T, 8>(logits, tokens, E, k, flags, scale, experts, weights, st);
-    if (E <= 512) return launch_route<T, 16>(logits, tokens, E, k, flags, scale, experts, weights, st);
-    if (E <= 1024) return launch_route<T, 32>(logits, tokens, E, k, flags, scale, experts, weights, st);
-    return launch_route<T, 128>(logits, tokens, E, k, flags, scale, experts, weights, st);
+static cudaError_t launch_route_for(const RouteCall& c) {
+    constexpr int kPer = 16 / sizeof(T);
+    const bool aligned = host_aligned(c.logits, 16) && host_aligned(c.dlogits, 16);
+    if (c.dlogits && (c.flags & (RGG_ROUTE_SIGMOID | RGG_ROUTE_RENORMALIZE))) {
+        const int wide = (c.E % kPer == 0 && host_aligned(c.dlogits, 16)) ? c.E / kPer : 0;
+        return launch_chained(route_backward_kernel<T, 1, false, false>, row_grid(c.T, kRouteThreads), kRouteThreads, 0,
+                              c.st, static_cast<const T*>(c.logits), static_cast<const int32_t*>(c.experts), c.dweights,
+                              c.T, c.E, c.k, c.flags, c.scale, wide, static_cast<T*>(c.dlogits), c.status);
+    }
+    if (aligned && c.E == 256) return launch_route<T, 8, true>(c);
+    if constexpr (kPer == 4) {
+        if (aligned && c.E == 128) return launch_route<T, 4, true>(c);
+    }
+    if (c.E <= 32) return launch_route<T, 1, false>(c);
+    if (c.E <= 64) return launch_route<T, 2, false>(c);
+    if (c.E <= 128) return launch_route<T, 4, false>(c);
+    if (c.E <= 256) return launch_route<T, 8, false>(c);
+    if (c.E <= 512) return launch_route<T, 16, false>(c);
+    if (c.E <= 1024) return launch_route<T, 32, false>(c);
+    return launch_route<T, 128, false>(c);
+}
+
+static rgg_status route_run(int dtype, const RouteCall& c, const char* what) {
+    cudaError_t err = dtype == RGG_FP32   ? launch_route_for<float>(c)
+                      : dtype == RGG_BF16 ? launch_route_for<__nv_bfloat16>(c)
+                                          : launch_route_for<__half>(c);
+    return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, what);
 }
 
 static rgg_status route_check(const rgg_handle* h, const void* logits, int dtype, int64_t T, int E, int k, int flags,
@@ -317,13 +420,10 @@ extern "C" rgg_status rgg_route_topk(rgg_handle* h, const void* logits, int dtyp
     const HostDevice dev = host_device(h);
     HostDeviceScope scope(dev.device);
     if (scope.error() != cudaSuccess) return host_cuda_failure(scope.error(), "cudaSetDevice");
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t err =
-        dtype == RGG_FP32 ? launch_route_for<float>(E, logits, T, k, flags, scale, experts, weights, st)
-        : dtype == RGG_BF16
-            ? launch_route_for<__nv_bfloat16>(E, logits, T, k, flags, scale, experts, weights, st)
-            : launch_route_for<__half>(E, logits, T, k, flags, scale, experts, weights, st);
-    return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, "route_topk launch");
+    const RouteCall c = {logits,  T,       E,       k,          flags,
+                         scale,   experts, weights, nullptr,    nullptr,
+                         nullptr, static_cast<cudaStream_t>(stream)};
+    return route_run(dtype, c, "route_topk launch");
 }
 
 extern "C" rgg_status rgg_route_topk_backward(rgg_handle* h, const void* logits, int dtype, const int32_t* experts,
@@ -339,20 +439,17 @@ extern "C" rgg_status rgg_route_topk_backward(rgg_handle* h, const void* logits,
     const HostDevice dev = host_device(h);
     HostDeviceScope scope(dev.device);
     if (scope.error() != cudaSuccess) return host_cuda_failure(scope.error(), "cudaSetDevice");
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int wide = (E * size % 16 == 0 && host_aligned(dlogits, 16)) ? E * size / 16 : 0;
-    const int grid = row_grid(T, kRouteThreads);
-    cudaError_t err;
-    if (dtype == RGG_FP32)
-        err = launch_chained(route_backward_kernel<float>, grid, kRouteThreads, 0, st, static_cast<const float*>(logits),
-                             experts, dweights, T, E, k, flags, scale, wide, static_cast<float*>(dlogits), dev.status);
-    else if (dtype == RGG_BF16)
-        err = launch_chained(route_backward_kernel<__nv_bfloat16>, grid, kRouteThreads, 0, st,
-                             static_cast<const __nv_bfloat16*>(logits), experts, dweights, T, E, k, flags, scale, wide,
-                             static_cast<__nv_bfloat16*>(dlogits), dev.status);
-    else
-        err = launch_chained(route_backward_kernel<__half>, grid, kRouteThreads, 0, st,
-                             static_cast<const __half*>(logits), experts, dweights, T, E, k, flags, scale, wide,
-                             static_cast<__half*>(dlogits), dev.status);
-    return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, "route_topk_backward launch");
+    const RouteCall c = {logits,
+                         T,
+                         E,
+                         k,
+                         flags,
+                         scale,
+                         const_cast<int32_t*>(experts),
+                         nullptr,
+                         dweights,
+                         dlogits,
+                         dev.status,
+                         static_cast<cudaStream_t>(stream)};
+    return route_run(dtype, c, "route_topk_backward launch");
 }

@@ -704,6 +704,26 @@ rgg_status rgg_grouped_gemm_swiglu_fp8_block(rgg_handle* h, const void* x_codes,
                                              const int32_t* group_offsets, void* h_codes, float* h_scales, int E,
                                              int64_t M_tot, int K, int N, void* stream, const rgg_options* opt);
 
+/*
+ * rgg_moe_swiglu_fp8_block -- a mixture-of-experts layer for serving, in one call:
+ *     out[t] = sum over j of w[t, j] * ffn of expert e[t, j] of X[t],
+ * the steps above one behind the other: rgg_route_topk (logits, k, flags, scale), rgg_sort_by_expert,
+ * rgg_fp8_block_quantize to the rows of the choices, rgg_grouped_gemm_swiglu_fp8_block,
+ * rgg_grouped_gemm_fp8_block and rgg_combine, with the results that these calls give.
+ *
+ * X: bf16 [T, K]; logits: [T, E] of type logits_dtype; w13: the codes [E, 2N, K] and scales of gate
+ * and up; w2: the codes [E, K_out, N] and scales of the down projection; out: bf16 [T, K_out].
+ * K a multiple of 16, N of 128, K_out of 8.  A token whose logits are all -inf gets zeros.
+ * workspace: device memory of at least rgg_moe_swiglu_fp8_block_workspace(...) bytes (0 for sizes that
+ * the call refuses), 256-byte aligned, not shared by calls that may overlap.  T may be 0.
+ * Asynchronous on `stream`; nothing is allocated; can be captured in a graph.
+ */
+int64_t rgg_moe_swiglu_fp8_block_workspace(int64_t T, int E, int k, int K, int N, int K_out);
+rgg_status rgg_moe_swiglu_fp8_block(rgg_handle* h, const void* X, const void* logits, int logits_dtype,
+                                    const void* w13_codes, const float* w13_scales, const void* w2_codes,
+                                    const float* w2_scales, void* out, int64_t T, int E, int k, int K, int N, int K_out,
+                                    int flags, float scale, void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,7 +25,7 @@ __all__ = [
     "rgg_route_topk", "rgg_route_topk_backward", "rgg_sort_by_expert", "rgg_dispatch", "rgg_combine",
     "rgg_combine_backward", "rgg_fp8_block_quantize", "rgg_fp8_block_dequantize", "rgg_fp8_block_quantize_weights",
     "rgg_fp8_block_dequantize_weights", "rgg_grouped_gemm_fp8_block", "rgg_grouped_gemm_swiglu_fp8_block",
-    "rgg_grouped_gemm_noalloc", "rgg_export_tiles", "rgg_export_walk",
+    "rgg_moe_swiglu_fp8_block", "rgg_grouped_gemm_noalloc", "rgg_export_tiles", "rgg_export_walk",
     "rgg_query_status",
     "rgg_plan", "rgg_status_string", "library_path", "load_library", "EXPORTED_SYMBOLS",
     "RGG_OK", "RGG_ERR_INVALID_ARG", "RGG_ERR_UNSUPPORTED", "RGG_ERR_CUDA", "RGG_ERR_BAD_OFFSETS",
@@ -61,7 +61,7 @@ EXPORTED_SYMBOLS = (
     "rgg_route_topk", "rgg_route_topk_backward", "rgg_sort_by_expert", "rgg_sort_by_expert_workspace", "rgg_dispatch",
     "rgg_combine", "rgg_combine_backward", "rgg_fp8_block_quantize", "rgg_fp8_block_dequantize",
     "rgg_fp8_block_quantize_weights", "rgg_fp8_block_dequantize_weights", "rgg_grouped_gemm_fp8_block",
-    "rgg_grouped_gemm_swiglu_fp8_block",
+    "rgg_grouped_gemm_swiglu_fp8_block", "rgg_moe_swiglu_fp8_block", "rgg_moe_swiglu_fp8_block_workspace",
 )
 
 
@@ -183,10 +183,13 @@ def open_library(path: str) -> ctypes.CDLL:
         getattr(lib, name).argtypes = [P, P, P, P, I, I, I, P]
     lib.rgg_grouped_gemm_fp8_block.argtypes = [P, P, P, P, P, P, P, I, I64, I, I, P, ctypes.POINTER(_Options)]
     lib.rgg_grouped_gemm_swiglu_fp8_block.argtypes = [P, P, P, P, P, P, P, P, I, I64, I, I, P, ctypes.POINTER(_Options)]
+    lib.rgg_moe_swiglu_fp8_block_workspace.argtypes = [I64, I, I, I, I, I]
+    lib.rgg_moe_swiglu_fp8_block_workspace.restype = I64
+    lib.rgg_moe_swiglu_fp8_block.argtypes = [P, P, P, I, P, P, P, P, P, I64, I, I, I, I, I, I, F, P, I64, P]
     for name in ("rgg_route_topk", "rgg_route_topk_backward", "rgg_sort_by_expert", "rgg_dispatch", "rgg_combine",
                  "rgg_combine_backward", "rgg_fp8_block_quantize", "rgg_fp8_block_dequantize",
                  "rgg_fp8_block_quantize_weights", "rgg_fp8_block_dequantize_weights", "rgg_grouped_gemm_fp8_block",
-                 "rgg_grouped_gemm_swiglu_fp8_block"):
+                 "rgg_grouped_gemm_swiglu_fp8_block", "rgg_moe_swiglu_fp8_block"):
         getattr(lib, name).restype = I
     lib.rgg_grouped_gemm_noalloc.argtypes = [P, P, P, P, I, I64, I, I, P, P]
     lib.rgg_grouped_gemm_noalloc.restype = I
@@ -1269,6 +1272,54 @@ def rgg_grouped_gemm_swiglu_fp8_block(x_codes, x_scales, w13_codes, w13_scales, 
         group_offsets.data_ptr(), h_codes.data_ptr(), h_scales.data_ptr(), E, M_tot, K, N, st, opt)
     _finish("rgg_grouped_gemm_swiglu_fp8_block", s, device, st, check)
     return h_codes, h_scales
+
+
+def rgg_moe_swiglu_fp8_block(X, logits, w13_codes, w13_scales, w2_codes, w2_scales, k, out=None, *, score="softmax",
+                             renormalize=True, scale=1.0, stream=None, check=False):
+    """A mixture-of-experts layer with 8-bit experts in one call, for serving:
+    ``rgg_route_topk``, ``rgg_sort_by_expert``, ``rgg_fp8_block_quantize`` to the
+    rows of the choices, the two products and ``rgg_combine``, with the results
+    that these calls give.
+
+    X: bf16 CUDA [T, K]; logits: bf16, fp16 or fp32 CUDA [T, E]; w13 and w2: the
+    weights as ``rgg_fp8_block_quantize_weights`` leaves them, float8_e4m3fn
+    [E, 2N, K] (gate first, N a multiple of 128) and [E, K_out, N]; out: optional
+    bf16 CUDA [T, K_out]."""
+    import torch
+    code = _logits(logits)
+    flags = _route_flags(score, renormalize)
+    if X.dim() != 2 or w13_codes.dim() != 3 or w2_codes.dim() != 3:
+        raise ValueError("X must be [T, K], w13_codes [E, 2N, K] and w2_codes [E, K_out, N]")
+    T, K = X.shape
+    E, cols = w13_codes.shape[:2]
+    K_out, N = w2_codes.shape[1:]
+    if cols != 2 * N or N % 128:
+        raise ValueError("w13_codes must have 2N columns for w2_codes' N = %d, a multiple of 128, not %d" % (N, cols))
+    k = int(k)
+    if not 1 <= k <= E:
+        raise ValueError("k must be between 1 and E = %d, not %d" % (E, k))
+    dev = X.device
+    fp8, fp32, bf16 = torch.float8_e4m3fn, torch.float32, torch.bfloat16
+    _operand("X", X, bf16, (T, K), dev)
+    _operand("logits", logits, logits.dtype, (T, E), dev)
+    _operand("w13_codes", w13_codes, fp8, (E, cols, K), dev)
+    _operand("w13_scales", w13_scales, fp32, _fp_weight_scale_shape(E, cols, K), dev)
+    _operand("w2_codes", w2_codes, fp8, (E, K_out, N), dev)
+    _operand("w2_scales", w2_scales, fp32, _fp_weight_scale_shape(E, K_out, N), dev)
+    if out is None:
+        out = _empty((T, K_out), bf16, dev, stream)
+    else:
+        _operand("out", out, bf16, (T, K_out), dev)
+    lib = load_library()
+    bytes_ = lib.rgg_moe_swiglu_fp8_block_workspace(T, E, k, K, N, K_out)
+    workspace = _empty((bytes_,), torch.uint8, dev, stream)
+    device = dev.index
+    st = _raw_stream(stream, device)
+    s = lib.rgg_moe_swiglu_fp8_block(_handle(device), X.data_ptr(), logits.data_ptr(), code, w13_codes.data_ptr(),
+                                     w13_scales.data_ptr(), w2_codes.data_ptr(), w2_scales.data_ptr(), out.data_ptr(), T,
+                                     E, k, K, N, K_out, flags, scale, workspace.data_ptr(), bytes_, st)
+    _finish("rgg_moe_swiglu_fp8_block", s, device, st, check)
+    return out
 
 
 def rgg_export_tiles(group_offsets, M_tot: int, N: int, bm: int, bn: int, cap: int | None = None, stream=None):

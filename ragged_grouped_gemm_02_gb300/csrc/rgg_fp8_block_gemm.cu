@@ -4,6 +4,7 @@
 #include "rgg_fp8_block.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "rgg_host.h"
@@ -11,19 +12,23 @@
 
 namespace rgg {
 
-template <typename Kernel>
-static cudaError_t launch_fp8_block(Kernel kernel, int grid, size_t smem, cudaStream_t stream, const FpMaps& maps,
-                                    const FpArgs& args) {
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(smem));
+using FpKernel = void (*)(FpMaps, FpArgs);
+constexpr int kFpKernels = 5;  // of which `which` numbers one
+
+// Once for each kernel and device: shared memory up to the device's most, and that its warps find the registers they share
+// out (with other code than was planned for they would wait for ever).
+static cudaError_t prepare_fp8_block(FpKernel kernel, int which, const HostDevice& dev) {
+    static std::atomic<uint64_t> ready[kFpKernels];
+    const uint64_t bit = dev.device < 64 ? uint64_t(1) << dev.device : 0;
+    if (ready[which].load(std::memory_order_acquire) & bit) return cudaSuccess;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dev.smem_optin);
     if (err != cudaSuccess) return err;
-    // the kernel's warps share out the registers that it was launched with: other code than
-    // was planned for would wait for ever
     cudaFuncAttributes attr;
     err = cudaFuncGetAttributes(&attr, kernel);
     if (err != cudaSuccess) return err;
     if (attr.numRegs != kFpRegsLaunch) return cudaErrorInvalidKernelImage;
-    return launch_chained(kernel, grid, kFpThreads, smem, stream, maps, args);
+    ready[which].fetch_or(bit, std::memory_order_release);
+    return cudaSuccess;
 }
 
 static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float* x_scales, const void* w_codes,
@@ -135,10 +140,12 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
     a.timeout_ns = (opt && opt->timeout_ns) ? opt->timeout_ns : kHostDefaultTimeoutNs;
     const int grid = static_cast<int>(pair ? 2 * std::max<int64_t>(1, std::min<int64_t>(cap / 2, most))
                                            : std::max<int64_t>(1, std::min<int64_t>(cap, most)));
-    auto kernel = pair ? (gate_up ? grouped_fp8_block_pair_kernel<true> : grouped_fp8_block_pair_kernel<false>)
-                  : gate_up ? grouped_fp8_block_kernel<kFpWide, true>
-                  : shape == kFpWide ? grouped_fp8_block_kernel<kFpWide, false> : grouped_fp8_block_kernel<kFpNarrow, false>;
-    cudaError_t err = launch_fp8_block(kernel, grid, smem, st, m, a);
+    const FpKernel kernels[kFpKernels] = {grouped_fp8_block_pair_kernel<false>, grouped_fp8_block_pair_kernel<true>,
+                                          grouped_fp8_block_kernel<kFpWide, false>, grouped_fp8_block_kernel<kFpWide, true>,
+                                          grouped_fp8_block_kernel<kFpNarrow, false>};
+    const int which = 2 * shape + (gate_up ? 1 : 0);
+    cudaError_t err = prepare_fp8_block(kernels[which], which, dev);
+    if (err == cudaSuccess) err = launch_chained(kernels[which], grid, kFpThreads, smem, st, m, a);
     return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, "grouped_gemm_fp8_block launch");
 }
 

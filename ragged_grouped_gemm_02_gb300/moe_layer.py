@@ -14,9 +14,9 @@ import functools
 
 import torch
 
-from . import (rgg_combine, rgg_combine_backward, rgg_dispatch, rgg_fp8_block_quantize, rgg_route_topk,
+from . import (rgg_combine, rgg_combine_backward, rgg_dispatch, rgg_moe_swiglu_fp8_block, rgg_route_topk,
                rgg_route_topk_backward, rgg_sort_by_expert)
-from .expert_layer import expert_ffn, expert_ffn_fp8
+from .expert_layer import expert_ffn
 
 __all__ = ["route_topk", "dispatch", "combine", "moe_ffn", "moe_ffn_fp8"]
 
@@ -104,18 +104,14 @@ def combine(Y, position, weights):
     return _Combine.apply(Y, position, weights)
 
 
-def _same_experts(logits, E):
-    if logits.dim() != 2 or logits.shape[1] != E:
-        raise ValueError("logits must be [T, E] with E = %d experts, not %s" % (E, tuple(logits.shape)))
-
-
 def moe_ffn(X, logits, W13, W2, k, *, score="softmax", renormalize=True, scale=1.0):
     """The layer's output for tokens X, with gradients by X, logits, W13 and W2 (first derivatives).
 
     X: bf16 CUDA [T, K]; logits: bf16, fp16 or fp32 CUDA [T, E]; W13: bf16 CUDA [E, K, 2N] (gate columns first);
     W2: bf16 CUDA [E, N, K_out]; k, score, renormalize, scale: as for ``rgg_route_topk``.  A token whose logits
     are all -inf gets zeros."""
-    _same_experts(logits, W13.shape[0])
+    if logits.dim() != 2 or logits.shape[1] != W13.shape[0]:
+        raise ValueError("logits must be [T, E] with E = %d experts, not %s" % (W13.shape[0], tuple(logits.shape)))
     experts, weights = route_topk(logits, k, score=score, renormalize=renormalize, scale=scale)
     group_offsets, _, position = rgg_sort_by_expert(experts, W13.shape[0])
     return combine(expert_ffn(dispatch(X, position), W13, W2, group_offsets), position, weights)
@@ -123,9 +119,7 @@ def moe_ffn(X, logits, W13, W2, k, *, score="softmax", renormalize=True, scale=1
 
 def moe_ffn_fp8(X, logits, experts, k, *, score="softmax", renormalize=True, scale=1.0):
     """The layer's output for tokens X with 8-bit experts (``expert_layer.quantize_experts_fp8``), for serving: a token
-    is quantised once and goes to its experts in 8 bits.  X: bf16 CUDA [T, K], K a multiple of 16."""
-    _same_experts(logits, experts[0][0].shape[0])
-    chosen, weights = rgg_route_topk(logits, k, score=score, renormalize=renormalize, scale=scale)
-    group_offsets, _, position = rgg_sort_by_expert(chosen, experts[0][0].shape[0])
-    rows = rgg_fp8_block_quantize(X, position)
-    return rgg_combine(expert_ffn_fp8(rows, experts, group_offsets), position, weights)
+    is quantised once and goes to its experts in 8 bits.  X: bf16 CUDA [T, K], K a multiple of 16.  One call of the
+    library: ``rgg_moe_swiglu_fp8_block``."""
+    w13, w2 = experts
+    return rgg_moe_swiglu_fp8_block(X, logits, *w13, *w2, k, score=score, renormalize=renormalize, scale=scale)

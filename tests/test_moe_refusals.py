@@ -48,7 +48,7 @@ def test_cpu_tensors(call):
     (lambda: rgg.rgg_fp8_block_quantize_weights(_t(16, 8)), ValueError),
     (lambda: quantize_experts_fp8(_t(2, 16, 24), _t(2, 8, 16)), ValueError),
     (lambda: moe_ffn(_t(4, 16), _t(4, 3), _t(2, 16, 16), _t(2, 8, 16), 1), ValueError),
-    (lambda: moe_ffn_fp8(_t(4, 16), _t(4, 3), ((_t(2, 256, 16, dtype=FP8), None), None), 1), ValueError),
+    (lambda: moe_ffn_fp8(_t(4, 16), _t(4, 2, dtype=I32), ((_t(2, 256, 16), None), (_t(2, 16, 128), None)), 1), TypeError),
 ])
 def test_shapes_and_types(call, error):
     with pytest.raises(error):
@@ -175,3 +175,20 @@ def test_product_arguments(lib, gate_up):
         assert call(N=64) == call(hs=None) == call(hs=P + 2) == call(N=2 ** 30) == INVALID
     for kw in ({"bn": 64}, {"bm": 256, "bn": 128}, {"bm": 64}, {"bm": 192}, {"max_ctas": -1}, {"stages": 1}, {"stages": 17}):
         assert call(opt=ctypes.byref(rgg._options(**kw)[0])) == INVALID, kw
+
+
+def test_moe_arguments(lib):
+    def call(h=HANDLE, X=P, lg=P, dt=1, a=P, b=P, c=P, d=P, out=P, T=4, E=4, k=2, K=32, N=128, K_out=32, flags=0, scale=1.0,
+             ws=P, nbytes=1 << 30):
+        return lib.rgg_moe_swiglu_fp8_block(h, X, lg, dt, a, b, c, d, out, T, E, k, K, N, K_out, flags, scale, ws, nbytes, None)
+
+    for bad in ({"h": None}, {"X": None}, {"lg": None}, {"dt": 3}, {"a": None}, {"b": None}, {"c": None}, {"d": None},
+                {"out": None}, {"T": -1}, {"E": 0}, {"k": 0}, {"k": 5}, {"K": 24}, {"N": 64}, {"K_out": 12}, {"flags": 4},
+                {"scale": float("nan")}, {"ws": None}, {"ws": P + 16}, {"nbytes": 100}, {"X": P + 8}, {"lg": P + 2},
+                {"a": P + 8}, {"b": P + 1}, {"c": P + 8}, {"d": P + 2}, {"out": P + 1}, {"T": 1 << 30}):
+        assert call(**bad) == INVALID, bad
+    assert call(E=4097) == call(E=64, k=33) == UNSUPPORTED
+    assert call(T=0) == rgg.RGG_OK
+    size = lib.rgg_moe_swiglu_fp8_block_workspace
+    assert size(4, 4, 5, 32, 128, 32) == size(4, 4, 2, 24, 128, 32) == 0
+    assert 0 < size(4, 4, 2, 32, 128, 32) < size(4000, 4, 2, 32, 128, 32)

@@ -24,7 +24,8 @@
 
 namespace rgg {
 
-constexpr int kFpRowSegment = 512;    // values of a row that a warp takes: 16 a lane, 8 lanes a block
+constexpr int kFpRowSegment = 512;    // values of a row that a warp's lanes take: 16 each, 8 lanes a block
+constexpr int kFpRowSteps = 2;        // segments that a warp has in flight
 constexpr int kFpWeightThreads = 256;
 
 __device__ __forceinline__ float fp_snap(float q) {
@@ -75,30 +76,45 @@ __global__ void __launch_bounds__(kRowThreads)
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int32_t segs = (K + kFpRowSegment - 1) / kFpRowSegment;
+    constexpr int kSteps = kFpRowSteps;
+    const int32_t segs = (K + kSteps * kFpRowSegment - 1) / (kSteps * kFpRowSegment);
     const int64_t blocks = fp_blocks(K);
     for (RowItems it(T, segs); it.left(); it.next()) {
         const int64_t t = it.token();
-        const int32_t c = static_cast<int32_t>(it.item - t * segs) * kFpRowSegment + 16 * lane;
-        const bool in = c < K;  // K is a multiple of 16
-        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-        if (in) {
-            const uint4* x = X + (t * K + c) / 8;
-            a = x[0];
-            b = x[1];
-        }
-        uint32_t m = a.x & 0x7fff7fffu;
-        m = max_abs2(max_abs2(max_abs2(m, a.y), a.z), a.w);
-        m = max_abs2(max_abs2(max_abs2(max_abs2(m, b.x), b.y), b.z), b.w);
+        const int32_t c = static_cast<int32_t>(it.item - t * segs) * (kSteps * kFpRowSegment) + 16 * lane;
+        uint4 x[kSteps][2];
 #pragma unroll
-        for (int d = 4; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float top = fp_top(m), inv = kFpMax / top, scale = top / kFpMax;
-        const uint4 q = make_uint4(fp_codes4(a.x, a.y, inv), fp_codes4(a.z, a.w, inv), fp_codes4(b.x, b.y, inv),
-                                   fp_codes4(b.z, b.w, inv));
+        for (int i = 0; i < kSteps; ++i) {
+            x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
+            const int32_t at = c + i * kFpRowSegment;
+            if (at >= K) continue;  // K is a multiple of 16
+            const uint4* from = X + (t * K + at) / 8;
+            x[i][0] = __ldg(from);
+            x[i][1] = __ldg(from + 1);
+        }
+        uint4 q[kSteps];
+        float scale[kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const uint4 a = x[i][0], b = x[i][1];
+            uint32_t m = a.x & 0x7fff7fffu;
+            m = max_abs2(max_abs2(max_abs2(m, a.y), a.z), a.w);
+            m = max_abs2(max_abs2(max_abs2(max_abs2(m, b.x), b.y), b.z), b.w);
+#pragma unroll
+            for (int d = 4; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+            const float top = fp_top(m), inv = kFpMax / top;
+            scale[i] = top / kFpMax;
+            q[i] = make_uint4(fp_codes4(a.x, a.y, inv), fp_codes4(a.z, a.w, inv), fp_codes4(b.x, b.y, inv),
+                              fp_codes4(b.z, b.w, inv));
+        }
         auto write = [&](int64_t row) {
-            if (!in) return;
-            *reinterpret_cast<uint4*>(codes + row * K + c) = q;
-            if ((lane & 7) == 0) scales[row * blocks + c / kFpBlock] = scale;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int32_t at = c + i * kFpRowSegment;
+                if (at >= K) continue;
+                *reinterpret_cast<uint4*>(codes + row * K + at) = q[i];
+                if ((lane & 7) == 0) scales[row * blocks + at / kFpBlock] = scale[i];
+            }
         };
         if (!position) {
             write(t);
@@ -111,19 +127,20 @@ __global__ void __launch_bounds__(kRowThreads)
     }
 }
 
-// rows_per: rows that share a row of scales (1, or 128 of each group of `group` rows).
+// rows_per: rows that share a row of scales (1, or 128 of each group of `group` rows).  kV8: X is 32-byte aligned.
+template <bool kV8>
 __global__ void __launch_bounds__(kRowThreads)
     fp8_dequantize_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales, int64_t rows, int64_t group,
                           int rows_per, int K, __nv_bfloat16* __restrict__ X) {
+    constexpr int kSteps = kFpRowSteps;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int32_t segs = (K + kFpRowSegment - 1) / kFpRowSegment;
+    const int32_t segs = (K + kSteps * kFpRowSegment - 1) / (kSteps * kFpRowSegment);
     const int64_t blocks = fp_blocks(K), group_blocks = rows_per > 1 ? (group + rows_per - 1) / rows_per : 0;
     for (RowItems it(rows, segs); it.left(); it.next()) {
         const int64_t r = it.token();
-        const int32_t c = static_cast<int32_t>(it.item - r * segs) * kFpRowSegment + 16 * lane;
-        if (c >= K) continue;
+        const int32_t c = static_cast<int32_t>(it.item - r * segs) * (kSteps * kFpRowSegment) + 16 * lane;
         int64_t scale_row = r;
         if (rows_per > 1) {
             // a division of 64 bits took a fifth of the call
@@ -132,12 +149,30 @@ __global__ void __launch_bounds__(kRowThreads)
                                   : r / group;
             scale_row = g * group_blocks + static_cast<uint32_t>(r - g * group) / static_cast<uint32_t>(rows_per);
         }
-        const uint4 q = *reinterpret_cast<const uint4*>(codes + r * K + c);
-        const float s = scales[scale_row * blocks + c / kFpBlock];
-        const uint2 v0 = fp_values4(q.x, s), v1 = fp_values4(q.y, s), v2 = fp_values4(q.z, s), v3 = fp_values4(q.w, s);
-        uint4* out = reinterpret_cast<uint4*>(X + r * K + c);
-        out[0] = make_uint4(v0.x, v0.y, v1.x, v1.y);
-        out[1] = make_uint4(v2.x, v2.y, v3.x, v3.y);
+        uint4 q[kSteps];
+        float s[kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int32_t at = c + i * kFpRowSegment;
+            if (at >= K) continue;
+            q[i] = __ldg(reinterpret_cast<const uint4*>(codes + r * K + at));
+            s[i] = scales[scale_row * blocks + at / kFpBlock];
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int32_t at = c + i * kFpRowSegment;
+            if (at >= K) continue;
+            const uint2 v0 = fp_values4(q[i].x, s[i]), v1 = fp_values4(q[i].y, s[i]), v2 = fp_values4(q[i].z, s[i]),
+                        v3 = fp_values4(q[i].w, s[i]);
+            __nv_bfloat16* out = X + r * K + at;
+            if constexpr (kV8) {
+                const uint32_t w[8] = {v0.x, v0.y, v1.x, v1.y, v2.x, v2.y, v3.x, v3.y};
+                st_global_v8(out, w);
+            } else {
+                reinterpret_cast<uint4*>(out)[0] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+                reinterpret_cast<uint4*>(out)[1] = make_uint4(v2.x, v2.y, v3.x, v3.y);
+            }
+        }
     }
 }
 
@@ -228,7 +263,7 @@ extern "C" rgg_status rgg_fp8_block_quantize(rgg_handle* h, const void* X, const
     const HostDevice dev = host_device(h);
     HostDeviceScope scope(dev.device);
     if (scope.error() != cudaSuccess) return host_cuda_failure(scope.error(), "cudaSetDevice");
-    const int64_t segs = (K + kFpRowSegment - 1) / kFpRowSegment;
+    const int64_t segs = (K + kFpRowSteps * kFpRowSegment - 1) / (kFpRowSteps * kFpRowSegment);
     cudaError_t err = launch_chained(fp8_quantize_kernel, row_grid(T * segs, kRowThreads), kRowThreads, 0,
                                      static_cast<cudaStream_t>(stream), static_cast<const uint4*>(X), position, T, k, rows,
                                      K, static_cast<uint8_t*>(codes), scales, dev.status);
@@ -243,8 +278,9 @@ static rgg_status fp8_dequantize(rgg_handle* h, const void* codes, const float* 
     const HostDevice dev = host_device(h);
     HostDeviceScope scope(dev.device);
     if (scope.error() != cudaSuccess) return host_cuda_failure(scope.error(), "cudaSetDevice");
-    const int64_t segs = (K + kFpRowSegment - 1) / kFpRowSegment;
-    cudaError_t err = launch_chained(fp8_dequantize_kernel, row_grid(rows * segs, kRowThreads), kRowThreads, 0,
+    const int64_t segs = (K + kFpRowSteps * kFpRowSegment - 1) / (kFpRowSteps * kFpRowSegment);
+    auto kernel = host_aligned(X, 32) ? fp8_dequantize_kernel<true> : fp8_dequantize_kernel<false>;
+    cudaError_t err = launch_chained(kernel, row_grid(rows * segs, kRowThreads), kRowThreads, 0,
                                      static_cast<cudaStream_t>(stream), static_cast<const uint8_t*>(codes), scales, rows,
                                      group, rows_per, K, static_cast<__nv_bfloat16*>(X));
     return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, "fp8_block_dequantize launch");

@@ -43,7 +43,9 @@ static MoePlan moe_plan(int64_t T, int E, int k, int K, int N, int K_out) {
 
 static bool moe_sizes_ok(int64_t T, int E, int k, int K, int N, int K_out) {
     const int64_t most = int64_t(1) << 31;
-    return T >= 0 && T < most && k >= 1 && k <= E && T * k < most && K % 16 == 0 && N % kFpBlock == 0 &&
+    if (T < 0 || T >= most || k < 1 || T * k >= most || T * k * std::max(K, std::max(N, K_out)) >= int64_t(1) << 56)
+        return false;  // the last: the workspace's size is counted in 64 bits
+    return k <= E && K % 16 == 0 && N % kFpBlock == 0 &&
            N <= kMaxWidth / 2 && host_check_sizes(E, T * k, K, N) == RGG_OK && host_check_sizes(E, T * k, N, K_out) == RGG_OK;
 }
 

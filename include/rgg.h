@@ -641,8 +641,8 @@ rgg_status rgg_sort_by_expert(rgg_handle* h, const int32_t* experts, int64_t T, 
  * RGG_ERR_BAD_ROW_INDEX.  Rows of no choice are left as they were.  Two choices must
  * not share a row of what a call writes.  dY or dweights may be NULL.
  *
- * T, rows, T k and N below 2^31; T and rows may be 0.  Pointers aligned to their
- * elements (wider loads are used where 16, 8 or 4 bytes divide them and the rows).
+ * T, rows and T k below 2^31, a row of fewer than 2^30 bytes; T and rows may be 0.  Pointers aligned to their
+ * elements (rows of whole, aligned 16 bytes are the fastest).
  * What is written must not overlap what is read.
  */
 rgg_status rgg_dispatch(rgg_handle* h, const void* X, const int32_t* position, int64_t T, int k, int64_t rows,

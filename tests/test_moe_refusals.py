@@ -120,7 +120,7 @@ def test_sort_workspace(lib):
 
 
 @pytest.mark.parametrize("T,k,rows,size", [(-1, 1, 4, 8), (BIG, 1, 4, 8), (4, 0, 4, 8), (4, 1, -1, 8), (4, 1, BIG, 8),
-                                           (4, 1, 4, 0), (4, 1, 4, BIG), (1 << 30, 2, 4, 8)])
+                                           (4, 1, 4, 0), (4, 1, 4, BIG), (4, 1, 4, 1 << 30), (1 << 30, 2, 4, 8)])
 def test_row_sizes(lib, T, k, rows, size):
     assert lib.rgg_dispatch(HANDLE, P, P, T, k, rows, size, P, None) == INVALID
     assert lib.rgg_combine(HANDLE, P, P, P, T, k, rows, size, P, None) == INVALID

@@ -255,91 +255,141 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const T* __restric
     }
 }
 
-// The gradient by a row's logits.  Softmax over all experts reads the whole row (V logits a lane); the other rules have a
-// gradient at the choices alone: zeros, and the choices' values behind them.
-template <typename T, int V, bool kWide, bool kDense>
+// Sums and maxima over groups of kLanes neighbouring lanes.
+template <int kLanes>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+template <int kLanes>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+
+// A choice as a lane of the backward pass has it: its gradient (times the scale) and its expert's logit; expert -1: none.
+// kLanes lanes a token, the lane's place among them its choice.  A token that names an expert twice has both
+// gradients: joined() gives each of its lanes their sum.
+template <typename T, int kLanes>
+struct RouteChoice {
+    int32_t expert = -1;
+    float g = 0.0f, l = 0.0f;
+    uint32_t same;
+    bool twice;
+    int k;
+
+    __device__ __forceinline__ RouteChoice(const T* row, const int32_t* experts, const float* dweights, bool in, int64_t token,
+                                           int lane, int E, int k_, float scale, int32_t* status)
+        : k(k_) {
+        const int j = lane % kLanes;
+        if (in && j < k) {
+            expert = checked_row(experts[token * k + j], E, status);
+            if (expert >= 0) {
+                g = dweights[token * k + j] * scale;
+                l = RouteType<T>::to_float(row[expert]);
+            }
+        }
+        same = __match_any_sync(0xffffffffu, expert >= 0 ? expert * (32 / kLanes) + lane / kLanes : -1);
+        twice = __any_sync(0xffffffffu, expert >= 0 && (same & (same - 1)) != 0);
+    }
+    __device__ __forceinline__ bool chosen() const { return expert >= 0; }
+    __device__ __forceinline__ float joined(float v) const {
+        if (!twice) return v;
+        float all = 0.0f;
+        const int first = (threadIdx.x & 31) / kLanes * kLanes;
+        for (int j = 0; j < k; ++j) {
+            const float other = __shfl_sync(0xffffffffu, v, first + j);
+            if (same >> (first + j) & 1u) all += other;
+        }
+        return all;
+    }
+};
+
+// The gradient by a row's logits for softmax over all experts, which reads the whole row: a warp a token, V logits a lane.
+template <typename T, int V, bool kWide>
 __global__ void __launch_bounds__(kRouteThreads)
-    route_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ experts,
-                          const float* __restrict__ dweights, int64_t tokens, int E, int k, int flags, float scale,
-                          int wide, T* __restrict__ dlogits, int32_t* status) {
-    using Type = RouteType<T>;
+    route_backward_dense_kernel(const T* __restrict__ logits, const int32_t* __restrict__ experts,
+                                const float* __restrict__ dweights, int64_t tokens, int E, int k, float scale,
+                                T* __restrict__ dlogits, int32_t* status) {
     using Row = RouteRow<T, V, kWide>;
     pdl_wait_prerequisites();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const bool sigmoid = flags & RGG_ROUTE_SIGMOID, renormalize = flags & RGG_ROUTE_RENORMALIZE;
     for (RowItems it(tokens, 1); it.left(); it.next()) {
         const T* row = logits + it.item * E;
         T* out = dlogits + it.item * E;
         float x[V];
-        if constexpr (kDense) Row::load(row, E, lane, x);
-        int32_t e = -1;
-        float g = 0.0f, l = 0.0f;
-        if (lane < k) {
-            e = checked_row(experts[it.item * k + lane], E, status);
-            if (e >= 0) {
-                g = dweights[it.item * k + lane] * scale;
-                l = Type::to_float(row[e]);
-            }
+        Row::load(row, E, lane, x);
+        const RouteChoice<T, 32> c(row, experts, dweights, true, it.item, lane, E, k, scale, status);
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) top = fmaxf(top, x[i]);
+        top = warp_max(top);
+        if (top == -INFINITY) top = 0.0f;  // all masked: every weight is 0
+        float total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = expf(x[i] - top);
+            total += x[i];
         }
-        const bool chosen = e >= 0;
-        // an expert that the row names twice has both gradients: each of its lanes then holds their sum
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        const bool twice = __any_sync(0xffffffffu, chosen && (same & (same - 1)) != 0);
-        auto joined = [&](float v) {
-            if (!twice) return v;
-            float all = 0.0f;
-            for (int j = 0; j < k; ++j) {
-                const float other = __shfl_sync(0xffffffffu, v, j);
-                if (same >> j & 1u) all += other;
-            }
-            return all;
-        };
-        float d;
-        if constexpr (kDense) {
-            float top = x[0];
+        const float inverse = 1.0f / not_zero(warp_sum(total));
+        const float s = c.chosen() ? expf(c.l - top) * inverse : 0.0f;
+        const float sum = warp_sum(c.g * s);
 #pragma unroll
-            for (int i = 1; i < V; ++i) top = fmaxf(top, x[i]);
-            top = warp_max(top);
-            if (top == -INFINITY) top = 0.0f;  // all masked: every weight is 0
-            float total = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                x[i] = expf(x[i] - top);
-                total += x[i];
-            }
-            const float inverse = 1.0f / not_zero(warp_sum(total));
-            const float s = chosen ? expf(l - top) * inverse : 0.0f;
-            const float sum = warp_sum(g * s);
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[i] *= -sum * inverse;
-            Row::store(out, E, lane, x);
-            d = s * (joined(g) - sum);
-        } else {
-            if (sigmoid) {
-                const float s = chosen ? sigmoid_f32(l) : 0.0f;
-                d = g * s * (1.0f - s);
-                if (renormalize) {
-                    const float total = warp_sum(s) + kRouteEps;
-                    d = (g - warp_sum(g * (s / total))) / total * s * (1.0f - s);
-                }
-            } else {
-                float top = warp_max(chosen ? l : -INFINITY);
-                if (top == -INFINITY) top = 0.0f;
-                float w = chosen ? expf(l - top) : 0.0f;
-                w = w / not_zero(warp_sum(w));
-                d = w * (g - warp_sum(g * w));
-            }
+        for (int i = 0; i < V; ++i) x[i] *= -sum * inverse;
+        Row::store(out, E, lane, x);
+        const float d = s * (c.joined(c.g) - sum);
+        __syncwarp();  // the row's other values are written before the choices'
+        if (c.chosen()) out[c.expert] = RouteType<T>::from_float(d);
+    }
+}
+
+// For the other rules, which have a gradient at the choices alone: zeros, and the choices' values behind them.  As many
+// tokens a warp as it has lanes for their choices (32,768 tokens x 256, k = 8: a token a warp 9.3 us).
+template <typename T, int kLanes>
+__global__ void __launch_bounds__(kRouteThreads)
+    route_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ experts,
+                          const float* __restrict__ dweights, int64_t tokens, int E, int k, int flags, float scale,
+                          int wide, T* __restrict__ dlogits, int32_t* status) {
+    constexpr int kTokens = 32 / kLanes;
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const bool sigmoid = flags & RGG_ROUTE_SIGMOID, renormalize = flags & RGG_ROUTE_RENORMALIZE;
+    for (RowItems it((tokens + kTokens - 1) / kTokens, 1); it.left(); it.next()) {
+        const int64_t t = it.item * kTokens + lane / kLanes;
+        const bool in = t < tokens;
+        T* out = dlogits + t * E;
+        if (in) {
+            const int j = lane % kLanes;
             if (wide) {  // rows of whole 16 bytes
                 const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                for (int i = lane; i < wide; i += 32) reinterpret_cast<uint4*>(out)[i] = zero;
+                for (int i = j; i < wide; i += kLanes) reinterpret_cast<uint4*>(out)[i] = zero;
             } else {
-                for (int i = lane; i < E; i += 32) out[i] = Type::from_float(0.0f);
+                for (int i = j; i < E; i += kLanes) out[i] = RouteType<T>::from_float(0.0f);
             }
-            d = joined(chosen ? d : 0.0f);
         }
-        __syncwarp();  // the row's other values are written before the choices'
-        if (chosen) out[e] = Type::from_float(d);
+        const RouteChoice<T, kLanes> c(logits + t * E, experts, dweights, in, t, lane, E, k, scale, status);
+        float d;
+        if (sigmoid) {
+            const float s = c.chosen() ? sigmoid_f32(c.l) : 0.0f;
+            d = c.g * s * (1.0f - s);
+            if (renormalize) {
+                const float total = group_sum<kLanes>(s) + kRouteEps;
+                d = (c.g - group_sum<kLanes>(c.g * (s / total))) / total * s * (1.0f - s);
+            }
+        } else {
+            float top = group_max<kLanes>(c.chosen() ? c.l : -INFINITY);
+            if (top == -INFINITY) top = 0.0f;
+            float w = c.chosen() ? expf(c.l - top) : 0.0f;
+            w = w / not_zero(group_sum<kLanes>(w));
+            d = w * (c.g - group_sum<kLanes>(c.g * w));
+        }
+        d = c.joined(c.chosen() ? d : 0.0f);
+        __syncwarp();  // the zeros are written before the choices' values
+        if (c.chosen()) out[c.expert] = RouteType<T>::from_float(d);
     }
 }
 
@@ -362,9 +412,9 @@ static cudaError_t launch_route(const RouteCall& c) {
     if (!c.dlogits)
         return launch_chained(route_kernel<T, V, kWide>, grid, kRouteThreads, 0, c.st, static_cast<const T*>(c.logits), c.T,
                               c.E, c.k, c.flags, c.scale, c.experts, c.weights);
-    return launch_chained(route_backward_kernel<T, V, kWide, true>, grid, kRouteThreads, 0, c.st,
+    return launch_chained(route_backward_dense_kernel<T, V, kWide>, grid, kRouteThreads, 0, c.st,
                           static_cast<const T*>(c.logits), static_cast<const int32_t*>(c.experts), c.dweights, c.T, c.E,
-                          c.k, c.flags, c.scale, 0, static_cast<T*>(c.dlogits), c.status);
+                          c.k, c.scale, static_cast<T*>(c.dlogits), c.status);
 }
 
 template <typename T>
@@ -373,9 +423,12 @@ static cudaError_t launch_route_for(const RouteCall& c) {
     const bool aligned = host_aligned(c.logits, 16) && host_aligned(c.dlogits, 16);
     if (c.dlogits && (c.flags & (RGG_ROUTE_SIGMOID | RGG_ROUTE_RENORMALIZE))) {
         const int wide = (c.E % kPer == 0 && host_aligned(c.dlogits, 16)) ? c.E / kPer : 0;
-        return launch_chained(route_backward_kernel<T, 1, false, false>, row_grid(c.T, kRouteThreads), kRouteThreads, 0,
-                              c.st, static_cast<const T*>(c.logits), static_cast<const int32_t*>(c.experts), c.dweights,
-                              c.T, c.E, c.k, c.flags, c.scale, wide, static_cast<T*>(c.dlogits), c.status);
+        const int tokens = c.k <= 8 ? 4 : c.k <= 16 ? 2 : 1;  // a warp
+        auto kernel = tokens == 4 ? route_backward_kernel<T, 8> : tokens == 2 ? route_backward_kernel<T, 16>
+                                                                              : route_backward_kernel<T, 32>;
+        return launch_chained(kernel, row_grid((c.T + tokens - 1) / tokens, kRouteThreads), kRouteThreads, 0, c.st,
+                              static_cast<const T*>(c.logits), static_cast<const int32_t*>(c.experts), c.dweights, c.T,
+                              c.E, c.k, c.flags, c.scale, wide, static_cast<T*>(c.dlogits), c.status);
     }
     if (aligned && c.E == 256) return launch_route<T, 8, true>(c);
     if constexpr (kPer == 4) {

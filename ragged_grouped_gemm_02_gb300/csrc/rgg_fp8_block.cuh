@@ -52,17 +52,9 @@ struct FpMaps {
     CUtensorMap x128, x32, w128, w64;
 };
 
-constexpr int kFpParts = 2;  // parts of 128 columns, each added up by a warp of every 32 TMEM lanes
-constexpr int kFpCols = 128 / kFpParts;
+constexpr int kFpSums = 64;      // columns whose sums a thread holds
 constexpr int kFpMostSlots = 4;  // accumulators, at most
 constexpr int kFpFactors = 8;    // stages whose scales' products are held, at most
-constexpr int kFpEpiWarps = 4 * kFpParts;
-constexpr int kFpThreads = 128 + 32 * kFpEpiWarps;
-// Registers a thread: at launch, and how the four warps that copy and issue and the
-// epilogue's share them out.  (An increase waits until the block has as many left,
-// so the shares must add up to the launch's, which the host checks.)
-constexpr int kFpRegsLaunch = 168, kFpRegsIssue = 40, kFpRegsEpi = 232;
-static_assert(128 * kFpRegsIssue + 32 * kFpEpiWarps * kFpRegsEpi == kFpThreads * kFpRegsLaunch, "");
 constexpr uint32_t kFpTile = 128u * 128u;  // bytes of 128 rows of a stage
 
 // The tiles: rows by columns of W.
@@ -74,6 +66,20 @@ __host__ __device__ constexpr int fp_halves(int shape) { return shape == kFpNarr
 __host__ __device__ constexpr uint32_t fp_w_bytes(int shape) {
     return fp_halves(shape) * kFpTile / (shape == kFpPair ? 2 : 1);
 }
+// Epilogue warps for each 32 TMEM lanes, which share out the columns, and threads: four warps that copy, issue and
+// multiply scales, and the epilogue's.
+__host__ __device__ constexpr int fp_parts(int shape) { return 128 * fp_halves(shape) / kFpSums; }
+__host__ __device__ constexpr int fp_threads(int shape) { return 128 + 128 * fp_parts(shape); }
+// Registers a thread: at launch, and how the first four warps and the epilogue's share them out.  (An increase waits
+// until the block has as many left, so the shares must add up to the launch's, which the host checks.)
+__host__ __device__ constexpr int fp_regs_launch(int shape) { return shape == kFpNarrow ? 168 : 96; }
+__host__ __device__ constexpr int fp_regs_issue(int shape) { return shape == kFpNarrow ? 40 : 32; }
+__host__ __device__ constexpr int fp_regs_epilogue(int shape) { return shape == kFpNarrow ? 232 : 112; }
+__host__ __device__ constexpr bool fp_regs_add_up(int shape) {
+    return 128 * fp_regs_issue(shape) + (fp_threads(shape) - 128) * fp_regs_epilogue(shape) ==
+           fp_threads(shape) * fp_regs_launch(shape);
+}
+static_assert(fp_regs_add_up(kFpPair) && fp_regs_add_up(kFpWide) && fp_regs_add_up(kFpNarrow), "");
 
 struct FpSmem {
     uint32_t b_off, factor_off, top_off, bar_off, misc_off, off_off, pre_off, total;
@@ -84,8 +90,8 @@ __host__ __device__ inline FpSmem fp_smem(int stages, int E, uint32_t w_bytes, b
     const uint32_t ex = 4u * static_cast<uint32_t>(E + 1);
     p.b_off = stages * kFpTile;
     p.factor_off = p.b_off + stages * w_bytes;            // [kFpFactors][128][2] products of a row's and the columns' scales
-    p.top_off = p.factor_off + 1024u * kFpFactors;        // gate-up: [2][kFpParts][128] magnitudes
-    p.bar_off = p.top_off + (gate_up ? 1024u * kFpParts : 0u);  // full[S], empty[S], acc_full[4], acc_empty[4], top[4], drain
+    p.top_off = p.factor_off + 1024u * kFpFactors;        // gate-up: [2][4][128] magnitudes
+    p.bar_off = p.top_off + (gate_up ? 4096u : 0u);  // full[S], empty[S], acc_full[4], acc_empty[4], top[4], drain
     p.misc_off = p.bar_off + 8u * (2u * stages + 2u * kFpMostSlots + 5u);
     p.misc_off = (p.misc_off + 15u) & ~15u;
     p.off_off = p.misc_off + 16u;
@@ -118,16 +124,6 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
         asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
     else
         asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Each thread reads its TMEM lane's 16 columns from taddr's on.
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
 }
 
 // Two fp32 sums in a register pair: sum += v * f, each rounded once, in one instruction.
@@ -172,6 +168,8 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
     constexpr int kHalves = fp_halves(kShape);
     constexpr int kOutN = kGateUp ? 128 : 128 * kHalves;
     constexpr uint32_t kWBytes = fp_w_bytes(kShape);
+    constexpr int kParts = fp_parts(kShape);
+    constexpr int kCols = 128 / kParts;            // columns of each half that a thread adds up
     constexpr uint32_t kHalfBytes = kFpTile;       // single CTAs: 128 rows of W
     constexpr uint32_t kSlotCols = 128 * kHalves;  // an accumulator; all of TMEM's 512 columns are in use
     constexpr uint32_t kSlots = 512 / kSlotCols;
@@ -223,9 +221,9 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
         }
         for (int a = 0; a < static_cast<int>(kSlots); ++a) {
             mbar_init(accf_bar(a), 1 + 2);  // the MMAs' commit, and two warps with the scales
-            mbar_init(acce_bar(a), (kPair ? 2 : 1) * kFpEpiWarps);
+            mbar_init(acce_bar(a), (kPair ? 2 : 1) * 4 * kParts);
         }
-        for (int q = 0; q < 4; ++q) mbar_init(top_bar(q), kFpParts);
+        for (int q = 0; q < 4; ++q) mbar_init(top_bar(q), kParts);
         mbar_init(drain_bar, 1);
         misc[1] = 0u;
         fence_mbar_init();
@@ -265,163 +263,163 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
     auto halves_of = [&](const TileCoord& c) -> int { return kHalves == 2 && (kGateUp || N - c.col0 > 128) ? 2 : 1; };
 
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFpRegsIssue));
-    if (warp == 0) {
-        // ---------------------------------------------------------- producer
-        if ((args.debug_flags & kDebugProducerStall) == 0) {
-            const uint32_t lead = elect_one();
-            int st = 0;
-            uint32_t ph = 0, issued = 0;
-            const uint32_t full0 = kPair ? map_to_rank(full_bar(0), 0) : full_bar(0);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(fp_regs_issue(kShape)));
+        if (warp == 0) {
+            // ---------------------------------------------------------- producer
+            if ((args.debug_flags & kDebugProducerStall) == 0) {
+                const uint32_t lead = elect_one();
+                int st = 0;
+                uint32_t ph = 0, issued = 0;
+                const uint32_t full0 = kPair ? map_to_rank(full_bar(0), 0) : full_bar(0);
+                bool ok = true;
+                for (int32_t t = unit; ok && t < T; t += units) {
+                    const TileCoord c = tile_at(t);
+                    const int halves = halves_of(c);
+                    // rows of x in each CTA, and the boxes that bring them: one of
+                    // 128 rows, or as many of 32 as hold rows of the expert
+                    auto boxes_of = [&](int32_t rows) { return rows > 96 ? 4 : (rows + 31) / 32; };
+                    const int32_t rows = c.rows - 128 * static_cast<int32_t>(rank);
+                    const int boxes = rows > 0 ? boxes_of(rows) : 0;
+                    const int32_t x_row = c.row0 + 128 * static_cast<int32_t>(rank);
+                    // first row of W in this CTA: a pair's second one has the second half, or half of the only one
+                    const int32_t w_row = c.col0 + (kPair && rank ? (kGateUp ? N : 64 * halves) : 0);
+                    uint32_t bytes = 0;
+                    if (rank == 0) {
+                        const int more = kPair && c.rows > 128 ? boxes_of(c.rows - 128) : 0;  // the peer's
+                        bytes = (boxes + more) * 4096u + halves * kFpTile;  // of W: a pair's halves are shared out
+                    }
+                    for (int kb = 0; kb < KB; ++kb) {
+                        if (!wait(empty_bar(st), ph ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t bar = full0 + 8u * st;
+                        if (rank == 0) expect_tx_if(lead, full_bar(st), bytes);
+                        const uint32_t a = a0 + st * kFpTile, b = b0 + st * kWBytes;
+                        const int32_t kx = kb * kFpBlock;
+                        auto x_ok = [&](int32_t row) {
+                            return RGG_BOUNDS_OK(x_box_ok(kx, row, args.K, args.M_tot, 1), args.status);
+                        };
+                        // a pair's second CTA may start past the last column: the copy zero-fills its rows
+                        auto w_ok = [&](int32_t row) {
+                            return RGG_BOUNDS_OK(w_box_ok(kx, row, c.expert, args.K, cols_w + 64, E, 1), args.status);
+                        };
+                        if (boxes == 4) {
+                            if (x_ok(x_row)) load_3d_if<kPair>(lead, a, &maps.x128, bar, kx, x_row, 0);
+                        } else {
+                            for (int i = 0; i < boxes; ++i)
+                                if (x_ok(x_row + 32 * i))
+                                    load_3d_if<kPair>(lead, a + 4096u * i, &maps.x32, bar, kx, x_row + 32 * i, 0);
+                        }
+                        if constexpr (kPair) {
+                            if (w_ok(w_row)) load_3d_if<kPair>(lead, b, halves == 1 ? &maps.w64 : &maps.w128, bar, kx, w_row, c.expert);
+                        } else {
+                            if (w_ok(w_row)) load_3d_if<kPair>(lead, b, &maps.w128, bar, kx, w_row, c.expert);
+                            if (halves == 2 && w_ok(w_row + (kGateUp ? N : 128)))
+                                load_3d_if<kPair>(lead, b + kHalfBytes, &maps.w128, bar, kx, w_row + (kGateUp ? N : 128), c.expert);
+                        }
+                        ++issued;
+                        if (++st == S) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+                if (!ok) {
+                    // copies are counted on the (leader's) full barriers, which a pair's second CTA does not watch
+                    const uint32_t n = issued < static_cast<uint32_t>(S) ? issued : static_cast<uint32_t>(S);
+                    if (rank == 0)
+                        for (uint32_t i = issued - n; i < issued; ++i)
+                            wait_bounded(full_bar(static_cast<int>(i % S)), (i / S) & 1u, kDrainLimitNs);
+                    else
+                        spin_ns(200000ull);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ----------------------------------------------- MMA issuer (leader)
+            if (rank == 0) {
+                const uint32_t lead = elect_one();
+                int st = 0;
+                uint32_t ph = 0, n = 0;  // stages multiplied
+                const uint64_t a_desc = sw128_desc(a0, 16u, 1024u), b_desc = sw128_desc(b0, 16u, 1024u);
+                bool ok = true;
+                for (int32_t t = unit; ok && t < T; t += units) {
+                    const uint32_t idesc = idesc_e4m3_f32(BM, 128 * halves_of(tile_at(t)), false);
+                    for (int kb = 0; kb < KB; ++kb, ++n) {
+                        // the slot's last sums have been read, and the stage's operands are here
+                        const uint32_t slot = n % kSlots;
+                        if ((n >= kSlots && !wait(acce_bar(slot), (n / kSlots - 1) & 1u)) || !wait(full_bar(st), ph)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        const uint64_t ad = a_desc + st * (kFpTile >> 4);
+                        const uint64_t bd = b_desc + st * (kWBytes >> 4);
+                        const int left = args.K - kb * kFpBlock;
+                        const int steps = left >= kFpBlock ? 4 : (left + 31) / 32;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (j >= steps) break;
+                            mma_e4m3_if<kPair>(lead, tmem_base + slot * kSlotCols, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u);
+                        }
+                        commit_if<kPair>(lead, accf_bar(slot));
+                        commit_if<kPair>(lead, empty_bar(st));
+                        if (++st == S) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+                if (!ok) {
+                    commit_if<kPair>(lead, drain_bar);
+                    wait_bounded(drain_bar, 0u, kDrainLimitNs);
+                }
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ scales
+            // Products of the scales of this CTA's rows (64 a warp) and of the columns, a stage at
+            // a time; the epilogue's wait for a stage is for these too.  Stage n takes the place of
+            // stage n - kRing.  Its sums were made before the epilogue gave back the accumulator of
+            // stage n - kRing + 1, and that before stage n - kRing + 1 + kSlots was multiplied:
+            // so this waits for that product.  (A phase on would need stage n's scales.)
+            constexpr uint32_t kBehind = kRing - 1 - kSlots;
+            const int row0 = 64 * (warp - 2) + lane;
+            float2* out = reinterpret_cast<float2*>(gbase + sp.factor_off) + row0;
+            const int nblocks = static_cast<int>(fp_blocks(cols_w));
+            uint32_t n = 0;
             bool ok = true;
             for (int32_t t = unit; ok && t < T; t += units) {
                 const TileCoord c = tile_at(t);
-                const int halves = halves_of(c);
-                // rows of x in each CTA, and the boxes that bring them: one of
-                // 128 rows, or as many of 32 as hold rows of the expert
-                auto boxes_of = [&](int32_t rows) { return rows > 96 ? 4 : (rows + 31) / 32; };
-                const int32_t rows = c.rows - 128 * static_cast<int32_t>(rank);
-                const int boxes = rows > 0 ? boxes_of(rows) : 0;
-                const int32_t x_row = c.row0 + 128 * static_cast<int32_t>(rank);
-                // first row of W in this CTA: a pair's second one has the second half, or half of the only one
-                const int32_t w_row = c.col0 + (kPair && rank ? (kGateUp ? N : 64 * halves) : 0);
-                uint32_t bytes = 0;
-                if (rank == 0) {
-                    const int more = kPair && c.rows > 128 ? boxes_of(c.rows - 128) : 0;  // the peer's
-                    bytes = (boxes + more) * 4096u + halves * kFpTile;  // of W: a pair's halves are shared out
-                }
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!wait(empty_bar(st), ph ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t bar = full0 + 8u * st;
-                    if (rank == 0) expect_tx_if(lead, full_bar(st), bytes);
-                    const uint32_t a = a0 + st * kFpTile, b = b0 + st * kWBytes;
-                    const int32_t kx = kb * kFpBlock;
-                    auto x_ok = [&](int32_t row) {
-                        return RGG_BOUNDS_OK(x_box_ok(kx, row, args.K, args.M_tot, 1), args.status);
-                    };
-                    // a pair's second CTA may start past the last column: the copy zero-fills its rows
-                    auto w_ok = [&](int32_t row) {
-                        return RGG_BOUNDS_OK(w_box_ok(kx, row, c.expert, args.K, cols_w + 64, E, 1), args.status);
-                    };
-                    if (boxes == 4) {
-                        if (x_ok(x_row)) load_3d_if<kPair>(lead, a, &maps.x128, bar, kx, x_row, 0);
-                    } else {
-                        for (int i = 0; i < boxes; ++i)
-                            if (x_ok(x_row + 32 * i))
-                                load_3d_if<kPair>(lead, a + 4096u * i, &maps.x32, bar, kx, x_row + 32 * i, 0);
-                    }
-                    if constexpr (kPair) {
-                        if (w_ok(w_row)) load_3d_if<kPair>(lead, b, halves == 1 ? &maps.w64 : &maps.w128, bar, kx, w_row, c.expert);
-                    } else {
-                        if (w_ok(w_row)) load_3d_if<kPair>(lead, b, &maps.w128, bar, kx, w_row, c.expert);
-                        if (halves == 2 && w_ok(w_row + (kGateUp ? N : 128)))
-                            load_3d_if<kPair>(lead, b + kHalfBytes, &maps.w128, bar, kx, w_row + (kGateUp ? N : 128), c.expert);
-                    }
-                    ++issued;
-                    if (++st == S) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
-                }
-            }
-            if (!ok) {
-                // copies are counted on the (leader's) full barriers, which a pair's second CTA does not watch
-                const uint32_t n = issued < static_cast<uint32_t>(S) ? issued : static_cast<uint32_t>(S);
-                if (rank == 0)
-                    for (uint32_t i = issued - n; i < issued; ++i)
-                        wait_bounded(full_bar(static_cast<int>(i % S)), (i / S) & 1u, kDrainLimitNs);
-                else
-                    spin_ns(200000ull);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ----------------------------------------------- MMA issuer (leader)
-        if (rank == 0) {
-            const uint32_t lead = elect_one();
-            int st = 0;
-            uint32_t ph = 0, n = 0;  // stages multiplied
-            const uint64_t a_desc = sw128_desc(a0, 16u, 1024u), b_desc = sw128_desc(b0, 16u, 1024u);
-            bool ok = true;
-            for (int32_t t = unit; ok && t < T; t += units) {
-                const uint32_t idesc = idesc_e4m3_f32(BM, 128 * halves_of(tile_at(t)), false);
+                const int r0 = 128 * static_cast<int>(rank) + row0;
+                const float* x0 = args.sx + static_cast<int64_t>(c.row0 + (r0 < c.rows ? r0 : 0)) * KB;
+                const float* x1 = args.sx + static_cast<int64_t>(c.row0 + (r0 + 32 < c.rows ? r0 + 32 : 0)) * KB;
+                const float* w0 = args.sw + (static_cast<int64_t>(c.expert) * nblocks + c.col0 / kFpBlock) * KB;
+                const float* w1 = halves_of(c) == 2 ? w0 + static_cast<int64_t>(kGateUp ? N / kFpBlock : 1) * KB : w0;
+                float a0 = x0[0], a1 = x1[0], b0 = w0[0], b1 = w1[0];
                 for (int kb = 0; kb < KB; ++kb, ++n) {
-                    // the slot's last sums have been read, and the stage's operands are here
-                    const uint32_t slot = n % kSlots;
-                    if ((n >= kSlots && !wait(acce_bar(slot), (n / kSlots - 1) & 1u)) || !wait(full_bar(st), ph)) {
+                    const float2 f0 = make_float2(a0 * b0, a0 * b1), f1 = make_float2(a1 * b0, a1 * b1);
+                    if (kb + 1 < KB) {
+                        a0 = x0[kb + 1];
+                        a1 = x1[kb + 1];
+                        b0 = w0[kb + 1];
+                        b1 = w1[kb + 1];
+                    }
+                    if (n >= kBehind && !wait(accf_bar((n - kBehind) % kSlots), ((n - kBehind) / kSlots) & 1u)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after_sync();
-                    const uint64_t ad = a_desc + st * (kFpTile >> 4);
-                    const uint64_t bd = b_desc + st * (kWBytes >> 4);
-                    const int left = args.K - kb * kFpBlock;
-                    const int steps = left >= kFpBlock ? 4 : (left + 31) / 32;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j >= steps) break;
-                        mma_e4m3_if<kPair>(lead, tmem_base + slot * kSlotCols, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u);
-                    }
-                    commit_if<kPair>(lead, accf_bar(slot));
-                    commit_if<kPair>(lead, empty_bar(st));
-                    if (++st == S) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
+                    out[(n % kRing) * 128] = f0;
+                    out[(n % kRing) * 128 + 32] = f1;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(accf_bar(n % kSlots));
                 }
             }
-            if (!ok) {
-                commit_if<kPair>(lead, drain_bar);
-                wait_bounded(drain_bar, 0u, kDrainLimitNs);
-            }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
-        // ------------------------------------------------------------ scales
-        // Products of the scales of this CTA's rows (64 a warp) and of the columns, a stage at
-        // a time; the epilogue's wait for a stage is for these too.  Stage n takes the place of
-        // stage n - kRing.  Its sums were made before the epilogue gave back the accumulator of
-        // stage n - kRing + 1, and that before stage n - kRing + 1 + kSlots was multiplied:
-        // so this waits for that product.  (A phase on would need stage n's scales.)
-        constexpr uint32_t kBehind = kRing - 1 - kSlots;
-        const int row0 = 64 * (warp - 2) + lane;
-        float2* out = reinterpret_cast<float2*>(gbase + sp.factor_off) + row0;
-        const int nblocks = static_cast<int>(fp_blocks(cols_w));
-        uint32_t n = 0;
-        bool ok = true;
-        for (int32_t t = unit; ok && t < T; t += units) {
-            const TileCoord c = tile_at(t);
-            const int r0 = 128 * static_cast<int>(rank) + row0;
-            const float* x0 = args.sx + static_cast<int64_t>(c.row0 + (r0 < c.rows ? r0 : 0)) * KB;
-            const float* x1 = args.sx + static_cast<int64_t>(c.row0 + (r0 + 32 < c.rows ? r0 + 32 : 0)) * KB;
-            const float* w0 = args.sw + (static_cast<int64_t>(c.expert) * nblocks + c.col0 / kFpBlock) * KB;
-            const float* w1 = halves_of(c) == 2 ? w0 + static_cast<int64_t>(kGateUp ? N / kFpBlock : 1) * KB : w0;
-            float a0 = x0[0], a1 = x1[0], b0 = w0[0], b1 = w1[0];
-            for (int kb = 0; kb < KB; ++kb, ++n) {
-                const float2 f0 = make_float2(a0 * b0, a0 * b1), f1 = make_float2(a1 * b0, a1 * b1);
-                if (kb + 1 < KB) {
-                    a0 = x0[kb + 1];
-                    a1 = x1[kb + 1];
-                    b0 = w0[kb + 1];
-                    b1 = w1[kb + 1];
-                }
-                if (n >= kBehind && !wait(accf_bar((n - kBehind) % kSlots), ((n - kBehind) / kSlots) & 1u)) {
-                    ok = false;
-                    break;
-                }
-                out[(n % kRing) * 128] = f0;
-                out[(n % kRing) * 128 + 32] = f1;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(accf_bar(n % kSlots));
-            }
-        }
-        __syncwarp();
-    }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFpRegsEpi));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(fp_regs_epilogue(kShape)));
         // ---------------------------------------------------------- epilogue
         auto epi_wait = [&](uint32_t bar, uint32_t parity) -> bool {
             return warp_wait_inline<kPair>(bar, parity, abort_flag, peer_flag, args.status, args.timeout_ns);
@@ -438,67 +436,48 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
             const TileCoord c = tile_at(t);
             const bool row_ok = r_local < c.rows;
             const int64_t row = static_cast<int64_t>(c.row0) + r_local;
-            const int col = part * kFpCols;  // first column of the thread's sums, in each half
-            uint64_t sums[kHalves * kFpCols / 2];
+            const int col = part * kCols;  // first column of the thread's sums, in each half
+            uint64_t sums[kFpSums / 2];
 #pragma unroll
-            for (int i = 0; i < kHalves * kFpCols / 2; ++i) sums[i] = 0u;
-            constexpr int kChunks = kHalves * kFpCols / 32, kPerHalf = kFpCols / 32;
-            uint32_t v[2][32];
-            auto load = [&](uint32_t slot, int i) {
-                const uint32_t c0 = slot * kSlotCols + col + 128 * (i / kPerHalf) + 32 * (i % kPerHalf);
-                if (RGG_BOUNDS_OK(tmem_cols_ok(c0, 32, 512), args.status)) tmem_ld_32x32b_x32(t_row + c0, v[i & 1]);
-            };
-            auto full = [&]() -> bool {  // the n-th stage's products are there
-                ok = epi_wait(accf_bar(n % kSlots), (n / kSlots) & 1u);
-                tc_fence_after_sync();
-                return ok;
-            };
-            if (!full()) break;
-            load(n % kSlots, 0);
-            load(n % kSlots, 1);
-            float2 factor = factors[(n % kRing) * 128];
+            for (int i = 0; i < kFpSums / 2; ++i) sums[i] = 0u;
 #pragma unroll 1
-            for (int kb = 0; kb < KB; ++kb) {
+            for (int kb = 0; kb < KB; ++kb, ++n) {
                 const uint32_t slot = n % kSlots;
-                ++n;
-                float2 next = factor;
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    if ((i & 1) == 0) {
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[0][j]), "+r"(v[1][j]));  // not before the wait
-                        if (i + 2 == kChunks) {  // all of the slot has been read
-                            tc_fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) arrive_relaxed<kPair>(acce0 + 8u * slot);
-                        }
-                    }
-                    const uint64_t ff = twice(i / kPerHalf ? factor.y : factor.x);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) add_scaled2(sums[16 * i + j], v[i & 1][2 * j], v[i & 1][2 * j + 1], ff);
-                    if (i + 2 < kChunks) {
-                        load(slot, i + 2);
-                    } else if (kb + 1 < KB) {
-                        if (i + 2 == kChunks) {
-                            if (!full()) break;
-                            next = factors[(n % kRing) * 128];
-                        }
-                        load(n % kSlots, i + 2 - kChunks);
-                    }
+                if (!epi_wait(accf_bar(slot), (n / kSlots) & 1u)) {
+                    ok = false;
+                    break;
                 }
-                if (!ok) break;
-                factor = next;
+                tc_fence_after_sync();
+                const float2 factor = factors[(n % kRing) * 128];
+                // 32 columns at a time; columns past N hold nothing that is read
+#pragma unroll
+                for (int i = 0; i < kFpSums / 32; ++i) {
+                    uint32_t v[32] = {};
+                    const int half = 32 * i / kCols;
+                    const uint32_t at = slot * kSlotCols + 128 * half + col + 32 * i % kCols;
+                    if (RGG_BOUNDS_OK(tmem_cols_ok(at, 32, 512), args.status)) tmem_ld_32x32b_x32(t_row + at, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[j]));  // not before the wait
+                    if (i + 1 == kFpSums / 32) {  // all of the accumulator has been read
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) arrive_relaxed<kPair>(acce0 + 8u * slot);
+                    }
+                    const uint64_t f = twice(half ? factor.y : factor.x);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) add_scaled2(sums[16 * i + j], v[2 * j], v[2 * j + 1], f);
+                }
             }
             if (!ok) break;
-            float sum[kHalves * kFpCols];
+            float sum[kFpSums];
 #pragma unroll
-            for (int i = 0; i < kHalves * kFpCols; ++i) sum[i] = half_of(sums[i / 2], i & 1);
+            for (int i = 0; i < kFpSums; ++i) sum[i] = half_of(sums[i / 2], i & 1);
             const int32_t row_lo = s_off[c.expert], row_hi = s_off[c.expert + 1];
             if constexpr (!kGateUp) {
 #pragma unroll
-                for (int i = 0; i < kHalves * kFpCols / 32; ++i) {
-                    const int cc = c.col0 + 128 * (32 * i / kFpCols) + col + 32 * i % kFpCols;
+                for (int i = 0; i < kFpSums / 32; ++i) {
+                    const int cc = c.col0 + 128 * (32 * i / kCols) + col + 32 * i % kCols;
                     if (cc >= N) continue;
                     uint32_t w[16];
 #pragma unroll
@@ -519,10 +498,10 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                     }
                 }
             } else {
-                // H, its largest magnitude over the 128 columns (two warps', through
+                // H, its largest magnitude over the 128 columns (all parts', through
                 // shared memory, two buffers by turns: a warp is in the next but one
                 // tile's only when all have left this one's), codes and scale
-                constexpr int kH = kFpCols;
+                constexpr int kH = kCols;
                 float top = kFpLeast;
 #pragma unroll
                 for (int i = 0; i < kH; ++i) {
@@ -530,7 +509,7 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                     sum[i] = __fdividef(g, 1.0f + __expf(-g)) * sum[kH + i];
                     top = fmaxf(top, fabsf(sum[i]));
                 }
-                float* s_top = reinterpret_cast<float*>(gbase + sp.top_off) + (tiles & 1) * (128 * kFpParts);
+                float* s_top = reinterpret_cast<float*>(gbase + sp.top_off) + (tiles & 1) * (128 * kParts);
                 s_top[part * 128 + 32 * q + lane] = top;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(top_bar(q));
@@ -539,7 +518,7 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                     break;
                 }
 #pragma unroll
-                for (int i = 0; i < kFpParts; ++i) top = fmaxf(top, s_top[i * 128 + 32 * q + lane]);
+                for (int i = 0; i < kParts; ++i) top = fmaxf(top, s_top[i * 128 + 32 * q + lane]);
                 const float inv = kFpMax / top;
                 uint32_t w[kH / 4];
 #pragma unroll
@@ -571,13 +550,13 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
 }
 
 template <int kShape, bool kGateUp>
-__global__ void __launch_bounds__(kFpThreads, 1)
+__global__ void __launch_bounds__(fp_threads(kShape), 1)
     grouped_fp8_block_kernel(const __grid_constant__ FpMaps maps, const __grid_constant__ FpArgs args) {
     fp8_block_tiles<kShape, kGateUp>(maps, args);
 }
 
 template <bool kGateUp>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFpThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp_threads(kFpPair), 1)
     grouped_fp8_block_pair_kernel(const __grid_constant__ FpMaps maps, const __grid_constant__ FpArgs args) {
     fp8_block_tiles<kFpPair, kGateUp>(maps, args);
 }

@@ -17,7 +17,7 @@ constexpr int kFpKernels = 5;  // of which `which` numbers one
 
 // Once for each kernel and device: shared memory up to the device's most, and that its warps find the registers they share
 // out (with other code than was planned for they would wait for ever).
-static cudaError_t prepare_fp8_block(FpKernel kernel, int which, const HostDevice& dev) {
+static cudaError_t prepare_fp8_block(FpKernel kernel, int which, int regs, const HostDevice& dev) {
     static std::atomic<uint64_t> ready[kFpKernels];
     const uint64_t bit = dev.device < 64 ? uint64_t(1) << dev.device : 0;
     if (ready[which].load(std::memory_order_acquire) & bit) return cudaSuccess;
@@ -26,7 +26,7 @@ static cudaError_t prepare_fp8_block(FpKernel kernel, int which, const HostDevic
     cudaFuncAttributes attr;
     err = cudaFuncGetAttributes(&attr, kernel);
     if (err != cudaSuccess) return err;
-    if (attr.numRegs != kFpRegsLaunch) return cudaErrorInvalidKernelImage;
+    if (attr.numRegs != regs) return cudaErrorInvalidKernelImage;
     ready[which].fetch_or(bit, std::memory_order_release);
     return cudaSuccess;
 }
@@ -144,8 +144,8 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
                                           grouped_fp8_block_kernel<kFpWide, false>, grouped_fp8_block_kernel<kFpWide, true>,
                                           grouped_fp8_block_kernel<kFpNarrow, false>};
     const int which = 2 * shape + (gate_up ? 1 : 0);
-    cudaError_t err = prepare_fp8_block(kernels[which], which, dev);
-    if (err == cudaSuccess) err = launch_chained(kernels[which], grid, kFpThreads, smem, st, m, a);
+    cudaError_t err = prepare_fp8_block(kernels[which], which, fp_regs_launch(shape), dev);
+    if (err == cudaSuccess) err = launch_chained(kernels[which], grid, fp_threads(shape), smem, st, m, a);
     return err == cudaSuccess ? RGG_OK : host_cuda_failure(err, "grouped_gemm_fp8_block launch");
 }
 

@@ -9,19 +9,31 @@
 // a scale per row and 128 columns, which the down product reads.
 //
 // The scales are arbitrary fp32 numbers, so the tensor core cannot apply them: each
-// stage of 128 of K by 128 columns is a product of its own, into one of four
-// accumulators in TMEM in turn, and the epilogue warps add it, times its two scales, to
-// the sums that they hold in registers while the next ones are multiplied.
+// stage of 128 of K is a product of its own, into accumulators in TMEM that are used
+// in turn, and the epilogue warps add it, times its two scales, to the sums that they
+// hold in registers while the next stage is multiplied.
 //
-// Two tile shapes, one kernel.  A CTA pair (cta_group::2) computes 256 x 256: each CTA
-// holds 128 rows of x and half of the W rows.  A single CTA computes 128 x 128, or for
-// gate-up 128 x 256 (128 columns of H, whose scale needs them all).
+// Three tile shapes, one kernel.  A CTA pair (cta_group::2) computes 256 x 256: each CTA
+// holds 128 rows of x and half of the W rows, 32 KB a stage.  A single CTA computes 128 x
+// 256 or, for few rows, where the weights' bytes bound the product and more, smaller tiles
+// keep all SMs reading, 128 x 128; gate-up takes 128 columns of gate and of up, as the scale
+// of a block of H needs them all.
 //
-// Persistent over the flat tile list; warp 0 copies, warp 1 issues, warps 4-11 add up
-// and write: two for each 32 TMEM lanes, with half of the columns each.  A thread holds up to
-// 128 sums and 32 values on their way from TMEM, so the epilogue's warps take over registers
-// that the others do not need.
-// A stage holds 128 bytes a row, one swizzle row, K-major on both sides.
+// Persistent over the flat tile list.  Warp 0 copies, warp 1 issues, warps 2 and 3 multiply
+// the stages' scales into shared memory, the others add up and write: two or four for each 32
+// TMEM lanes, 64 columns a thread.  The sums, and what is on its way from TMEM, take more
+// registers than an even share, so the first four warps give up theirs.  A stage holds 128
+// bytes a row, one swizzle row, K-major on both sides.
+//
+// Measured on a GB300 machine, a few calls after a pause: 32 experts x 1,024 rows, 6144 x 4096 580 us on
+// pairs (2 840 TFLOP/s), 592 on 128 x 256, 696 on 128 x 128; 16 rows per expert 127 us (6.3 TB/s); gate-up
+// 64 experts x 256 rows, 1024 x 2 * 1408 64 us.  A stage of a pair then takes 730 cycles.  With
+// the epilogue waiting and answering but adding nothing it takes 570 (the MMAs alone 512 at the
+// nominal rate), without the sums' multiplications 580, without half of the loads from TMEM 730:
+// the sums themselves, 128 x 256 a CTA and stage, set the pace.  Tried: one sum an instruction
+// (621 us), the next stage's loads issued before the last sums of one (no gain, with 8 warps or 16),
+// halves of the columns multiplied and handed over one by one (964), waits that poll (601 to 647).
+// In long runs the product is at the power cap (1.6 GHz; 720 us of uneven experts).
 #pragma once
 
 #include "rgg_fp8_block.h"

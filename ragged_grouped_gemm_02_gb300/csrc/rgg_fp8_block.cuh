@@ -25,7 +25,7 @@
 // registers than an even share, so the first four warps give up theirs.  A stage holds 128
 // bytes a row, one swizzle row, K-major on both sides.
 //
-// Measured on a GB300 machine, a few calls after a pause: 32 experts x 1,024 rows, 6144 x 4096 564 us on
+// Measured on a GB300, a few calls after a pause: 32 experts x 1,024 rows, 6144 x 4096 564 us on
 // pairs (2 920 TFLOP/s), 572 on 128 x 256, 675 on 128 x 128; 16 rows per expert 127 us (6.3 TB/s); gate-up
 // 64 experts x 256 rows, 1024 x 2 * 1408 58 us.  What bounds many rows are the sums, 128 x 256 multiplications
 // and additions a CTA and stage: with the epilogue waiting and answering but adding nothing a pair's

@@ -79,8 +79,8 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
         // pair's tile as for a wide one, and a launch of pairs starts 0.9 us later.  Experts are taken to spread around
         // their mean as choices at random do.  Of 32 experts, 6144 x 4096: with about 1,024 rows each wide tiles take 707
         // us, pairs 722, narrow ones 797; with about 160 rows 179, 174, 211.  Narrow tiles make the most of few (2 experts
-        // x about 1,024 rows, 6144 x 1024: 15.8 us, wide ones 21.9).  On 128 other products (K, N from 2048 x 2048 to 3584 x 7168) the
-        // choice is 0.7 % on average, 13 % at most, behind the best shape.
+        // x about 1,024 rows, 6144 x 1024: 15.8 us, wide ones 21.9).  On 128 other products (2048 x 2048 to 3584 x 7168)
+        // the choice is 0.7 % on average, 13 % at most, behind the best shape.
         const double kb = static_cast<double>(fp_blocks(K));
         const double fixed[3] = {1.46, 1.46, 0.5}, stage[3] = {0.403, 0.403, 0.257}, start[3] = {0.9, 0.0, 0.0};
         const double spread = std::sqrt(avg);

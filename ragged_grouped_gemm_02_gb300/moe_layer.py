@@ -80,6 +80,8 @@ class _Dispatch(torch.autograd.Function):
 def dispatch(X, position):
     """``rgg_dispatch`` of bf16 tokens with its gradient by them; rows of no choice hold unspecified values, and what
     comes back for them is not read."""
+    if X.is_cuda and X.dtype is not torch.bfloat16:
+        raise TypeError("X must be bf16, as its gradient is, not %s (rgg_dispatch takes any type)" % X.dtype)
     return _Dispatch.apply(X, position)
 
 

@@ -169,3 +169,11 @@ def test_equal_calls_give_equal_bits():
         runs.append([out, *torch.autograd.grad(out.float().square().sum(), leaves)])
     for r in runs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(runs[0], r))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_dispatch_with_a_gradient_takes_bf16(dtype):
+    # the gradient is a sum of bf16 rows: refused at the call, not in the backward pass
+    X = torch.zeros(4, 8, dtype=dtype, device="cuda", requires_grad=True)
+    with pytest.raises(TypeError, match="bf16"):
+        dispatch(X, torch.zeros(4, 2, dtype=torch.int32, device="cuda"))

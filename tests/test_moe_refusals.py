@@ -7,7 +7,7 @@ import torch
 import ragged_grouped_gemm_02_gb300 as rgg
 from ragged_grouped_gemm_02_gb300 import _build
 from ragged_grouped_gemm_02_gb300.expert_layer import quantize_experts_fp8
-from ragged_grouped_gemm_02_gb300.moe_layer import dispatch, moe_ffn, moe_ffn_fp8
+from ragged_grouped_gemm_02_gb300.moe_layer import moe_ffn, moe_ffn_fp8
 
 BF16, FP32, I32, FP8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 
@@ -192,10 +192,3 @@ def test_moe_arguments(lib):
     size = lib.rgg_moe_swiglu_fp8_block_workspace
     assert size(4, 4, 5, 32, 128, 32) == size(4, 4, 2, 24, 128, 32) == 0
     assert 0 < size(4, 4, 2, 32, 128, 32) < size(4000, 4, 2, 32, 128, 32)
-
-
-@pytest.mark.parametrize("dtype", [FP32, torch.float16])
-def test_dispatch_with_a_gradient_takes_bf16(dtype):
-    # the gradient is a sum of bf16 rows: refused at the call, not in the backward pass
-    with pytest.raises(TypeError, match="bf16"):
-        dispatch(_t(4, 8, dtype=dtype).requires_grad_(), _t(4, 2, dtype=I32))

@@ -196,7 +196,8 @@ extern "C" rgg_status rgg_sort_by_expert(rgg_handle* h, const int32_t* experts, 
     const int warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(32, room), (chunk + 31) / 32)));
     const size_t smem = 4u * (static_cast<size_t>(warps + 2) * E + 1);
     if (smem > 48 * 1024) {
-        err = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        // the device's most, not this call's: another thread's call may come between this and the launch
+        err = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dev.smem_optin);
         if (err != cudaSuccess) return host_cuda_failure(err, "cudaFuncSetAttribute");
     }
     err = launch_chained(sort_place_kernel, blocks, 32 * warps, smem, st, experts, n, k, E, chunk,

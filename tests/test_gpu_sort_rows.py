@@ -193,3 +193,31 @@ def test_sort_feeds_the_gather_products():
     a = rgg.rgg_grouped_gemm(rgg.rgg_dispatch(X, position), W, offsets, check=True)
     b = rgg.rgg_grouped_gemm_gather(X, row_index, W, offsets, check=True)
     assert torch.equal(a[:rows], b[:rows])
+
+
+def test_sorts_of_two_threads():
+    # tables of 70 KB and 221 KB of shared memory by turns: neither thread's call takes room from the other's
+    import threading
+    cases = [torch.randint(-1, E, (1024, 4), generator=_gen(E), dtype=torch.int32) for E in (512, 2048)]
+    want = [refs.sort(c, E) for c, E in zip(cases, (512, 2048))]
+    errors = []
+
+    def work(i, E):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                experts = cases[i].cuda()
+                for _ in range(300):
+                    got = rgg.rgg_sort_by_expert(experts, E)
+            stream.synchronize()
+            assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want[i]))
+        except BaseException as e:  # shown by the test's thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in ((0, 512), (1, 2048))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert rgg.rgg_query_status() == rgg.RGG_OK

@@ -87,23 +87,26 @@ def dispatch(X, position):
 
 class _Combine(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, Y, position, weights):
+    def forward(ctx, Y, position, weights, whole):
         ctx.save_for_backward(Y, position, weights)
+        ctx.whole = whole
         return rgg_combine(Y, position, weights)
 
     @staticmethod
     @_first_derivatives
     def backward(ctx, dout):
         Y, position, weights = ctx.saved_tensors
-        dY = torch.zeros_like(Y) if ctx.needs_input_grad[0] else False  # rows of no choice: zero
+        dY = False
+        if ctx.needs_input_grad[0]:
+            dY = torch.zeros_like(Y) if ctx.whole else None  # rows of no choice: zero, or unspecified
         dY, dweights = rgg_combine_backward(dout.contiguous(), Y, position, weights, dY,
                                             None if ctx.needs_input_grad[2] else False)
-        return dY, None, dweights
+        return dY, None, dweights, None
 
 
 def combine(Y, position, weights):
     """``rgg_combine`` with its gradients by Y (zero for rows of no choice) and the weights."""
-    return _Combine.apply(Y, position, weights)
+    return _Combine.apply(Y, position, weights, True)
 
 
 def moe_ffn(X, logits, W13, W2, k, *, score="softmax", renormalize=True, scale=1.0):
@@ -116,7 +119,9 @@ def moe_ffn(X, logits, W13, W2, k, *, score="softmax", renormalize=True, scale=1
         raise ValueError("logits must be [T, E] with E = %d experts, not %s" % (W13.shape[0], tuple(logits.shape)))
     experts, weights = route_topk(logits, k, score=score, renormalize=renormalize, scale=scale)
     group_offsets, _, position = rgg_sort_by_expert(experts, W13.shape[0])
-    return combine(expert_ffn(dispatch(X, position), W13, W2, group_offsets), position, weights)
+    Y = expert_ffn(dispatch(X, position), W13, W2, group_offsets)
+    # whose backward pass reads the experts' rows alone: the others' gradient need not be filled with zeros
+    return _Combine.apply(Y, position, weights, False)
 
 
 def moe_ffn_fp8(X, logits, experts, k, *, score="softmax", renormalize=True, scale=1.0):

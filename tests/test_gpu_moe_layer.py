@@ -177,3 +177,32 @@ def test_dispatch_with_a_gradient_takes_bf16(dtype):
     X = torch.zeros(4, 8, dtype=dtype, device="cuda", requires_grad=True)
     with pytest.raises(TypeError, match="bf16"):
         dispatch(X, torch.zeros(4, 2, dtype=torch.int32, device="cuda"))
+
+
+def test_rows_of_no_choice_do_not_reach_gradients(monkeypatch):
+    # tokens with fewer experts than k, or none: rows behind the last expert's hold NaN on the way forward and back
+    from ragged_grouped_gemm_02_gb300 import moe_layer
+    X, logits, W13, W2 = _layer(T=90, E=5)
+    logits[::4, 1:] = float("-inf")
+    logits[::7] = float("-inf")
+    leaves = [t.requires_grad_() for t in (X, logits, W13, W2)]
+
+    def grads():
+        return torch.autograd.grad(moe_ffn(*leaves, 3).float().square().sum(), leaves)
+
+    want = grads()
+    dispatch_, backward_, passed = rgg.rgg_dispatch, rgg.rgg_combine_backward, []
+
+    def nan_dispatch(X, position):
+        return dispatch_(X, position, torch.full((position.numel(), X.shape[1]), float("nan"), dtype=X.dtype, device="cuda"))
+
+    def nan_backward(dout, Y, position, weights, dY=None, dweights=None):
+        passed.append(dY)
+        return backward_(dout, Y, position, weights, torch.full_like(Y, float("nan")), dweights)
+
+    monkeypatch.setattr(moe_layer, "rgg_dispatch", nan_dispatch)
+    monkeypatch.setattr(moe_layer, "rgg_combine_backward", nan_backward)
+    got = grads()
+    assert passed == [None]
+    assert all(torch.equal(a, b) and bool(torch.isfinite(a).all()) for a, b in zip(got, want))
+    assert rgg.rgg_query_status() == rgg.RGG_OK

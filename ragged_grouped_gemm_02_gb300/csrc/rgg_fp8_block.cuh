@@ -68,7 +68,9 @@ struct FpMaps {
 
 constexpr int kFpSums = 64;      // columns whose sums a thread holds
 constexpr int kFpMostSlots = 4;  // accumulators, at most
-constexpr int kFpFactors = 8;    // stages whose scales' products are held, at most
+constexpr int kFpRing = 8;       // stages whose scales' products are held
+constexpr int kFpGroup = kFpRing / 2;  // of which the epilogue gives so many back at a time
+constexpr int kFpTiles = 2 * kFpRing;  // tiles whose coordinates are held
 constexpr uint32_t kFpTile = 128u * 128u;  // bytes of 128 rows of a stage
 
 // The tiles: rows by columns of W.
@@ -103,11 +105,11 @@ __host__ __device__ inline FpSmem fp_smem(int stages, int E, uint32_t w_bytes, b
     FpSmem p;
     const uint32_t ex = 4u * static_cast<uint32_t>(E + 1);
     p.b_off = stages * kFpTile;
-    p.factor_off = p.b_off + stages * w_bytes;            // [kFpFactors][128][2] products of a row's and the columns' scales
-    p.top_off = p.factor_off + 1024u * kFpFactors;        // gate-up: [2][4][128] magnitudes
-    p.tile_off = p.top_off + (gate_up ? 4096u : 0u);      // [kFpFactors] tiles
-    p.bar_off = p.tile_off + 16u * kFpFactors;  // full[S], empty[S], acc_full[4], acc_empty[4], top[4], drain
-    p.misc_off = p.bar_off + 8u * (2u * stages + 2u * kFpMostSlots + 5u);
+    p.factor_off = p.b_off + stages * w_bytes;            // [kFpRing][128][2] products of a row's and the columns' scales
+    p.top_off = p.factor_off + 1024u * kFpRing;           // gate-up: [2][4][128] magnitudes
+    p.tile_off = p.top_off + (gate_up ? 4096u : 0u);      // [kFpTiles] tiles
+    p.bar_off = p.tile_off + 16u * kFpTiles;  // full[S], empty[S], acc_full[4], acc_empty[4], top[4], drain, read[2]
+    p.misc_off = p.bar_off + 8u * (2u * stages + 2u * kFpMostSlots + 7u);
     p.misc_off = (p.misc_off + 15u) & ~15u;
     p.off_off = p.misc_off + 16u;
     p.pre_off = p.off_off + ex;
@@ -130,9 +132,10 @@ __device__ __forceinline__ void mma_e4m3_if(uint32_t lead, uint32_t d_tmem, uint
         mma_single_if<true>(lead, d_tmem, a_desc, b_desc, idesc, accumulate);
 }
 
-// Arrives on `bar` (kPair: a cluster address) behind the warp's loads from TMEM.  Relaxed: nothing
-// that was written to memory is handed over, and a release at cluster scope waits for the
-// scales' loads as well (32,768 rows, 6144 x 4096, on pairs: 1 402 us with it).
+// Arrives on `bar` (kPair: a cluster address) behind the warp's loads from TMEM.  Relaxed: what it
+// gives back lies in TMEM alone, which tc_fence_before_sync orders; the scales' places in shared
+// memory have barriers of their own.  A release at cluster scope would wait for the warp's stores of
+// the last tile too (with loads of the scales ahead of it, 32,768 rows, 6144 x 4096, on pairs took 1 402 us).
 template <bool kPair>
 __device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
     if constexpr (kPair)
@@ -211,8 +214,8 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
     constexpr uint32_t kHalfBytes = kFpTile;       // single CTAs: 128 rows of W
     constexpr uint32_t kSlotCols = 128 * kHalves;  // an accumulator; all of TMEM's 512 columns are in use
     constexpr uint32_t kSlots = 512 / kSlotCols;
-    constexpr uint32_t kRing = 2 * kSlots;         // stages whose scales' products are held
-    static_assert(kRing <= kFpFactors && kRing >= kSlots + 2 && kRing <= 2 * kSlots + 1, "");
+    constexpr uint32_t kRing = kFpRing, kGroup = kFpGroup;
+    static_assert(kSlots <= kGroup, "the MMAs never wait for the scales' places");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
 
     const int warp = uniform_warp();
@@ -236,6 +239,9 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
     auto acce_bar = [&](int a) { return bars + 8u * (2 * S + kFpMostSlots + a); };
     auto top_bar = [&](int q) { return bars + 8u * (2 * S + 2 * kFpMostSlots + q); };
     const uint32_t drain_bar = bars + 8u * (2 * S + 2 * kFpMostSlots + 4);
+    auto read_bar = [&](uint32_t g) {  // the epilogue's warps have read the groups of that parity
+        return bars + 8u * (2 * S + 2 * kFpMostSlots + 5 + g);
+    };
     uint32_t* misc = reinterpret_cast<uint32_t*>(gbase + sp.misc_off);
     int32_t* s_off = reinterpret_cast<int32_t*>(gbase + sp.off_off);
     int32_t* s_pre = reinterpret_cast<int32_t*>(gbase + sp.pre_off);
@@ -263,6 +269,8 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
         }
         for (int q = 0; q < 4; ++q) mbar_init(top_bar(q), kParts);
         mbar_init(drain_bar, 1);
+        mbar_init(read_bar(0), 4 * kParts);
+        mbar_init(read_bar(1), 4 * kParts);
         misc[1] = 0u;
         fence_mbar_init();
     }
@@ -418,11 +426,10 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
         } else {
             // ------------------------------------------------------------ scales
             // Products of the scales of this CTA's rows (64 a warp) and of the columns, a stage at
-            // a time; the epilogue's wait for a stage is for these too.  Stage n takes the place of
-            // stage n - kRing.  Its sums were made before the epilogue gave back the accumulator of
-            // stage n - kRing + 1, and that before stage n - kRing + 1 + kSlots was multiplied:
-            // so this waits for that product.  (A phase on would need stage n's scales.)
-            constexpr uint32_t kBehind = kRing - 1 - kSlots;
+            // a time; the epilogue's wait for a stage is for these too.  Two waits: for kGroup places,
+            // which all of the epilogue's warps give back when they have read them; and for the end of
+            // the phase before, of the barrier that is arrived on.
+            // Neither holds up the MMAs, which are at most kSlots stages ahead of the epilogue.
             const int row0 = 64 * (warp - 2) + lane;
             float2* out = reinterpret_cast<float2*>(gbase + sp.factor_off) + row0;
             const int nblocks = static_cast<int>(fp_blocks(cols_w));
@@ -445,15 +452,16 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                         b0 = w0[kb + 1];
                         b1 = w1[kb + 1];
                     }
-                    if (n >= kBehind && !wait(accf_bar((n - kBehind) % kSlots), ((n - kBehind) / kSlots) & 1u)) {
+                    if ((n >= kRing && n % kGroup == 0 && !wait(read_bar(n / kGroup & 1u), (n / kRing - 1) & 1u)) ||
+                        (n >= kSlots && !wait(accf_bar(n % kSlots), (n / kSlots - 1) & 1u))) {
                         ok = false;
                         break;
                     }
                     out[(n % kRing) * 128] = f0;
                     out[(n % kRing) * 128 + 32] = f1;
-                    // the tile, for the epilogue (16 warps would each look it up).  No more than
-                    // 2 kSlots - 1 stages, and so tiles, ahead of one that it still writes.
-                    if (kb == 0 && warp == 2 && lane == 0) s_tile[tiles % kFpFactors] = make_int4(c.expert, c.row0, c.rows, c.col0);
+                    // the tile, for the epilogue (16 warps would each look it up); what its place held was
+                    // read kFpTiles stages ago or more, so before the groups that have been given back
+                    if (kb == 0 && warp == 2 && lane == 0) s_tile[tiles % kFpTiles] = make_int4(c.expert, c.row0, c.rows, c.col0);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(accf_bar(n % kSlots));
                 }
@@ -483,6 +491,9 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
 #pragma unroll 1
             for (int kb = 0; kb < KB; ++kb, ++n) {
                 const uint32_t slot = n % kSlots;
+                // The warp has read the places of the group before (__syncwarp below).  Here, and not beside the
+                // accumulator's arrival: a branch in that one's took 6 % (582 us on 128 x 256 tiles, 626 there).
+                if (n % kGroup == 0 && n > 0 && lane == 0) mbar_arrive(read_bar((n / kGroup - 1) & 1u));
                 if (!epi_wait(accf_bar(slot), (n / kSlots) & 1u)) {
                     ok = false;
                     break;
@@ -510,7 +521,7 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                 }
             }
             if (!ok) break;
-            const int4 tile = s_tile[tiles % kFpFactors];
+            const int4 tile = s_tile[tiles % kFpTiles];
             const TileCoord c = {tile.x, tile.y, tile.z, tile.w};
             const bool row_ok = r_local < c.rows;
             const int64_t row = static_cast<int64_t>(c.row0) + r_local;

@@ -687,8 +687,9 @@ rgg_status rgg_fp8_block_dequantize_weights(rgg_handle* h, const void* codes, co
  * times its two scales, the result rounded once to bf16: Y [M_tot, N].
  * rgg_grouped_gemm_swiglu_fp8_block is the gate-up projection: the weight has 2N
  * columns, gate first, and H = silu(g) * u leaves as activations of this form, codes
- * [M_tot, N] and scales [M_tot, N / 128], quantised from fp32 by the rule above; N
- * must be a multiple of 128 (fill other widths up with zero columns of gate and up).
+ * [M_tot, N] and scales [M_tot, N / 128], quantised from fp32 by the rule above,
+ * Inf and NaN as there; 448 / a is rounded before the multiplication, so that a code
+ * next to a tie may be either neighbour.  N must be a multiple of 128 (fill other widths up with zero columns of gate and up).
  *
  * Rows of no expert are never written.  Of `opt` they read bm (256: CTA pairs, 128:
  * single CTAs, 0: by the sizes), bn (the columns of W in a single CTA's tile: 256, or

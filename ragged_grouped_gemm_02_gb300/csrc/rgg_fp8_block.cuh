@@ -170,6 +170,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// The larger one; NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // z / (1 + exp(-z)) of both, each step to 2 units in the last place (the exponential: 2 + 1.2 |z|), without the handling
 // of subnormal numbers: 0 where the denominator passes 2^126.
 __device__ __forceinline__ uint64_t silu2(uint64_t z) {
@@ -552,13 +559,14 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
             } else {
                 // H, its largest magnitude over the 128 columns (all parts', through
                 // shared memory, two buffers by turns: a warp is in the next but one
-                // tile's only when all have left this one's), codes and scale
+                // tile's only when all have left this one's), codes and scale.  NaN stays in the
+                // largest, so that a block which holds one has a scale of NaN
                 constexpr int kH = kCols;
                 float top = kFpLeast;
 #pragma unroll
                 for (int i = 0; i < kH / 2; ++i) {
                     sums[i] = mul2(silu2(sums[i]), sums[kH / 2 + i]);
-                    top = fmaxf(top, fmaxf(fabsf(half_of(sums[i], 0)), fabsf(half_of(sums[i], 1))));
+                    top = max_nan(top, max_nan(fabsf(half_of(sums[i], 0)), fabsf(half_of(sums[i], 1))));
                 }
                 float* s_top = reinterpret_cast<float*>(gbase + sp.top_off) + (tiles & 1) * (128 * kParts);
                 s_top[part * 128 + 32 * q + lane] = top;
@@ -569,7 +577,7 @@ __device__ __forceinline__ void fp8_block_tiles(const FpMaps& maps, const FpArgs
                     break;
                 }
 #pragma unroll
-                for (int i = 0; i < kParts; ++i) top = fmaxf(top, s_top[i * 128 + 32 * q + lane]);
+                for (int i = 0; i < kParts; ++i) top = max_nan(top, s_top[i * 128 + 32 * q + lane]);
                 const uint64_t inv = twice(kFpMax / top);
                 uint32_t w[kH / 4];
 #pragma unroll

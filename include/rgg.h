@@ -692,8 +692,8 @@ rgg_status rgg_fp8_block_dequantize_weights(rgg_handle* h, const void* codes, co
  * next to a tie may be either neighbour.  N must be a multiple of 128 (fill other widths up with zero columns of gate and up).
  *
  * Rows of no expert are never written.  Of `opt` they read bm (256: CTA pairs, 128:
- * single CTAs, 0: by the sizes), bn (the columns of W in a single CTA's tile: 256, or
- * for the plain product 128; 0: by the sizes), stages, max_ctas (at least 2 for pairs),
+ * single CTAs, 0: by the sizes), bn (the columns of W in a tile: 256, or
+ * for the plain product on single CTAs 128; 0: by the sizes), stages, max_ctas (at least 2 for pairs),
  * timeout_ns and debug_flags.  The shape of the tiles does not change a result.  K a multiple of 16, N of 8; pointers 16-byte aligned (scales 4).
  * Other arguments, errors and the stream contract as for rgg_grouped_gemm.
  */

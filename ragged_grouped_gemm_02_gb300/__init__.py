@@ -1222,8 +1222,8 @@ def rgg_grouped_gemm_fp8_block(x_codes, x_scales, w_codes, w_scales, group_offse
     """Y_e = X_e . W_e for every expert with 8-bit operands and a scale per block of
     128, as ``rgg_fp8_block_quantize`` and ``rgg_fp8_block_quantize_weights`` leave
     them; Y: optional bf16 CUDA [M_tot, N].  bm: 256 (256 x 256 tiles on CTA
-    pairs), 128 (single CTAs, with bn 128 or 256 columns a tile) or 0, by the
-    sizes."""
+    pairs), 128 (single CTAs) or 0, by the sizes; bn: 256 or, on single CTAs,
+    128 columns a tile, or 0, by the sizes."""
     import torch
     M_tot, K, E, N, dev = _fp8_block_operands(x_codes, x_scales, w_codes, w_scales, group_offsets)
     if Y is None:

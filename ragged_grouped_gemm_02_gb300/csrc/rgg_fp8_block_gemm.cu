@@ -62,6 +62,7 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
     auto tile_n = [&](int shape) { return gate_up || shape == kFpNarrow ? 128 : 256; };
     auto tiles_n = [&](int shape) { return (N + tile_n(shape) - 1) / tile_n(shape); };
     const int want_bn = opt ? opt->bn : 0;
+    const bool narrow_ok = !gate_up && want_bn != 256;
     int shape;
     if (want_bm == 256) {
         shape = kFpPair;
@@ -72,7 +73,7 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
     } else if (avg <= 128) {
         // The weights' bytes bound the product, and more, smaller tiles keep all SMs reading (32 experts x 16 rows, 6144 x
         // 4096: 127 us; wide tiles 131, pairs 150).
-        shape = gate_up ? kFpWide : kFpNarrow;
+        shape = narrow_ok ? kFpNarrow : kFpWide;
     } else {
         // The shape with the shorter waves.  A tile costs a fixed part and a part per stage, in us, by least squares over
         // 112 products (2 to 32 experts of 160 to 4,096 rows on average, K = 1024 and 6144); an SM takes as long for half a
@@ -90,7 +91,7 @@ static rgg_status fp8_block_call(rgg_handle* h, const void* x_codes, const float
         double best = 1e300;
         shape = kFpWide;
         for (int s2 = kFpPair; s2 <= kFpNarrow; ++s2) {
-            if ((s2 == kFpPair && (cap < 2 || want_bm == 128)) || (s2 == kFpNarrow && gate_up)) continue;
+            if ((s2 == kFpPair && (cap < 2 || want_bm == 128)) || (s2 == kFpNarrow && !narrow_ok)) continue;
             const int units = s2 == kFpPair ? cap / 2 : cap;
             const double tiles = E * tiles_m(s2 == kFpPair ? 256 : 128) * tiles_n(s2);
             const double cost = start[s2] + std::max(1.0, std::ceil(tiles / units)) * (fixed[s2] + stage[s2] * kb);

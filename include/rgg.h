@@ -685,6 +685,9 @@ rgg_status rgg_fp8_block_dequantize_weights(rgg_handle* h, const void* codes, co
  *     Y[i, n] = sum over k of x[i, k] * w[e, n, k]      for every row i of expert e,
  * the products of a block of 128 of K summed on the tensor core, the blocks in fp32, each
  * times its two scales, the result rounded once to bf16: Y [M_tot, N].
+ * A block's two scales are multiplied first, in fp32, so the formula holds where their
+ * product is a normal number: from 2^-126 (below, it loses bits or is 0) to below 2^128
+ * (from there on it is Inf, which times a sum of 0 is NaN).
  * rgg_grouped_gemm_swiglu_fp8_block is the gate-up projection: the weight has 2N
  * columns, gate first, and H = silu(g) * u leaves as activations of this form, codes
  * [M_tot, N] and scales [M_tot, N / 128], quantised from fp32 by the rule above,

@@ -17,8 +17,9 @@ namespace rgg {
 
 constexpr int kFpBlock = 128;        // values of K, and columns of a weight, that share a scale
 constexpr float kFpMax = 448.0f;     // E4M3's largest value
-// The least largest magnitude a block is scaled by, 2^-100: 448 / a and products
-// of two scales stay inside fp32's normal range.
+// The least largest magnitude a block is scaled by, 2^-100: 448 / a stays inside
+// fp32's normal range.  (Its scale is 2^-108.8.  The product multiplies a row's scale by
+// a weight's first, in fp32: two of the least give 0, two above 2^64 Inf.)
 constexpr float kFpLeast = 7.888609052210118e-31f;
 
 __host__ __device__ inline int64_t fp_blocks(int64_t n) { return (n + kFpBlock - 1) / kFpBlock; }

@@ -376,11 +376,12 @@ __global__ void __launch_bounds__(kRouteThreads)
         const RouteChoice<T, kLanes> c(logits + t * E, experts, dweights, in, t, lane, E, k, scale, status);
         float d;
         if (sigmoid) {
-            const float s = c.chosen() ? sigmoid_f32(c.l) : 0.0f;
-            d = c.g * s * (1.0f - s);
+            // 1 - s from the logit: from s, which is 1 in fp32 above a logit of 17, it would have few bits or none
+            const float s = c.chosen() ? sigmoid_f32(c.l) : 0.0f, rest = c.chosen() ? sigmoid_f32(-c.l) : 0.0f;
+            d = c.g * s * rest;
             if (renormalize) {
                 const float total = group_sum<kLanes>(s) + kRouteEps;
-                d = (c.g - group_sum<kLanes>(c.g * (s / total))) / total * s * (1.0f - s);
+                d = (c.g - group_sum<kLanes>(c.g * (s / total))) / total * s * rest;
             }
         } else {
             float top = group_max<kLanes>(c.chosen() ? c.l : -INFINITY);

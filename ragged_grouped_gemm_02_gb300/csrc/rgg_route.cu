@@ -11,7 +11,7 @@
 //     softmax, divided    dl_i = scale w_i (g_i - sum g_j w_j),  i in C, else 0
 //     sigmoid             dl_i = scale g_i s_i (1 - s_i),        i in C, else 0
 //     sigmoid, divided    dl_i = scale (g_i - sum g_j w_j) / (sum s_j + 1e-20) s_i (1 - s_i)
-// with w before the scale.
+// with w before the scale.  The differences are formed so that they keep their bits where a weight is nearly 1.
 //
 // A warp takes a token, each lane up to 8 logits (kWide: neighbouring ones, read by one or
 // two 16-byte loads; else l, l + 32, ...; above 256 experts more).  The order is by value,
@@ -374,21 +374,26 @@ __global__ void __launch_bounds__(kRouteThreads)
             }
         }
         const RouteChoice<T, kLanes> c(logits + t * E, experts, dweights, in, t, lane, E, k, scale, status);
-        float d;
-        if (sigmoid) {
-            // 1 - s from the logit: from s, which is 1 in fp32 above a logit of 17, it would have few bits or none
-            const float s = c.chosen() ? sigmoid_f32(c.l) : 0.0f, rest = c.chosen() ? sigmoid_f32(-c.l) : 0.0f;
-            d = c.g * s * rest;
-            if (renormalize) {
-                const float total = group_sum<kLanes>(s) + kRouteEps;
-                d = (c.g - group_sum<kLanes>(c.g * (s / total))) / total * s * rest;
+        // 1 - s from the logit: from s, which is 1 in fp32 above a logit of 17, it would have few bits or none
+        const float s = sigmoid && c.chosen() ? sigmoid_f32(c.l) : 0.0f, rest = sigmoid && c.chosen() ? sigmoid_f32(-c.l) : 0.0f;
+        float d = c.g * s * rest;
+        if (renormalize) {
+            // g_i - sum g_j w_j as differences from the gradient g0 of the largest weight, (g_i - q g0) - sum w_j (g_j - g0)
+            // with q = sum w_j: beside a weight of nearly 1 its own gradient would leave nothing of the others'
+            const float top = group_max<kLanes>(c.chosen() ? c.l : -INFINITY);
+            const int base = lane & ~(kLanes - 1);
+            const uint32_t tops = __ballot_sync(0xffffffffu, c.chosen() && c.l == top) & (0xffffffffu >> (32 - kLanes) << base);
+            const int largest = tops ? __ffs(tops) - 1 : base;
+            const float g0 = __shfl_sync(0xffffffffu, c.g, largest);
+            if (sigmoid) {
+                const float sum = group_sum<kLanes>(s), total = sum + kRouteEps;
+                const float own = lane == largest ? g0 * (kRouteEps / total) : c.g - g0 * (sum / total);
+                d = (own - group_sum<kLanes>((c.g - g0) * (s / total))) / total * s * rest;
+            } else {
+                float w = c.chosen() ? expf(c.l - (top == -INFINITY ? 0.0f : top)) : 0.0f;
+                w = w / not_zero(group_sum<kLanes>(w));
+                d = w * ((c.g - g0) - group_sum<kLanes>((c.g - g0) * w));
             }
-        } else {
-            float top = group_max<kLanes>(c.chosen() ? c.l : -INFINITY);
-            if (top == -INFINITY) top = 0.0f;
-            float w = c.chosen() ? expf(c.l - top) : 0.0f;
-            w = w / not_zero(group_sum<kLanes>(w));
-            d = w * (c.g - group_sum<kLanes>(c.g * w));
         }
         d = c.joined(c.chosen() ? d : 0.0f);
         __syncwarp();  // the zeros are written before the choices' values

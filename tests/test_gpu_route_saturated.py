@@ -13,6 +13,7 @@ from ragged_grouped_gemm_02_gb300 import _build
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
+EPS = 1e-20
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -31,6 +32,12 @@ def _check(got, want, limit):
     assert bool(((got - want).abs() <= limit + 2.0 ** -126).all()), float(worst)
 
 
+def _choices(z, k, shuffled, gen):
+    """The k largest of each row, in their order or in another."""
+    experts = torch.topk(z, k, dim=1).indices
+    return experts.gather(1, torch.rand(experts.shape, generator=gen).argsort(1)) if shuffled else experts
+
+
 def test_sigmoid():
     gen = torch.Generator().manual_seed(0)
     z = torch.cat([torch.linspace(-60, 60, 240), 8 + 32 * torch.rand(240, generator=gen)]).view(60, 8)
@@ -39,3 +46,38 @@ def test_sigmoid():
     want = torch.zeros(60, 8, dtype=torch.float64).scatter(1, experts, scale * g.double() * torch.sigmoid(l) * torch.sigmoid(-l))
     # both sigmoids 6 u, four products
     _check(_backward(z, experts, g, "sigmoid", False, scale), want, want.abs() * 16 * U)
+
+
+def _pairs(w, g):
+    """For each choice i: sum over j of w_j (g_i - g_j), and of the magnitudes."""
+    d = g.unsqueeze(2) - g.unsqueeze(1)
+    return (w.unsqueeze(1) * d).sum(2), (w.unsqueeze(1) * d.abs()).sum(2)
+
+
+@pytest.mark.parametrize("shuffled", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [1, 2, 3, 8, 16, 20])
+def test_renormalized(k, score, shuffled):
+    gen = torch.Generator().manual_seed(k)
+    T, E, scale = 41, 24, 1.5
+    z = torch.randn(T, E, generator=gen)
+    z[:, 5] += torch.linspace(0, 30, T)  # one expert takes more and more of the weight
+    z = z[:, torch.randperm(E, generator=gen)] if score == "softmax" else z - 12
+    experts, g = _choices(z, k, shuffled, gen), torch.randn(T, k, generator=gen)
+    l = z.double().gather(1, experts)
+    if score == "softmax":
+        w, rest, factor = torch.softmax(l, 1), 0.0, torch.softmax(l, 1)
+    else:
+        s = torch.sigmoid(l)
+        total = s.sum(1, keepdim=True) + EPS
+        w, rest, factor = s / total, EPS / total, s * torch.sigmoid(-l) / total
+    diff, size = _pairs(w, g.double())
+    want = scale * factor * (diff + rest * g.double())
+    # with r the largest weight's choice, (g_i - g_r) - sum w_j (g_j - g_r): |g_i - g_r| <= k size_i as w_r >= 1 / k, so the
+    # terms sum to at most (2 k + 1) size_i; each is off by the weights' 24 u, their arguments' and the sums' k u
+    spread = l.amax(1, keepdim=True) - l.amin(1, keepdim=True)
+    units = (24 + 2 * k + 2 * spread) * U
+    limit = scale * factor * ((2 * k + 1) * size + 2 * rest * g.double().abs()) * units
+    got = _backward(z, experts, g, score, True, scale)
+    _check(got.gather(1, experts), want, limit)
+    assert bool((got.scatter(1, experts, 0.0) == 0).all())

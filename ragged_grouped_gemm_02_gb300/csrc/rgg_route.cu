@@ -337,12 +337,24 @@ __global__ void __launch_bounds__(kRouteThreads)
             total += x[i];
         }
         const float inverse = 1.0f / not_zero(warp_sum(total));
-        const float s = c.chosen() ? expf(c.l - top) * inverse : 0.0f;
+        const float s = c.chosen() ? expf(c.l - top) * inverse : 0.0f, g = c.joined(c.g);
         const float sum = warp_sum(c.g * s);
+        float d = s * (g - sum);
+        const uint32_t tops = inverse > 0.5f ? __ballot_sync(0xffffffffu, c.chosen() && c.l == top) : 0u;
+        if (tops) {
+            // A choice t with more than half of the weight, whose gradient g - sum would leave few bits: as differences
+            // from it, (g - g_t) - (sum over the other choices of g s - g_t (1 - s_t)), 1 - s_t from the others.
+            const int32_t t = __shfl_sync(0xffffffffu, c.expert, __ffs(tops) - 1);
+            const float g_t = __shfl_sync(0xffffffffu, g, __ffs(tops) - 1);
+            float others = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) others += Row::expert(i, lane) == t ? 0.0f : x[i];
+            const float rest = warp_sum(c.expert == t ? 0.0f : c.g * s);
+            d = s * ((g - g_t) - (rest - g_t * (warp_sum(others) * inverse)));
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) x[i] *= -sum * inverse;
         Row::store(out, E, lane, x);
-        const float d = s * (c.joined(c.g) - sum);
         __syncwarp();  // the row's other values are written before the choices'
         if (c.chosen()) out[c.expert] = RouteType<T>::from_float(d);
     }

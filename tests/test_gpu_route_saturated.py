@@ -81,3 +81,25 @@ def test_renormalized(k, score, shuffled):
     got = _backward(z, experts, g, score, True, scale)
     _check(got.gather(1, experts), want, limit)
     assert bool((got.scatter(1, experts, 0.0) == 0).all())
+
+
+@pytest.mark.parametrize("E", [6, 40, 128, 200, 256, 300])
+def test_softmax_over_all(E):
+    gen = torch.Generator().manual_seed(E)
+    T, k, scale = 31, 4, 2.5
+    z = torch.randn(T, E, generator=gen)
+    z[:, 3] += torch.linspace(8, 30, T)  # more than half of the weight in each row
+    experts, g = _choices(z, k, True, gen), torch.randn(T, k, generator=gen).double()
+    s = torch.softmax(z.double(), 1)
+    all_g = torch.zeros(T, E, dtype=torch.float64).scatter(1, experts, g)
+    want = scale * s * _pairs(s, all_g)[0]
+    assert bool((s[:, 3] > 0.5).all()) and bool((experts == 3).any(1).all())
+    # with r the largest: (g_i - g_r) - (sum over the other choices of s_j g_j - g_r sum over j != r of s_j)
+    g_r, others = all_g[:, 3:4], s.clone()
+    others[:, 3] = 0.0
+    terms = (all_g - g_r).abs() + (others * (all_g.abs() + g_r.abs())).sum(1, keepdim=True)
+    plain = (s * all_g.abs()).sum(1, keepdim=True).expand(T, E)  # experts of no choice
+    chosen = torch.zeros(T, E, dtype=torch.bool).scatter(1, experts, True)
+    spread = z.double().amax(1, keepdim=True) - z.double().amin(1, keepdim=True)
+    limit = scale * s * torch.where(chosen, terms, plain) * (24 + 2 * E + 2 * spread) * U
+    _check(_backward(z, experts, g.float(), "softmax", False, scale), want, limit)

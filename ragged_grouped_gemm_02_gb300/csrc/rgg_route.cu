@@ -386,21 +386,21 @@ __global__ void __launch_bounds__(kRouteThreads)
             }
         }
         const RouteChoice<T, kLanes> c(logits + t * E, experts, dweights, in, t, lane, E, k, scale, status);
-        // 1 - s from the logit: from s, which is 1 in fp32 above a logit of 17, it would have few bits or none
-        const float s = sigmoid && c.chosen() ? sigmoid_f32(c.l) : 0.0f, rest = sigmoid && c.chosen() ? sigmoid_f32(-c.l) : 0.0f;
+        // s and 1 - s from one exponential: from s, which is 1 in fp32 above a logit of 17, 1 - s would have few bits or none
+        const float e = expf(-fabsf(c.l)), r = sigmoid && c.chosen() ? 1.0f / (1.0f + e) : 0.0f;
+        const float s = c.l < 0.0f ? e * r : r, rest = c.l < 0.0f ? r : e * r;
         float d = c.g * s * rest;
         if (renormalize) {
-            // g_i - sum g_j w_j as differences from the gradient g0 of the largest weight, (g_i - q g0) - sum w_j (g_j - g0)
-            // with q = sum w_j: beside a weight of nearly 1 its own gradient would leave nothing of the others'
+            // g_i - sum g_j w_j as differences from the gradient g0 of the largest weight, (g_i - g0) - sum w_j (g_j - g0),
+            // + g0 (1 - sum w_j): beside a weight of nearly 1 its own gradient would leave nothing of the others'
             const float top = group_max<kLanes>(c.chosen() ? c.l : -INFINITY);
             const int base = lane & ~(kLanes - 1);
             const uint32_t tops = __ballot_sync(0xffffffffu, c.chosen() && c.l == top) & (0xffffffffu >> (32 - kLanes) << base);
             const int largest = tops ? __ffs(tops) - 1 : base;
             const float g0 = __shfl_sync(0xffffffffu, c.g, largest);
             if (sigmoid) {
-                const float sum = group_sum<kLanes>(s), total = sum + kRouteEps;
-                const float own = lane == largest ? g0 * (kRouteEps / total) : c.g - g0 * (sum / total);
-                d = (own - group_sum<kLanes>((c.g - g0) * (s / total))) / total * s * rest;
+                const float inverse = 1.0f / (group_sum<kLanes>(s) + kRouteEps), w = s * inverse, diff = c.g - g0;
+                d = (diff - group_sum<kLanes>(diff * w) + g0 * (kRouteEps * inverse)) * w * rest;
             } else {
                 float w = c.chosen() ? expf(c.l - (top == -INFINITY ? 0.0f : top)) : 0.0f;
                 w = w / not_zero(group_sum<kLanes>(w));

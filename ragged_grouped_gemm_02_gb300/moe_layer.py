@@ -98,7 +98,8 @@ class _Combine(torch.autograd.Function):
         Y, position, weights = ctx.saved_tensors
         dY = False
         if ctx.needs_input_grad[0]:
-            dY = torch.zeros_like(Y) if ctx.whole else None  # rows of no choice: zero, or unspecified
+            # rows of no choice: zero, or unspecified where nobody looks at them (anomaly mode looks for NaN)
+            dY = torch.zeros_like(Y) if ctx.whole or torch.is_anomaly_enabled() else None
         dY, dweights = rgg_combine_backward(dout.contiguous(), Y, position, weights, dY,
                                             None if ctx.needs_input_grad[2] else False)
         return dY, None, dweights, None

@@ -107,6 +107,8 @@ class _Combine(torch.autograd.Function):
 
 def combine(Y, position, weights):
     """``rgg_combine`` with its gradients by Y (zero for rows of no choice) and the weights."""
+    if not isinstance(weights, torch.Tensor):
+        raise TypeError("weights must be a tensor [T, k] (rgg_combine takes None, for sums without weights)")
     return _Combine.apply(Y, position, weights, True)
 
 

@@ -13,6 +13,7 @@ report RGG_ERR_DEVICE_BOUNDS instead (csrc/rgg_checks.cuh).
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -46,6 +47,25 @@ def _inputs_mtime() -> float:
     return max(os.path.getmtime(p) for p in names)
 
 
+# The source of the kernels whose warps share out the block's registers.
+SHARED_OUT = "rgg_fp8_block_gemm.cu"
+
+
+def _check_registers(ptxas_log: str) -> None:
+    """Raises if a kernel of SHARED_OUT did not compile to the registers that its warps share out.  (Calls would be
+    refused: with fewer, the warps that take more would wait for ever.)"""
+    with open(os.path.join(CSRC, "rgg_fp8_block.cuh")) as f:
+        narrow, others = re.search(r"fp_regs_launch\(int shape\) { return shape == kFpNarrow \? (\d+) : (\d+); }", f.read()).groups()
+    used = re.findall(r"Compiling entry function '(\w*grouped_fp8_block\w*)'.*?Used (\d+) registers", ptxas_log, re.S)
+    if not used:
+        raise RuntimeError("ptxas printed no registers for the kernels of %s" % SHARED_OUT)
+    for name, registers in used:
+        want = narrow if "grouped_fp8_block_kernelILi2E" in name else others
+        if registers != want:
+            raise RuntimeError("%s compiled to %s registers a thread, and its warps share out %s: plan fp_regs_* in "
+                               "rgg_fp8_block.cuh for this compiler" % (name, registers, want))
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile and link librgg.so and librgg_debug.so if any source is newer
     than them; return the path of librgg.so."""
@@ -67,11 +87,16 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     def compile_one(job) -> str:
         _, src, out_dir, extra = job
         obj = os.path.join(out_dir, os.path.splitext(src)[0] + ".o")
+        shared_out = src == SHARED_OUT
+        if shared_out and not ptxas_verbose:
+            extra = extra + ["-Xptxas", "-v"]
         cmd = [nvcc] + common + extra + ["-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("nvcc failed for %s:\n%s\n%s" % (src, " ".join(cmd), r.stderr))
-        if verbose or ptxas_verbose:
+        if shared_out:
+            _check_registers(r.stdout + r.stderr)
+        if ptxas_verbose or (verbose and not shared_out):
             sys.stderr.write(r.stderr)
         return obj
 

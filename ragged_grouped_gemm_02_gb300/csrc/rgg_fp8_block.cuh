@@ -25,9 +25,9 @@
 // registers than an even share, so the first four warps give up theirs.  A stage holds 128
 // bytes a row, one swizzle row, K-major on both sides.
 //
-// Measured on a GB300, a few calls after a pause: 32 experts x 1,024 rows, 6144 x 4096 556 to 564 us
-// on pairs (2 967 TFLOP/s), 572 on 128 x 256, 675 on 128 x 128; 16 rows per expert 123 us (6.6 TB/s); gate-up
-// 64 experts x 256 rows, 1024 x 2 * 1408 56 us.  What bounds many rows are the sums, 128 x 256 multiplications
+// Measured on a GB300, a few calls after a pause: 32 experts x 1,024 rows, 6144 x 4096 551 to 570 us
+// on pairs (2 994 TFLOP/s at best), 565 to 583 on 128 x 256, 671 to 684 on 128 x 128; 16 rows per expert 124 us
+// (6.6 TB/s); gate-up 64 experts x 256 rows, 1024 x 2 * 1408 57 us.  What bounds many rows are the sums, 128 x 256 multiplications
 // and additions a CTA and stage: with the epilogue waiting and answering but adding nothing a pair's
 // stage took 570 cycles of 730 (the MMAs alone 512 at the nominal rate), without the multiplications 580,
 // without half of the loads from TMEM 730.  So its other instructions count: the tile comes from
@@ -35,7 +35,7 @@
 // an instruction (621 us for 591), the next stage's loads issued before the last sums of one (no gain, with
 // 8 warps or 16), halves of the columns multiplied and handed over one by one (964), waits
 // that poll (601 to 647), sums that a stage of its own begins instead of zeros (620 for 572: moves).
-// In long runs the product is at the power cap (1.6 GHz; 700 us of uneven experts).
+// In long runs the product is at the power cap (1.6 GHz; 735 us of uneven experts).
 #pragma once
 
 #include "rgg_fp8_block.h"

@@ -22,7 +22,10 @@
 // the lanes' first, and its lane moves on to its next.  Bound by the instructions that
 // takes (83 % of the issue slots): 32,768 tokens x 256 experts, k = 8, bf16 (17 MB) 14.5 us, fp32
 // 21; searching all logits of a lane k times took 24 and 30.  Tokens in turn on fewer blocks, the
-// next one's logits on their way, were slower (16.4).
+// next one's logits on their way, were slower (16.4).  Above 256 experts a lane keeps its logits unsorted and
+// searches them all again after each choice of its own; above 1,024 they no longer fit its registers
+// (4,096 x 4,096, softmax over all, 63 us of 10; its gradient 33).  The gradient of 32,768 x 256 bf16, k = 8: 6.2
+// to 6.6 us where the choices alone have one, 10.9 by softmax over all.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -65,7 +68,7 @@ struct RouteType<__nv_bfloat16> {
     static __device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
 };
 template <>
-struct RouteType<__half> {  // 10 bits of mantissa do not fit beside an expert's number: as fp32
+struct RouteType<__half> {  // as fp32 (its 19 bits and an expert's 12 would fit a 32-bit key of their own: not built)
     using Key = uint64_t;
     static __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
     static __device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
@@ -450,6 +453,9 @@ static cudaError_t launch_route_for(const RouteCall& c) {
                               static_cast<const T*>(c.logits), static_cast<const int32_t*>(c.experts), c.dweights, c.T,
                               c.E, c.k, c.flags, c.scale, wide, static_cast<T*>(c.dlogits), c.status);
     }
+    // Wide loads: lanes of whole 16-byte blocks, E = 32 V, among the V that a network sorts and that are whole blocks of
+    // the type (bf16 8, fp32 4 and 8).  At 160, 192 or 224 experts a lane's part is none; above 256 the choices take the
+    // time, not the loads.
     if (aligned && c.E == 256) return launch_route<T, 8, true>(c);
     if constexpr (kPer == 4) {
         if (aligned && c.E == 128) return launch_route<T, 4, true>(c);

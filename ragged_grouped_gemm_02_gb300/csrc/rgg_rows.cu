@@ -5,16 +5,19 @@
 //     combine's gradient   dY[position[t, j]] = w[t, j] * dout[t]
 //                          dw[t, j] = sum over columns of dout[t] * Y[position[t, j]]
 //
-// All of them go by token, so a token's row is read (or written) once however many
-// experts it went to, and sums over its choices are made in registers, in the order
-// of the choices: no atomics, equal calls give equal bits.  Choices without a row
+// Dispatch and combine go by token: a token's row comes from memory (or goes there)
+// once however many experts it went to, and sums over its choices are made in registers, in
+// the order of the choices.  Combine's gradient goes by choice; the choices of a token are
+// neighbours, so that dout's row comes from memory once and from cache k - 1 times, as X's does in
+// dispatch where rows are not whole 16 bytes.  No atomics, equal calls give equal bits.  Choices without a row
 // (position -1) add nothing; rows of no choice are left alone.  Bound by memory.
 //
 // Rows move in blocks of 16 bytes, aligned where they are written.  Where rows are not
 // whole 16 bytes (an odd width), a block that is read starts anywhere: it is put together
 // from an aligned one and the next lane's, by a funnel shift that is the same for a whole
 // row (so 32 lanes give 31 blocks); the first and last blocks of a written row are stored
-// element by element.
+// element by element.  A row that is read next to a tensor's end, where the blocks around it may
+// be outside, is read byte by byte over its whole length.
 //
 // Measured: 8,192 tokens x 4, 6144 columns (503 MB) dispatch 75 us, combine 81, its gradient (906 MB)
 // 135; 8,192 x 6 of 2688 columns 47, 53 and 93, of 2693 columns 57, 83 and 123, where

@@ -5,8 +5,9 @@ tokens sorted by expert, the expert layer, and the weighted sum back.
 
 ``moe_ffn`` has gradients by the tokens, the logits and the experts' weights;
 ``moe_ffn_fp8`` is the serving form with 8-bit experts.  The logits are the caller's
-(a product of the tokens with the router's weight, say), so that biases and masks
-(-inf) are too.
+(a product of the tokens with the router's weight, say), so that masks (-inf) and biases
+are too.  Choices and weights come from the same logits: a bias that is to move the
+choices alone has no place here.
 """
 from __future__ import annotations
 
